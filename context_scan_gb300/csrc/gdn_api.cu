@@ -480,6 +480,11 @@ gdn_status check_bwd(const gdn_problem* p, int nseg) {
 
 }  // namespace
 
+namespace gdn {
+gdn_status current_device_status() { return check_device(); }
+int current_sm_count() { return sm_count(); }
+}  // namespace gdn
+
 extern "C" {
 
 size_t gdn_workspace_bytes(const gdn_problem* p, int nseg) {

@@ -40,6 +40,16 @@ struct DeviceError {
     unsigned detail;  // which wait gave up (kernel-specific tag)
 };
 
+// Workspaces of the operators outside the chunked path: the device error word, at kWsVerdict a word that
+// a call's first kernel leaves for its next one, then from kWsHeader on what the operator keeps,
+// in regions of 256 bytes.
+constexpr size_t kWsHeader = 256, kWsVerdict = 128;
+inline size_t ws_round(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// Of the current device (gdn_api.cu): GDN_OK on an sm_103 GPU; its SM count (0: unknown).
+gdn_status current_device_status();
+int current_sm_count();
+
 // One launch of the chain kernels: every (b, h, segment) is an independent "chain" that
 // walks its segment's chunks in order, carrying the state on chip.
 struct ChainParams {

@@ -23,7 +23,9 @@ EXPORTED = ("gdn_workspace_bytes", "gdn_segmented_pieces", "gdn_segmented_plan",
             "gdn_segmented_fwd_timed", "gdn_segmented_fwd_noalloc",
             "gdn_varlen_workspace_bytes", "gdn_varlen_fwd", "gdn_varlen_fwd_timed",
             "gdn_state_grad_summary", "gdn_state_grad_scan", "gdn_chunk_bwd_workspace_bytes",
-            "gdn_chunk_bwd", "gdn_chunk_bwd_timed", "gdn_status_string", "gdn_check_device_error", "gdn_selftest_wait_timeout")
+            "gdn_chunk_bwd", "gdn_chunk_bwd_timed",
+            "gdn_recurrent_workspace_bytes", "gdn_recurrent_fwd",
+            "gdn_status_string", "gdn_check_device_error", "gdn_selftest_wait_timeout")
 
 
 class GdnError(RuntimeError):
@@ -78,6 +80,10 @@ def lib():
         L.gdn_chunk_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_chunk_bwd.argtypes = [pp, ctypes.c_int] + [_P] * 15 + [ctypes.c_size_t, _P]
         L.gdn_chunk_bwd_timed.argtypes = L.gdn_chunk_bwd.argtypes + [_P]
+        L.gdn_recurrent_workspace_bytes.argtypes = [ctypes.c_int]
+        L.gdn_recurrent_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_recurrent_fwd.argtypes = ([pp, ctypes.c_int, ctypes.c_int] + [_P] * 7 + [ctypes.c_int] +
+                                        [_P] * 2 + [ctypes.c_int] + [_P] * 2 + [ctypes.c_size_t, _P])
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_check_device_error.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_uint)]
@@ -86,7 +92,7 @@ def lib():
                    "gdn_segmented_fwd", "gdn_segmented_fwd_timed", "gdn_segmented_fwd_noalloc",
                    "gdn_varlen_fwd", "gdn_varlen_fwd_timed", "gdn_check_device_error",
                    "gdn_selftest_wait_timeout", "gdn_state_grad_summary", "gdn_state_grad_scan",
-                   "gdn_chunk_bwd", "gdn_chunk_bwd_timed"):
+                   "gdn_chunk_bwd", "gdn_chunk_bwd_timed", "gdn_recurrent_fwd"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -326,6 +332,71 @@ def gdn_chunk_bwd_timed(q, k, v, g, beta, h0, dO, dht, dq, dk, dv, dg, dbeta, dh
                                      _ptr(dh0), _ptr(workspace),
                                      workspace.numel() if workspace is not None else 0,
                                      _stream(stream), arr), "gdn_chunk_bwd_timed")
+
+
+def _on_device(**tensors):
+    """Raises ValueError unless every tensor (or None) lies contiguous on the current CUDA device:
+    the library takes plain pointers and launches on that device."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+
+
+def _is(name, t, dtype, shape):
+    """Raises ValueError unless t (or None) has this dtype and shape."""
+    if t is not None and (t.dtype != dtype or t.shape != shape):
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, not {dtype} {tuple(shape)}")
+
+
+def alloc_recurrent_workspace(num_slots: int, device="cuda"):
+    """A zeroed workspace tensor for gdn_recurrent_fwd on a cache of num_slots slots."""
+    import torch
+    n = int(lib().gdn_recurrent_workspace_bytes(num_slots))
+    if n == 0:
+        raise GdnError(1, "gdn_recurrent_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def gdn_recurrent_fwd(q, k, v, g, beta, state, slots_in, slots_out, o, workspace, cu_seqlens=None,
+                      per_token=False, decay_first=False, stream=None):
+    """The rule token by token over a state cache [num_slots, H, K, V] fp32: q, k [B, T, Hqk, K],
+    v, o [B, T, H, V], g [B, T, H] (or [B, T, H, K]), beta [B, T, H]. Without cu_seqlens B
+    sequences of T tokens; with it (int32, on the GPU) B == 1 and len(cu_seqlens) - 1 packed
+    sequences. slots_in, slots_out: int32 GPU tensors (or None), one entry a sequence; with
+    per_token slots_out has one entry a token. Negative entries: a zero state, not written."""
+    import torch
+    B, T, H, V = v.shape
+    Hqk, K = k.shape[2], k.shape[3]
+    nseq = B if cu_seqlens is None else int(cu_seqlens.numel()) - 1
+    _on_device(q=q, k=k, v=v, g=g, beta=beta, state=state, slots_in=slots_in, slots_out=slots_out,
+               o=o, workspace=workspace, cu_seqlens=cu_seqlens)
+    gate_k = g.dim() == 4
+    _is("q", q, k.dtype, (B, T, Hqk, K))
+    _is("k", k, k.dtype, (B, T, Hqk, K))
+    _is("v", v, k.dtype, v.shape)
+    _is("g", g, k.dtype, (B, T, H, K) if gate_k else (B, T, H))
+    _is("beta", beta, k.dtype, (B, T, H))
+    _is("o", o, o.dtype, v.shape)
+    slots = 0
+    if state is not None:
+        slots = state.shape[0]
+        _is("state", state, torch.float32, (slots, H, K, V))
+    _is("slots_in", slots_in, torch.int32, (nseq,))
+    _is("slots_out", slots_out, torch.int32, (B * T if per_token else nseq,))
+    if cu_seqlens is not None:
+        _is("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,))
+    prob = Problem(B, T, H, K, V, 64, _dtype_code(k), _dtype_code(o), int(decay_first), int(gate_k))
+    _check(lib().gdn_recurrent_fwd(ctypes.byref(prob), Hqk, nseq, _ptr(cu_seqlens), _ptr(q), _ptr(k),
+                                   _ptr(v), _ptr(g), _ptr(beta), _ptr(state), slots, _ptr(slots_in),
+                                   _ptr(slots_out), int(per_token), _ptr(o), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)),
+           "gdn_recurrent_fwd")
 
 
 def gdn_selftest_wait_timeout(workspace, limit_cycles, stream=None):

@@ -379,6 +379,48 @@ GDN_API gdn_status gdn_varlen_fwd_timed(const gdn_problem* p, int nseq, const in
                                         size_t workspace_bytes, void* stream,
                                         void* const* stage_events);
 
+/* ---------------------------------------------------------------------------------------
+ * The recurrent form over a state cache (decode, draft tokens, the ends of prompts)
+ * ---------------------------------------------------------------------------------------
+ * A state cache is an array state [num_slots, H, K, V] fp32: slot (page) i holds one sequence's
+ * state. The rule of RFC section 2.1 runs token by token from the state in one slot, in fp32
+ * throughout, for any number of tokens from none on -- one new token of every sequence of a decode
+ * batch, a few draft tokens, a prompt's last tokens. (Long prompts: gdn_varlen_fwd, whose h_final
+ * rows are pages, is faster from about a chunk of tokens on when the shapes allow it.) */
+
+/* Workspace bytes for gdn_recurrent_fwd on a cache of num_slots slots: the header and one int per
+ * slot. Returns 0 for num_slots < 0. */
+GDN_API size_t gdn_recurrent_workspace_bytes(int num_slots);
+
+/* nseq sequences, each from its slot of the cache.
+ *   Tokens: with cu_seqlens NULL, p->B == nseq sequences of p->T tokens each; else p->B == 1 and
+ *   sequence s holds tokens cu_seqlens[s] .. cu_seqlens[s+1]-1 of p->T packed ones ([nseq + 1]
+ *   int32 DEVICE array: 0 first, T last, non-decreasing). p->chunk is not read.
+ *   Heads: q, k [B,T,Hqk,K] with p->H % Hqk == 0; head h reads q/k head h / (H / Hqk). v, o
+ *   [B,T,H,V]; g [B,T,H] (or [B,T,H,K], gate_k); beta [B,T,H]. K and V in {64, 128}, each.
+ *   slots_in  [nseq] int32 DEVICE array: the slot each sequence starts from; a negative entry, or
+ *             slots_in NULL, is a zero state.
+ *   slots_out int32 DEVICE array, or NULL (no state is written): per_token == 0: [nseq], the slot
+ *             that receives the state after the sequence's last token (after none: the state it
+ *             starts from); per_token == 1: [B*T], for every token the slot that receives the state
+ *             after it. A negative entry is not written.
+ *   A sequence may write the slot it reads, and one slot several times (the last token's state
+ *   stays). Several sequences may read one slot. A slot that one sequence writes and another one
+ *   reads or writes in the same call is not written by any and is recorded in the error word.
+ *   o         [B,T,H,V] out_dtype, written.
+ *   The lengths and slots are checked on the device (GDN_ERR_INVALID_ARG from
+ *   gdn_check_device_error): a bad cu_seqlens writes nothing at all; a slots_in entry >= num_slots
+ *   leaves its sequence out, a slots_out entry >= num_slots that state.
+ *   Workspace: gdn_recurrent_workspace_bytes(num_slots), its first 256 bytes zero before the
+ *   first call. The index arrays need 4-byte alignment, every other pointer 16. Nothing is read
+ *   back to the host: the call can be captured in a CUDA graph. */
+GDN_API gdn_status gdn_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, const int* cu_seqlens,
+                                     const void* q, const void* k, const void* v, const void* g,
+                                     const void* beta, float* state, int num_slots,
+                                     const int* slots_in, const int* slots_out, int per_token,
+                                     void* o, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 /* Self-test of the failure path every kernel wait takes: one CTA waits on a barrier that
  * nothing arrives at, with a limit of limit_cycles SM clock cycles (1 .. 2^32), then records
  * GDN_ERR_TIMEOUT (detail word 0x5E) in the workspace's device error word and returns, as a
@@ -392,8 +434,9 @@ GDN_API const char* gdn_status_string(gdn_status s);
 
 /* Synchronises `stream`, reads the workspace's device error word, clears it, and returns
  * GDN_OK, GDN_ERR_TIMEOUT (a bounded wait ran out; the results of the affected calls are
- * invalid), GDN_ERR_INVALID_ARG (gdn_varlen_fwd got a bad cu_seqlens) or GDN_ERR_CUDA. If `detail` is non-NULL it receives the recorded detail word
- * (which wait gave up), or 0. */
+ * invalid), GDN_ERR_INVALID_ARG (gdn_varlen_fwd or gdn_recurrent_fwd got a bad cu_seqlens, or an
+ * entry of an index array was refused) or GDN_ERR_CUDA. If `detail` is non-NULL it receives the
+ * recorded detail word (which wait gave up, which check failed), or 0. */
 GDN_API gdn_status gdn_check_device_error(void* workspace, void* stream, unsigned* detail);
 
 #ifdef __cplusplus

@@ -1,0 +1,71 @@
+"""The operators over the state cache and of the outputs' normalisation refuse bad calls on the host,
+before anything is launched (no GPU: nothing here gets as far as a launch)."""
+import ctypes
+
+import pytest
+import torch
+
+from context_scan_gb300 import _build, gdn
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build_cuda()
+    return gdn.lib()
+
+
+FAKE = ctypes.c_void_p(1 << 20)          # never dereferenced: every case fails validation first
+ODD = ctypes.c_void_p((1 << 20) + 8)
+BYTE = ctypes.c_void_p((1 << 20) + 2)
+
+
+def P(**kw):
+    d = dict(B=2, T=3, H=4, K=128, V=128, chunk=64, in_dtype=1, out_dtype=0, decay_first=0, gate_k=0)
+    d.update(kw)
+    return gdn.Problem(**d)
+
+
+def recurrent(L, prob=None, Hqk=2, nseq=2, cu=None, q=FAKE, k=FAKE, v=FAKE, g=FAKE, beta=FAKE,
+              state=FAKE, slots=5, sin=FAKE, sout=FAKE, per_token=0, o=FAKE, ws=FAKE, n=1 << 20):
+    return L.gdn_recurrent_fwd(ctypes.byref(prob or P()), Hqk, nseq, cu, q, k, v, g, beta, state, slots,
+                               sin, sout, per_token, o, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(prob=P(B=0)), 1), (dict(prob=P(T=-1)), 1), (dict(prob=P(H=0)), 1), (dict(nseq=0), 1),
+    (dict(nseq=3), 1),                              # B sequences without cu_seqlens
+    (dict(cu=FAKE), 1),                             # B == 1 with it
+    (dict(Hqk=0), 1), (dict(Hqk=3), 2), (dict(Hqk=8), 2),
+    (dict(slots=-1), 1), (dict(per_token=2), 1),
+    (dict(prob=P(decay_first=2)), 1), (dict(prob=P(gate_k=-1)), 1),
+    (dict(prob=P(K=96)), 2), (dict(prob=P(V=32)), 2), (dict(prob=P(V=256)), 2),
+    (dict(prob=P(in_dtype=2)), 3), (dict(prob=P(out_dtype=99)), 3),
+    (dict(prob=P(B=1 << 16, T=1 << 15), nseq=1 << 16), 2),
+    (dict(prob=P(B=1 << 28, T=1), nseq=1 << 28), 2),
+    (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(g=None), 1), (dict(beta=None), 1),
+    (dict(o=None), 1), (dict(state=None), 1),
+    (dict(ws=None), 5), (dict(n=256), 5),
+    (dict(q=ODD), 4), (dict(k=ODD), 4), (dict(v=ODD), 4), (dict(g=ODD), 4), (dict(beta=ODD), 4),
+    (dict(state=ODD), 4), (dict(o=ODD), 4), (dict(ws=ODD), 4), (dict(sin=BYTE), 4),
+    (dict(sout=BYTE), 4), (dict(prob=P(B=1), cu=BYTE), 4),
+])
+def test_recurrent_refusals(L, kw, status):
+    assert recurrent(L, **kw) == status
+
+
+def test_recurrent_workspace(L):
+    assert L.gdn_recurrent_workspace_bytes(-1) == 0
+    assert L.gdn_recurrent_workspace_bytes(0) == 256
+    assert L.gdn_recurrent_workspace_bytes(1) == 512
+    assert L.gdn_recurrent_workspace_bytes(64) == 512
+    assert L.gdn_recurrent_workspace_bytes(65) == 768
+    with pytest.raises(gdn.GdnError):
+        gdn.alloc_recurrent_workspace(-1, device="cpu")
+
+
+def test_recurrent_binding_refuses_tensors_off_the_device(L):
+    q, v, gate = torch.zeros(1, 1, 1, 64), torch.zeros(1, 1, 2, 64), torch.zeros(1, 1, 2)
+    state, slots = torch.zeros(3, 2, 64, 64), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="q is on cpu"):
+        gdn.gdn_recurrent_fwd(q, q, v, gate, gate, state, slots, slots, v.clone(),
+                              torch.zeros(512, dtype=torch.uint8))
