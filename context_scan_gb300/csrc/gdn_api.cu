@@ -962,6 +962,7 @@ const char* gdn_status_string(gdn_status s) {
         case GDN_ERR_CUDA: return "CUDA error";
         case GDN_ERR_TIMEOUT: return "a kernel's bounded wait ran out";
         case GDN_ERR_DEVICE: return "current device is not an sm_103 GPU";
+        case GDN_ERR_NO_PAGE: return "no free page left in the state cache";
     }
     return "unknown status";
 }
@@ -991,7 +992,7 @@ gdn_status gdn_check_device_error(void* workspace, void* stream, unsigned* detai
     if (cudaMemsetAsync(workspace, 0, sizeof(host), s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return GDN_ERR_CUDA;
-    if (host.code == GDN_ERR_TIMEOUT || host.code == GDN_ERR_INVALID_ARG)
+    if (host.code == GDN_ERR_TIMEOUT || host.code == GDN_ERR_INVALID_ARG || host.code == GDN_ERR_NO_PAGE)
         return static_cast<gdn_status>(host.code);
     return GDN_ERR_CUDA;
 }

@@ -17,7 +17,8 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libgdn.so")
 GDN_DTYPE_F32, GDN_DTYPE_BF16 = 0, 1
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARG", 2: "GDN_ERR_UNSUPPORTED_SHAPE",
           3: "GDN_ERR_UNSUPPORTED_DTYPE", 4: "GDN_ERR_MISALIGNED", 5: "GDN_ERR_WORKSPACE",
-          6: "GDN_ERR_CUDA", 7: "GDN_ERR_TIMEOUT", 8: "GDN_ERR_DEVICE"}
+          6: "GDN_ERR_CUDA", 7: "GDN_ERR_TIMEOUT", 8: "GDN_ERR_DEVICE",
+          9: "GDN_ERR_NO_PAGE"}
 EXPORTED = ("gdn_workspace_bytes", "gdn_segmented_pieces", "gdn_segmented_plan", "gdn_chunk_fwd",
             "gdn_segment_summary", "gdn_summary_scan", "gdn_segment_fwd", "gdn_segmented_fwd",
             "gdn_segmented_fwd_timed", "gdn_segmented_fwd_noalloc",
@@ -25,6 +26,8 @@ EXPORTED = ("gdn_workspace_bytes", "gdn_segmented_pieces", "gdn_segmented_plan",
             "gdn_state_grad_summary", "gdn_state_grad_scan", "gdn_chunk_bwd_workspace_bytes",
             "gdn_chunk_bwd", "gdn_chunk_bwd_timed",
             "gdn_recurrent_workspace_bytes", "gdn_recurrent_fwd",
+            "gdn_cache_workspace_bytes", "gdn_cache_copy", "gdn_cache_fork", "gdn_cache_free",
+            "gdn_cache_compact",
             "gdn_status_string", "gdn_check_device_error", "gdn_selftest_wait_timeout")
 
 
@@ -84,6 +87,14 @@ def lib():
         L.gdn_recurrent_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_recurrent_fwd.argtypes = ([pp, ctypes.c_int, ctypes.c_int] + [_P] * 7 + [ctypes.c_int] +
                                         [_P] * 2 + [ctypes.c_int] + [_P] * 2 + [ctypes.c_size_t, _P])
+        L.gdn_cache_workspace_bytes.argtypes = [ctypes.c_int, ctypes.c_int]
+        L.gdn_cache_workspace_bytes.restype = ctypes.c_size_t
+        pages = [_P, ctypes.c_int, ctypes.c_int, ctypes.c_size_t]
+        ws = [_P, ctypes.c_size_t, _P]
+        L.gdn_cache_copy.argtypes = pages + [ctypes.c_int, _P, _P] + ws
+        L.gdn_cache_fork.argtypes = pages + [_P, ctypes.c_int, _P, _P, ctypes.c_int] + ws
+        L.gdn_cache_free.argtypes = [ctypes.c_int, _P, ctypes.c_int, _P] + ws
+        L.gdn_cache_compact.argtypes = pages + [_P, ctypes.c_int, _P, _P, _P] + ws
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_check_device_error.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_uint)]
@@ -92,7 +103,8 @@ def lib():
                    "gdn_segmented_fwd", "gdn_segmented_fwd_timed", "gdn_segmented_fwd_noalloc",
                    "gdn_varlen_fwd", "gdn_varlen_fwd_timed", "gdn_check_device_error",
                    "gdn_selftest_wait_timeout", "gdn_state_grad_summary", "gdn_state_grad_scan",
-                   "gdn_chunk_bwd", "gdn_chunk_bwd_timed", "gdn_recurrent_fwd"):
+                   "gdn_chunk_bwd", "gdn_chunk_bwd_timed", "gdn_recurrent_fwd", "gdn_cache_copy",
+                   "gdn_cache_fork", "gdn_cache_free", "gdn_cache_compact"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -397,6 +409,83 @@ def gdn_recurrent_fwd(q, k, v, g, beta, state, slots_in, slots_out, o, workspace
                                    _ptr(slots_out), int(per_token), _ptr(o), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(), _stream(stream)),
            "gdn_recurrent_fwd")
+
+
+def alloc_cache_workspace(num_pages: int, n: int = 0, device="cuda"):
+    """A zeroed workspace tensor for the gdn_cache calls on a cache of num_pages pages, with at most
+    n pairs (copy) or requests (fork) a call."""
+    import torch
+    size = int(lib().gdn_cache_workspace_bytes(num_pages, n))
+    if size == 0:
+        raise GdnError(1, "gdn_cache_workspace_bytes")
+    return torch.zeros(size, dtype=torch.uint8, device=device)
+
+
+def _pages(pages):
+    if pages.dim() < 3:
+        raise ValueError("pages is [layers, num_pages, ...]")
+    layers, num = pages.shape[0], pages.shape[1]
+    total = pages.numel() * pages.element_size()
+    return pages.data_ptr(), layers, num, total // (layers * num) if total else 0
+
+
+def _indexes(**arrays):
+    """Lengths aside, index arrays are one-dimensional int32."""
+    import torch
+    for name, t in arrays.items():
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1):
+            raise ValueError(f"{name} is not a one-dimensional int32 tensor")
+
+
+def _room(workspace):
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def gdn_cache_copy(pages, src, dst, workspace, stream=None):
+    """pages [layers, num_pages, ...]: page dst[i] := page src[i] in every layer (zeros for a
+    negative src, nothing for a negative dst); src, dst int32 GPU tensors."""
+    _on_device(pages=pages, src=src, dst=dst, workspace=workspace)
+    _indexes(src=src, dst=dst)
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst differ in length")
+    _check(lib().gdn_cache_copy(*_pages(pages), src.numel(), _ptr(src), _ptr(dst), *_room(workspace),
+                                _stream(stream)), "gdn_cache_copy")
+
+
+def gdn_cache_fork(pages, refs, parents, children, workspace, share=False, stream=None):
+    """A copy of page parents[i] (zeros for a negative one) in the next of the lowest-numbered free
+    pages (refs 0), its number in children[i] (-1: refused); share: the parent gains a user
+    instead. refs, parents, children int32 GPU tensors."""
+    _on_device(pages=pages, refs=refs, parents=parents, children=children, workspace=workspace)
+    _indexes(refs=refs, parents=parents, children=children)
+    if parents.numel() != children.numel() or refs.numel() != pages.shape[1]:
+        raise ValueError("one child a parent and one count a page are wanted")
+    _check(lib().gdn_cache_fork(*_pages(pages), _ptr(refs), parents.numel(), _ptr(parents),
+                                _ptr(children), int(share), *_room(workspace), _stream(stream)),
+           "gdn_cache_fork")
+
+
+def gdn_cache_free(refs, pages, workspace, stream=None):
+    """One user less of every page named in `pages` (int32; negative entries are skipped)."""
+    _on_device(refs=refs, pages=pages, workspace=workspace)
+    _indexes(refs=refs, pages=pages)
+    _check(lib().gdn_cache_free(refs.numel(), _ptr(refs), pages.numel(), _ptr(pages),
+                                *_room(workspace), _stream(stream)), "gdn_cache_free")
+
+
+def gdn_cache_compact(pages, refs, table, remap, live, workspace, stream=None):
+    """The pages in use move to the front of the cache; table (or None) is rewritten to the new
+    numbers, remap [num_pages] (or None) and live [1] (or None) receive every page's new number
+    and how many are in use."""
+    _on_device(pages=pages, refs=refs, table=table, remap=remap, live=live, workspace=workspace)
+    _indexes(refs=refs, table=table, remap=remap, live=live)
+    num = pages.shape[1]
+    if refs.numel() != num or (remap is not None and remap.numel() != num) or (
+            live is not None and live.numel() != 1):
+        raise ValueError("one count and one new number a page are wanted, and one int for live")
+    _check(lib().gdn_cache_compact(*_pages(pages), _ptr(refs), 0 if table is None else table.numel(),
+                                   _ptr(table), _ptr(remap), _ptr(live), *_room(workspace),
+                                   _stream(stream)), "gdn_cache_compact")
 
 
 def gdn_selftest_wait_timeout(workspace, limit_cycles, stream=None):

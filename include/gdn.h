@@ -82,7 +82,8 @@ typedef enum {
     GDN_ERR_WORKSPACE = 5,         /* workspace NULL or smaller than gdn_workspace_bytes() */
     GDN_ERR_CUDA = 6,              /* a CUDA runtime call or launch failed */
     GDN_ERR_TIMEOUT = 7,           /* a kernel's bounded wait ran out (device error word) */
-    GDN_ERR_DEVICE = 8             /* the current device is not an sm_103 GPU */
+    GDN_ERR_DEVICE = 8,            /* the current device is not an sm_103 GPU */
+    GDN_ERR_NO_PAGE = 9            /* a state cache had no free page left (device error word) */
 } gdn_status;
 
 typedef enum { GDN_DTYPE_F32 = 0, GDN_DTYPE_BF16 = 1 } gdn_dtype;
@@ -421,6 +422,59 @@ GDN_API gdn_status gdn_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, co
                                      void* o, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Pages of a state cache
+ * ---------------------------------------------------------------------------------------
+ * A cache is pages [layers, num_pages, page_bytes]: a page number names one page in every
+ * layer's array (layer l's array is the state of gdn_recurrent_fwd; a page is H*K*V*4 bytes there,
+ * but the calls below move bytes of any meaning). page_bytes % 16 == 0. Which pages are in use
+ * stands in refs [num_pages] int32 on the device: a page's count of users, 0 (or less) a free page.
+ * All page numbers and counts live on the device, nothing is read back to the host, and every call
+ * can be captured in a CUDA graph. The index arrays are int32 DEVICE arrays of 4-byte alignment
+ * that do not overlap one another unless a call says so; pages and the workspace need 16 bytes.
+ * Entries that a call refuses are recorded in the error word (gdn_check_device_error):
+ * GDN_ERR_INVALID_ARG, or GDN_ERR_NO_PAGE when a cache is full. */
+
+/* Workspace bytes for the calls below on a cache of num_pages pages and at most n pairs or requests a
+ * call (n of gdn_cache_copy and gdn_cache_fork; 0 for the others). Its first 256 bytes must be zero
+ * before the first call. Returns 0 for num_pages < 1 or n < 0. */
+GDN_API size_t gdn_cache_workspace_bytes(int num_pages, int n);
+
+/* Page dst[i] := page src[i] in every layer, i < n; src[i] < 0: page dst[i] := zeros; dst[i] < 0: the
+ * pair is skipped. The result is that of reading every page before writing any: a pair whose dst is
+ * another pair's dst or src is left out and refused, as is one with a number >= num_pages. */
+GDN_API gdn_status gdn_cache_copy(void* pages, int layers, int num_pages, size_t page_bytes, int n,
+                                  const int* src, const int* dst, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* n new pages: request i takes the next of the lowest-numbered free pages, whose count becomes 1 and
+ * whose contents become those of page parents[i] (zeros for parents[i] < 0, a new sequence), and
+ * children[i] receives its number. A parent that is free or >= num_pages is refused; once the
+ * cache is full GDN_ERR_NO_PAGE is recorded; either way children[i] is -1 and no page is taken.
+ * share == 1: no page is taken, the parent's count goes up by one and children[i] = parents[i] (a
+ * negative parent is refused): sequences that start from one page and write others
+ * (slots_in, slots_out of gdn_recurrent_fwd). children may be parents. */
+GDN_API gdn_status gdn_cache_fork(void* pages, int layers, int num_pages, size_t page_bytes,
+                                  int* refs, int n, const int* parents, int* children, int share,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* One user less of each of the n pages in list (negative entries are skipped; a page named several
+ * times loses as many). A count that would fall below zero stays at zero and is refused, as is a
+ * number >= num_pages. The pages' contents stay as they are. */
+GDN_API gdn_status gdn_cache_free(int num_pages, int* refs, int n, const int* list, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* The pages in use move to the front: with L of them, those at page L and behind go, in order, to the
+ * free pages before page L, in order, in every layer, and their counts with them. The other pages in
+ * use stay; pages from L on are free afterwards (their contents stay).
+ *   table  [n] page numbers, rewritten to the new ones (negative entries stay; an entry that names a
+ *          free page or one >= num_pages becomes -1 and is refused). n may be 0.
+ *   remap  [num_pages], or NULL: receives the new number of every page, -1 for free ones.
+ *   live   one int, or NULL: receives L. */
+GDN_API gdn_status gdn_cache_compact(void* pages, int layers, int num_pages, size_t page_bytes,
+                                     int* refs, int n, int* table, int* remap, int* live,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* Self-test of the failure path every kernel wait takes: one CTA waits on a barrier that
  * nothing arrives at, with a limit of limit_cycles SM clock cycles (1 .. 2^32), then records
  * GDN_ERR_TIMEOUT (detail word 0x5E) in the workspace's device error word and returns, as a
@@ -435,7 +489,7 @@ GDN_API const char* gdn_status_string(gdn_status s);
 /* Synchronises `stream`, reads the workspace's device error word, clears it, and returns
  * GDN_OK, GDN_ERR_TIMEOUT (a bounded wait ran out; the results of the affected calls are
  * invalid), GDN_ERR_INVALID_ARG (gdn_varlen_fwd or gdn_recurrent_fwd got a bad cu_seqlens, or an
- * entry of an index array was refused) or GDN_ERR_CUDA. If `detail` is non-NULL it receives the
+ * entry of an index array was refused), GDN_ERR_NO_PAGE (gdn_cache_fork) or GDN_ERR_CUDA. If `detail` is non-NULL it receives the
  * recorded detail word (which wait gave up, which check failed), or 0. */
 GDN_API gdn_status gdn_check_device_error(void* workspace, void* stream, unsigned* detail);
 

@@ -30,3 +30,52 @@ def recurrence(q, k, v, g, beta, state, slots_in, slots_out, lens, per_token=Fal
         if not per_token and slots_out is not None and slots_out[s] >= 0:
             after[slots_out[s]] = S
     return o, after
+
+
+def cache_copy(pages, src, dst):
+    """pages [layers, num_pages, ...] after the copy; pairs that the call refuses are left out, and
+    whether any was."""
+    after, bad = pages.clone(), False
+    num = pages.shape[1]
+    for i, (a, b) in enumerate(zip(src, dst)):
+        others = [(x, y) for j, (x, y) in enumerate(zip(src, dst)) if j != i]
+        if a >= num or b >= num or (b >= 0 and any(b in pair for pair in others)):
+            bad = True
+        elif b >= 0:
+            after[:, b] = pages[:, a] if a >= 0 else 0
+    return after, bad
+
+
+def cache_fork(pages, refs, parents):
+    """(pages, refs, children, code of the error word) after a fork."""
+    pages, refs, before = pages.clone(), list(refs), list(refs)
+    free = [p for p, r in enumerate(refs) if r <= 0]
+    children, code = [], 0
+    for a in parents:
+        if a >= len(refs) or (a >= 0 and before[a] <= 0):
+            children.append(-1)
+            code = 1   # (recorded before a full cache is)
+        elif not free:
+            children.append(-1)
+            code = code or 9
+        else:
+            child = free.pop(0)
+            pages[:, child] = pages[:, a] if a >= 0 else 0
+            refs[child] = 1
+            children.append(child)
+    return pages, refs, children, code
+
+
+def cache_compact(pages, refs, table):
+    """(pages, refs, table, remap, live) after a compaction."""
+    pages, refs = pages.clone(), list(refs)
+    num = len(refs)
+    live = sum(r > 0 for r in refs)
+    remap = [p if refs[p] > 0 else -1 for p in range(num)]
+    holes = [p for p in range(live) if refs[p] <= 0]
+    for p in range(live, num):
+        if refs[p] > 0:
+            to = holes.pop(0)
+            pages[:, to], refs[to], refs[p], remap[p] = pages[:, p], refs[p], 0, to
+    table = [t if t < 0 else remap[t] if t < num else -1 for t in table]
+    return pages, refs, table, remap, live

@@ -69,3 +69,51 @@ def test_recurrent_binding_refuses_tensors_off_the_device(L):
     with pytest.raises(ValueError, match="q is on cpu"):
         gdn.gdn_recurrent_fwd(q, q, v, gate, gate, state, slots, slots, v.clone(),
                               torch.zeros(512, dtype=torch.uint8))
+
+
+def test_cache_workspace(L):
+    W = L.gdn_cache_workspace_bytes
+    assert W(0, 1) == 0 and W(1, -1) == 0
+    # header, an int a page, eight bytes a job (pairs, or at most half of the pages), an int a request
+    assert W(1, 0) == 256 + 256 + 256
+    assert W(1000, 0) == 256 + 4096 + 4096
+    assert W(1000, 700) == 256 + 4096 + 5632 + 2816
+    with pytest.raises(gdn.GdnError):
+        gdn.alloc_cache_workspace(0, device="cpu")
+
+
+PAGES = dict(pages=FAKE, layers=2, num=8, bytes=4096)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(pages=None), 1), (dict(layers=0), 1), (dict(num=0), 1), (dict(n=-1), 1),
+    (dict(bytes=0), 2), (dict(bytes=24), 2), (dict(bytes=1 << 40), 2), (dict(pages=ODD), 4),
+    (dict(ws=None), 5), (dict(room=256), 5), (dict(ws=ODD), 4),
+    (dict(a=None), 1), (dict(b=None), 1), (dict(a=BYTE), 4), (dict(b=BYTE), 4),
+    (dict(refs=None), 1), (dict(refs=BYTE), 4), (dict(share=2), 1), (dict(remap=BYTE), 4),
+    (dict(live=BYTE), 4),
+])
+def test_cache_refusals(L, kw, status):
+    a = dict(PAGES, n=3, a=FAKE, b=FAKE, refs=FAKE, share=0, remap=None, live=None, ws=FAKE, room=1 << 20)
+    a.update(kw)
+    head, ws = (a["pages"], a["layers"], a["num"], a["bytes"]), (a["ws"], a["room"], None)
+    only = set(kw)
+    if not only & {"refs", "share", "remap", "live"}:
+        assert L.gdn_cache_copy(*head, a["n"], a["a"], a["b"], *ws) == status
+    if not only & {"remap", "live"}:
+        assert L.gdn_cache_fork(*head, a["refs"], a["n"], a["a"], a["b"], a["share"], *ws) == status
+    if not only & {"b", "share"}:
+        assert L.gdn_cache_compact(*head, a["refs"], a["n"], a["a"], a["remap"], a["live"], *ws) == status
+    if only <= {"num", "n", "ws", "room", "a", "refs"}:
+        assert L.gdn_cache_free(a["num"], a["refs"], a["n"], a["a"], *ws) == status
+
+
+def test_cache_binding_refuses_tensors_off_the_device(L):
+    pages, idx = torch.zeros(1, 4, 16), torch.zeros(1, dtype=torch.int32)
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    for call in (lambda: gdn.gdn_cache_copy(pages, idx, idx, ws),
+                 lambda: gdn.gdn_cache_fork(pages, idx, idx, idx, ws),
+                 lambda: gdn.gdn_cache_free(idx, idx, ws),
+                 lambda: gdn.gdn_cache_compact(pages, idx, None, None, None, ws)):
+        with pytest.raises(ValueError, match="is on cpu"):
+            call()
