@@ -27,7 +27,7 @@ EXPORTED = ("gdn_workspace_bytes", "gdn_segmented_pieces", "gdn_segmented_plan",
             "gdn_chunk_bwd", "gdn_chunk_bwd_timed",
             "gdn_recurrent_workspace_bytes", "gdn_recurrent_fwd",
             "gdn_cache_workspace_bytes", "gdn_cache_copy", "gdn_cache_fork", "gdn_cache_free",
-            "gdn_cache_compact",
+            "gdn_cache_compact", "gdn_norm_fwd", "gdn_norm_bwd_workspace_bytes", "gdn_norm_bwd",
             "gdn_status_string", "gdn_check_device_error", "gdn_selftest_wait_timeout")
 
 
@@ -95,6 +95,11 @@ def lib():
         L.gdn_cache_fork.argtypes = pages + [_P, ctypes.c_int, _P, _P, ctypes.c_int] + ws
         L.gdn_cache_free.argtypes = [ctypes.c_int, _P, ctypes.c_int, _P] + ws
         L.gdn_cache_compact.argtypes = pages + [_P, ctypes.c_int, _P, _P, _P] + ws
+        rows = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float]
+        L.gdn_norm_fwd.argtypes = rows + [_P] * 6
+        L.gdn_norm_bwd_workspace_bytes.argtypes = [ctypes.c_longlong, ctypes.c_int]
+        L.gdn_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_norm_bwd.argtypes = rows + [_P] * 9 + ws
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_check_device_error.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_uint)]
@@ -104,7 +109,8 @@ def lib():
                    "gdn_varlen_fwd", "gdn_varlen_fwd_timed", "gdn_check_device_error",
                    "gdn_selftest_wait_timeout", "gdn_state_grad_summary", "gdn_state_grad_scan",
                    "gdn_chunk_bwd", "gdn_chunk_bwd_timed", "gdn_recurrent_fwd", "gdn_cache_copy",
-                   "gdn_cache_fork", "gdn_cache_free", "gdn_cache_compact"):
+                   "gdn_cache_fork", "gdn_cache_free", "gdn_cache_compact", "gdn_norm_fwd",
+                   "gdn_norm_bwd"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -486,6 +492,46 @@ def gdn_cache_compact(pages, refs, table, remap, live, workspace, stream=None):
     _check(lib().gdn_cache_compact(*_pages(pages), _ptr(refs), 0 if table is None else table.numel(),
                                    _ptr(table), _ptr(remap), _ptr(live), *_room(workspace),
                                    _stream(stream)), "gdn_cache_compact")
+
+
+def _rows(x, y_like, params, **rest):
+    """(rows, N) of x [..., N]; the tensors of y's type have x's shape, the parameters are fp32 [N]."""
+    import torch
+    N = x.shape[-1]
+    for name, t in rest.items():
+        _is(name, t, y_like.dtype, x.shape)
+    for name, t in params.items():
+        _is(name, t, torch.float32, (N,))
+    return x.numel() // N if N else 0, N
+
+
+def gdn_norm_fwd(x, w, b, z, y, eps=1e-6, rms=True, stream=None):
+    """y = ((x - m) s w + b) z sigmoid(z) row by row: x, z, y [..., N], w, b [N] fp32 (w, b, z may
+    be None); rms: the root-mean-square norm (m = 0), else the layer norm. z has y's type."""
+    _on_device(x=x, w=w, b=b, z=z, y=y)
+    rows, N = _rows(x, y, dict(w=w, b=b), z=z, y=y)
+    _check(lib().gdn_norm_fwd(rows, N, _dtype_code(x), _dtype_code(y), int(rms), eps, _ptr(x), _ptr(w),
+                              _ptr(b), _ptr(z), _ptr(y), _stream(stream)), "gdn_norm_fwd")
+
+
+def alloc_norm_bwd_workspace(rows: int, N: int, device="cuda"):
+    """A workspace tensor for gdn_norm_bwd on rows rows of N values."""
+    import torch
+    n = int(lib().gdn_norm_bwd_workspace_bytes(rows, N))
+    if n == 0:
+        raise GdnError(2, "gdn_norm_bwd_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def gdn_norm_bwd(x, w, b, z, dy, dx, dz, dw, db, workspace, eps=1e-6, rms=True, stream=None):
+    """Gradients of gdn_norm_fwd for dy (z's and y's type): dx (x's type), dz (None skips it), dw, db
+    [N] fp32 (None skips either)."""
+    _on_device(x=x, w=w, b=b, z=z, dy=dy, dx=dx, dz=dz, dw=dw, db=db, workspace=workspace)
+    rows, N = _rows(x, dy, dict(w=w, b=b, dw=dw, db=db), z=z, dy=dy, dz=dz)
+    _is("dx", dx, x.dtype, x.shape)
+    _check(lib().gdn_norm_bwd(rows, N, _dtype_code(x), _dtype_code(dy), int(rms), eps, _ptr(x), _ptr(w),
+                              _ptr(b), _ptr(z), _ptr(dy), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(db),
+                              *_room(workspace), _stream(stream)), "gdn_norm_bwd")
 
 
 def gdn_selftest_wait_timeout(workspace, limit_cycles, stream=None):

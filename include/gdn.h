@@ -475,6 +475,35 @@ GDN_API gdn_status gdn_cache_compact(void* pages, int layers, int num_pages, siz
                                      int* refs, int n, int* table, int* remap, int* live,
                                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Normalisation of the outputs, and its gradients
+ * ---------------------------------------------------------------------------------------
+ * What follows the rule in a layer: each row of N values -- a token's output of one head, or a hidden
+ * state -- is normalised, scaled, and gated:
+ *   y = ((x - m) s w + b) [z sigmoid(z)],  m = mean(x),  s = 1 / sqrt(mean((x - m)^2) + eps)
+ * (layer norm), or with m = 0 (rms == 1, the root-mean-square norm); w, b, z NULL leave their factor
+ * or term out. With rms == 1, w = 1/sqrt(N) and eps / N for eps it is the L2 normalisation of q and k.
+ * x [rows, N] in x_dtype (the rule's out_dtype); z, y [rows, N] in y_dtype; w, b [N] fp32; contiguous.
+ * 1 <= N <= 8192, rows >= 0, rows * N < 2^40, eps >= 0 and finite; pointers 16-byte aligned.
+ * Sums and statistics are fp32 (a row whose squares leave fp32's range overflows as they do). */
+GDN_API gdn_status gdn_norm_fwd(long long rows, int N, int x_dtype, int y_dtype, int rms, float eps,
+                                const void* x, const float* w, const float* b, const void* z,
+                                void* y, void* stream);
+
+/* Workspace bytes for gdn_norm_bwd: the blocks' sums of dw and db (at most 33 MiB). It needs no
+ * initial value. Returns 0 for rows or N outside the set above. */
+GDN_API size_t gdn_norm_bwd_workspace_bytes(long long rows, int N);
+
+/* The gradients for dy [rows, N] in y_dtype, the gradient on y: dx [rows, N] in x_dtype (it is the dO
+ * of gdn_chunk_bwd); dz [rows, N] in y_dtype (NULL skips it, and must be without z); dw, db [N] fp32,
+ * summed over the rows in a fixed order (NULL skips either). The statistics are formed again
+ * from x. dx may be x and dz may be z (also y of the forward x or z, where the types agree); otherwise
+ * outputs overlap nothing. */
+GDN_API gdn_status gdn_norm_bwd(long long rows, int N, int x_dtype, int y_dtype, int rms, float eps,
+                                const void* x, const float* w, const float* b, const void* z,
+                                const void* dy, void* dx, void* dz, float* dw, float* db,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* Self-test of the failure path every kernel wait takes: one CTA waits on a barrier that
  * nothing arrives at, with a limit of limit_cycles SM clock cycles (1 .. 2^32), then records
  * GDN_ERR_TIMEOUT (detail word 0x5E) in the workspace's device error word and returns, as a

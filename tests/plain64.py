@@ -79,3 +79,37 @@ def cache_compact(pages, refs, table):
             pages[:, to], refs[to], refs[p], remap[p] = pages[:, p], refs[p], 0, to
     table = [t if t < 0 else remap[t] if t < num else -1 for t in table]
     return pages, refs, table, remap, live
+
+
+def norm(x, w, b, z, rms, eps):
+    """y in float64 (differentiable)."""
+    m = 0.0 if rms else x.mean(-1, keepdim=True)
+    var = ((x - m) ** 2).mean(-1, keepdim=True)
+    y = (x - m) / torch.sqrt(var + eps)
+    if w is not None:
+        y = y * w
+    if b is not None:
+        y = y + b
+    return y if z is None else y * z * torch.sigmoid(z)
+
+
+def norm_grads(x, w, b, z, dy, rms, eps):
+    """(dx, dz, dw, db) by the formulas, in float64; the parameters' gradients also where they are None."""
+    x, dy = x.double(), dy.double()
+    n = x.shape[-1]
+    w = torch.ones(n, dtype=torch.float64) if w is None else w.double()
+    b = torch.zeros(n, dtype=torch.float64) if b is None else b.double()
+    xm = x if rms else x - x.mean(-1, keepdim=True)
+    s = 1.0 / torch.sqrt((xm * xm).mean(-1, keepdim=True) + eps)
+    xh, d, dz = xm * s, dy, None
+    if z is not None:
+        z = z.double()
+        sg = torch.sigmoid(z)
+        dz = dy * (xh * w + b) * sg * (1 + z * (1 - sg))
+        d = dy * z * sg
+    dw, db = (d * xh).sum(0), d.sum(0)
+    dxh = d * w
+    dx = dxh - xh * (dxh * xh).mean(-1, keepdim=True)
+    if not rms:
+        dx = dx - dxh.mean(-1, keepdim=True)
+    return dx * s, dz, dw, db

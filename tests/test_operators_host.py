@@ -117,3 +117,38 @@ def test_cache_binding_refuses_tensors_off_the_device(L):
                  lambda: gdn.gdn_cache_compact(pages, idx, None, None, None, ws)):
         with pytest.raises(ValueError, match="is on cpu"):
             call()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), 1), (dict(N=0), 1), (dict(rms=2), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
+    (dict(eps=float("inf")), 1), (dict(N=8193), 2), (dict(rows=1 << 40), 2), (dict(xt=2), 3), (dict(yt=-1), 3),
+    (dict(x=None), 1), (dict(y=None), 1), (dict(x=ODD), 4), (dict(w=ODD), 4), (dict(b=ODD), 4),
+    (dict(z=ODD), 4), (dict(y=ODD), 4), (dict(dy=None), 1), (dict(dy=ODD), 4), (dict(dz=ODD), 4),
+    (dict(z=None, dz=FAKE), 1), (dict(dw=ODD), 4), (dict(db=ODD), 4), (dict(ws=None), 5), (dict(room=256), 5),
+    (dict(ws=ODD), 4),
+])
+def test_norm_refusals(L, kw, status):
+    a = dict(rows=4, N=64, xt=0, yt=1, rms=1, eps=1e-6, x=FAKE, w=FAKE, b=FAKE, z=FAKE, y=FAKE, dy=FAKE,
+             dz=FAKE, dw=FAKE, db=FAKE, ws=FAKE, room=1 << 25)
+    a.update(kw)
+    head = [a[k] for k in ("rows", "N", "xt", "yt", "rms", "eps")]
+    if not set(kw) & {"dy", "dz", "dw", "db", "ws", "room"}:
+        assert L.gdn_norm_fwd(*head, a["x"], a["w"], a["b"], a["z"], a["y"], None) == status
+    assert L.gdn_norm_bwd(*head, a["x"], a["w"], a["b"], a["z"], a["dy"], a["y"], a["dz"], a["dw"], a["db"],
+                          a["ws"], a["room"], None) == status
+
+
+def test_norm_workspace(L):
+    W = L.gdn_norm_bwd_workspace_bytes
+    assert W(-1, 8) == 0 and W(1, 0) == 0 and W(1, 8193) == 0
+    assert W(0, 64) == 256
+    assert W(1, 64) == 256 + 512                      # one block's sums of dw and db
+    assert max(W(1 << 24, n) for n in (1, 128, 256, 257, 2048, 4096, 8192)) <= 33 << 20   # 2 * 8192 * 4 B * 512 blocks
+
+
+def test_norm_binding_refuses_tensors_off_the_device(L):
+    x, w = torch.zeros(2, 64), torch.zeros(64)
+    with pytest.raises(ValueError, match="is on cpu"):
+        gdn.gdn_norm_fwd(x, w, None, None, x.clone())
+    with pytest.raises(ValueError, match="is on cpu"):
+        gdn.gdn_norm_bwd(x, w, None, None, x, x.clone(), None, w.clone(), None, torch.zeros(4096, dtype=torch.uint8))
