@@ -1,19 +1,31 @@
 // gdn_recurrent.cu -- the recurrent gated delta rule over a state cache (gdn_recurrent_fwd):
-// every sequence's tokens one after another from the state in one cache page, fp32 throughout.
+// every sequence's tokens in order from the state in one cache page, fp32 throughout.
 //
 // Per sequence, head and token ("RFC: HyperParallel Linear Attention Context Parallel", section
 // 2.1; the decayed read as in "Context Parallelism in ART", section 08), with E = exp(g) or, per
 // key channel, diag(exp(g)), and H_read = H or E H:
 //   r = beta (v - k^T H_read),   H' = E H + k r^T,   o = q^T H' = (E q)^T H + (q . k) r.
+//
 // The last form lets both products read the state before the update, so a token takes one pass
 // of sums, one exchange between lanes and one pass of updates.
 //
-// Split: every column of the state is independent given k, q and the gates. A warp owns CW
-// columns of one head, all K rows of them in registers (each lane four columns of every
-// 128 / CW -th quad of rows, the rows in pairs for the two-wide fp32 instructions), so the state is
-// read from memory once, when the sequence starts, and written once, when it ends (or after every
-// token when the caller keeps them all). The tokens' k, q, v and gates are staged in shared memory
-// eight at a time, the next eight loading while these are worked on.
+// Every column of the state is independent given k, q and the gates. A warp owns CW columns of one
+// head, all K rows of them in registers (Tile below), so the state is read from memory once, when the
+// sequence starts, and written once, when it ends (or after every token when the caller keeps
+// them all). Two kernels, whose measurements stand beside the rule that picks the split (launch_k):
+//  - decode_kernel, one token a sequence: bound by the memory traffic of the states. A warp needs
+//    nothing of another one, so it waits for nothing but its own loads; four blocks of 128 registers a
+//    thread keep 128 KB of states on their way per SM. 256 sequences, H = 32, K = V = 128:
+//    172 us, 6.3 TB/s (93 % of a copy); tokens_kernel took 214 us there.
+//  - tokens_kernel, any number of tokens: bound by traffic up to a few tokens (48 sequences of 1 to 8
+//    tokens, every state kept: 95 us, 5.9 TB/s), then by the fp32 pipe, which the two-wide
+//    multiply-adds hold for two cycles each, and by the passes' latencies (37 sequences of up to 63
+//    tokens, H = 16, per-channel gates: 79 us; 103 us without the order of ordered_sequence).
+//    A block form over eight tokens (all products with the state first, then a triangular solve in each
+//    lane) and one with the next token's sums formed beside the update both took longer there (113
+//    and 83 us): what they save in waiting they spend in instructions.
+#include <climits>
+
 #include <cuda_bf16.h>
 
 #include "gdn_internal.h"
@@ -21,7 +33,8 @@
 namespace gdn {
 namespace {
 
-constexpr int kTokens = 8;   // tokens staged at once
+constexpr int kTokens = 8;   // tokens of a block
+constexpr int kWarps = 4;    // of every thread block
 // detail words of GDN_ERR_INVALID_ARG
 constexpr unsigned kTagLengths = 0x41, kTagSlotRange = 0x42, kTagSlotShared = 0x43;
 constexpr int kNobody = -1, kShared = -2;
@@ -42,6 +55,7 @@ struct RecurrentParams {
     DeviceError* err;
     int nseq, T, H, Hqk, V, num_slots;
     int out_bf16, decay_first, per_token;
+    int ordered;           // the longest sequences first (ordered_sequence)
 };
 
 using pair_t = unsigned long long;   // two fp32 values of one column, rows 2 i and 2 i + 1
@@ -100,6 +114,27 @@ struct Raw8 {
                 f[4 + i] = __uint_as_float(t[i]);
             }
         }
+    }
+};
+
+// four consecutive values as stored
+template <bool BF>
+struct Raw4 {
+    unsigned u[BF ? 2 : 4];
+    __device__ __forceinline__ void load(const void* base, long long at) {
+        if constexpr (BF) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>((const char*)base + 2 * at));
+            u[0] = x.x, u[1] = x.y;
+        } else {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>((const char*)base + 4 * at));
+            u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
+        }
+    }
+    __device__ __forceinline__ void pairs(pair_t (&d)[2]) const {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            d[j] = BF ? pack(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u))
+                      : pack(__uint_as_float(u[BF ? 0 : 2 * j]), __uint_as_float(u[BF ? 0 : 2 * j + 1]));
     }
 };
 
@@ -194,90 +229,342 @@ __global__ void __launch_bounds__(kClaimThreads)
     }
 }
 
-template <int K, int CW, int WARPS, bool GATEK, bool BF>
-__global__ void __launch_bounds__(32 * WARPS) recurrent_kernel(RecurrentParams p) {
-    constexpr int THREADS = 32 * WARPS;
-    constexpr int CL = CW / 4;            // lanes along the columns, four columns each
-    constexpr int RG = 32 / CL;           // lanes along the rows
-    constexpr int NQ = K / 4 / RG;        // row quads of a lane: quads i * RG + rg
-    constexpr int COLS = CW * WARPS;      // columns of the CTA
-    constexpr int KV8 = K / 8;            // threads that stage one token's k and q
-    constexpr int TB = THREADS / KV8 < kTokens ? THREADS / KV8 : kTokens;
-    constexpr int NV = (TB * COLS / 8 + THREADS - 1) / THREADS;
-    static_assert(NQ >= 1 && NV == 1, "one vector of v a thread");
+// CW columns of one head's state in a warp: lane (rg, cl) holds CPL adjacent columns of every RG-th quad
+// of rows, the rows in pairs for the two-wide fp32 instructions.
+template <int K, int CW, int CPL>
+struct Tile {
+    static constexpr int CL = CW / CPL;        // lanes along the columns
+    static constexpr int RG = 32 / CL;         // lanes along the rows
+    static constexpr int NQ = K / 4 / RG;      // row quads of a lane
+    static_assert(NQ >= 1 && RG >= 1 && (CPL == 1 || CPL == 2 || CPL == 4), "a tile's shape");
+    pair_t S[NQ][2][CPL];
+    int lane, cl, rg;
 
-    __shared__ __align__(16) float ks[2][TB][K], qs[2][TB][K];
-    __shared__ __align__(16) float es[2][GATEK ? TB : 1][GATEK ? K : 4];   // exp(g), per channel
-    __shared__ __align__(16) float kr[2][GATEK ? TB : 1][GATEK ? K : 4];   // k as the read sees it
-    __shared__ __align__(16) float vs[2][TB][COLS];
-    __shared__ float4 sc[2][TB];   // exp(g), beta, q . k
+    __device__ __forceinline__ explicit Tile(int l) : lane(l), cl(l % CL), rg(l / CL) {}
+    __device__ __forceinline__ int row(int i) const { return 4 * (i * RG + rg); }   // first of quad i
+    __device__ __forceinline__ int col(int c) const { return CPL * cl + c; }        // this lane's c-th
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cl = lane % CL, rg = lane / CL;
-    const int tiles = p.V / COLS;
-    const int tile = blockIdx.x % tiles;
-    const int h = (blockIdx.x / tiles) % p.H;
-    const int s = blockIdx.x / (tiles * p.H);
-    const int c0 = tile * COLS + warp * CW + 4 * cl;   // this lane's columns c0 .. c0 + 3
-    const int hk = h / (p.H / p.Hqk);
-
-    const int slot_in = p.slots_in ? __ldg(p.slots_in + s) : -1;
-    int lo, n;
-    token_range(p, s, lo, n);
-    const int slot_out = p.slots_out && !p.per_token ? __ldg(p.slots_out + s) : -1;
-
-    // the state, on its way while the tokens and the checks are looked at
-    pair_t S[NQ][2][4];
-    const long long page = (long long)p.H * K * p.V;
-    const long long lane_off = (long long)h * K * p.V + c0;
-    const bool in_ok = slot_in < p.num_slots;
-    if (slot_in >= 0 && in_ok) {
-        const float* src = p.state + slot_in * page + lane_off;
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float* row = src + (long long)(4 * (i * RG + rg) + 2 * j) * p.V;
-                const float4 a = __ldcg(reinterpret_cast<const float4*>(row));
-                const float4 b = __ldcg(reinterpret_cast<const float4*>(row + p.V));
-                S[i][j][0] = pack(a.x, b.x);
-                S[i][j][1] = pack(a.y, b.y);
-                S[i][j][2] = pack(a.z, b.z);
-                S[i][j][3] = pack(a.w, b.w);
-            }
-        }
-    } else {
+    __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) S[i][j][c] = 0;
+                for (int c = 0; c < CPL; ++c) S[i][j][c] = 0;
     }
+    // base: row 0, this warp's column 0
+    __device__ __forceinline__ void load(const float* base, int V) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float a[CPL], b[CPL];
+                const float* at = base + (row(i) + 2 * j) * V + col(0);
+                if constexpr (CPL == 4) {
+                    const float4 x = __ldcs(reinterpret_cast<const float4*>(at));
+                    const float4 y = __ldcs(reinterpret_cast<const float4*>(at + V));
+                    a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
+                    b[0] = y.x, b[1] = y.y, b[2] = y.z, b[3] = y.w;
+                } else if constexpr (CPL == 2) {
+                    const float2 x = __ldcs(reinterpret_cast<const float2*>(at));
+                    const float2 y = __ldcs(reinterpret_cast<const float2*>(at + V));
+                    a[0] = x.x, a[1] = x.y;
+                    b[0] = y.x, b[1] = y.y;
+                } else {
+                    a[0] = __ldcs(at);
+                    b[0] = __ldcs(at + V);
+                }
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) S[i][j][c] = pack(a[c], b[c]);
+            }
+    }
+    __device__ __forceinline__ void store(float* base, int V) const {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float a[CPL], b[CPL];
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) unpack(S[i][j][c], a[c], b[c]);
+                float* at = base + (row(i) + 2 * j) * V + col(0);
+                if constexpr (CPL == 4) {
+                    __stcs(reinterpret_cast<float4*>(at), make_float4(a[0], a[1], a[2], a[3]));
+                    __stcs(reinterpret_cast<float4*>(at + V), make_float4(b[0], b[1], b[2], b[3]));
+                } else if constexpr (CPL == 2) {
+                    __stcs(reinterpret_cast<float2*>(at), make_float2(a[0], a[1]));
+                    __stcs(reinterpret_cast<float2*>(at + V), make_float2(b[0], b[1]));
+                } else {
+                    __stcs(at, a[0]);
+                    __stcs(at + V, b[0]);
+                }
+            }
+    }
+    // Sums over the lanes that hold the same columns: lane l ends with the whole sum of its column own().
+    __device__ __forceinline__ float join(const pair_t (&acc)[CPL]) const {
+        float d[CPL];
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) d[c] = total(acc[c]);
+        int off = 16;
+#pragma unroll
+        for (int n = CPL / 2; n >= 1; n /= 2) {   // each half of the lanes takes half of the columns
+            const bool up = lane & off;
+#pragma unroll
+            for (int c = 0; c < n; ++c) {
+                const float keep = up ? d[c + n] : d[c], send = up ? d[c] : d[c + n];
+                d[c] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+            }
+            off /= 2;
+        }
+        return rows_sum(d[0], off);
+    }
+    // (the lanes that hold the same own() column, from distance off on)
+    __device__ __forceinline__ float rows_sum(float x, int off) const {
+#pragma unroll
+        for (; off >= CL; off /= 2) x += __shfl_xor_sync(0xffffffffu, x, off);
+        return x;
+    }
+    __device__ __forceinline__ int own() const {
+        int c = 0, off = 16;
+#pragma unroll
+        for (int n = CPL / 2; n >= 1; n /= 2, off /= 2) c += lane & off ? n : 0;
+        return c;
+    }
+    // one lane for each column
+    __device__ __forceinline__ bool first() const { return (lane & (32 / CPL - 1) & ~(CL - 1)) == 0; }
+    // The other way: from each lane's value of its own() column to the values of all its columns, twice over.
+    __device__ __forceinline__ void spread(float mine, pair_t (&r)[CPL]) const {
+        float d[CPL];
+        d[0] = mine;
+        int off = 32 / CPL;
+#pragma unroll
+        for (int n = 1; n < CPL; n *= 2, off *= 2) {
+            const bool up = lane & off;
+#pragma unroll
+            for (int c = 0; c < n; ++c) {
+                const float other = __shfl_xor_sync(0xffffffffu, d[c], off);
+                d[c + n] = up ? d[c] : other;
+                d[c] = up ? other : d[c];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) r[c] = pack(d[c], d[c]);
+    }
+};
 
-    // staging: thread tid holds eight key channels of token tid / KV8's k and q, and eight
-    // columns of token tid / (COLS / 8)'s v
+struct Place {   // of a warp: sequence, head, first column, and where its states start
+    int s, h, col0, hk;
+    long long page, off;
+    __device__ __forceinline__ Place(const RecurrentParams& p, int K, int CW, int warp) {
+        const int COLS = CW * kWarps, tiles = p.V / COLS;
+        const int hs = blockIdx.x / tiles;
+        s = hs / p.H;
+        h = hs - s * p.H;
+        col0 = (blockIdx.x - hs * tiles) * COLS + warp * CW;
+        hk = h / (p.H / p.Hqk);
+        page = (long long)p.H * K * p.V;
+        off = (long long)h * K * p.V + col0;
+    }
+};
+
+__device__ __forceinline__ void store_o(const RecurrentParams& p, long long at, float o) {
+    if (p.out_bf16)
+        reinterpret_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(o);
+    else
+        reinterpret_cast<float*>(p.o)[at] = o;
+}
+
+// Whether another sequence names the slot that sequence s writes (every lane looks at some; the answer is the
+// warp's). Only where no claims were made.
+__device__ __forceinline__ bool named_by_others(const RecurrentParams& p, int s, int slot, int lane) {
+    bool shared = false;
+    for (int j = lane; j < p.nseq; j += 32)
+        shared |= j != s && (__ldg(p.slots_out + j) == slot || (p.slots_in && __ldg(p.slots_in + j) == slot));
+    return __any_sync(0xffffffffu, shared);
+}
+
+// What the checks say before anything is written: false when the call or the sequence is refused; `write`:
+// whether the final state may go to slot_out.
+__device__ __forceinline__ bool admitted(const RecurrentParams& p, const Place& at, int slot_in, int slot_out,
+                                         int lane, bool& write) {
+    const bool tell = lane == 0 && at.col0 == 0;   // one warp a head
+    write = slot_out >= 0 && slot_out < p.num_slots;
+    if (p.owner) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (__ldcg(p.cu_bad)) return false;
+        if (write && __ldcg(p.owner + slot_out) != at.s) {
+            write = false;
+            if (tell) report(p.err, kTagSlotShared);
+        }
+    } else {
+        if (p.cu) {
+            bool bad = lane == 0 && (__ldg(p.cu) != 0 || __ldg(p.cu + p.nseq) != p.T);
+            for (int j = lane; j < p.nseq; j += 32) bad |= __ldg(p.cu + j + 1) < __ldg(p.cu + j);
+            if (__any_sync(0xffffffffu, bad)) {
+                if (tell) report(p.err, kTagLengths);
+                return false;
+            }
+        }
+        if (write && p.nseq > 1 && named_by_others(p, at.s, slot_out, lane)) {
+            write = false;
+            if (tell) report(p.err, kTagSlotShared);
+        }
+    }
+    if (tell && (slot_in >= p.num_slots || slot_out >= p.num_slots)) report(p.err, kTagSlotRange);
+    return slot_in < p.num_slots;
+}
+
+// One token a sequence (p.T == 1, no cu_seqlens, states at the end).
+template <int K, int CW, int CPL, bool GATEK, bool BF>
+__global__ void __launch_bounds__(32 * kWarps, CW == 16 ? 4 : 1) decode_kernel(RecurrentParams p) {
+    using Cols = Tile<K, CW, CPL>;
+    constexpr int NQ = Cols::NQ;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Place at(p, K, CW, warp);
+    Cols tile(lane);
+
+    const int slot_in = p.slots_in ? __ldg(p.slots_in + at.s) : -1;
+    const int slot_out = p.slots_out ? __ldg(p.slots_out + at.s) : -1;
+    // the token's values that this lane needs, of its rows and of its own column
+    Raw4<BF> rk[NQ], rq[NQ], rg[NQ];
+    const long long kq = ((long long)at.s * p.Hqk + at.hk) * K, sh = (long long)at.s * p.H + at.h;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        rk[i].load(p.k, kq + tile.row(i));
+        rq[i].load(p.q, kq + tile.row(i));
+        if constexpr (GATEK) rg[i].load(p.g, sh * K + tile.row(i));
+    }
+    const long long oat = sh * p.V + at.col0 + tile.col(tile.own());
+    const float v = load1<BF>(p.v, oat), beta = load1<BF>(p.beta, sh);
+    const float g = GATEK ? 0.f : load1<BF>(p.g, sh);
+    if (slot_in >= 0 && slot_in < p.num_slots)
+        tile.load(p.state + slot_in * at.page + at.off, p.V);
+    else
+        tile.zero();
+    bool write;
+    if (!admitted(p, at, slot_in, slot_out, lane, write)) return;
+
+    const float e = expf(g);
+    pair_t k2[NQ][2], e2[NQ][2], ak[CPL] = {}, aq[CPL] = {}, qk2 = 0;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        pair_t q2[2];
+        rk[i].pairs(k2[i]);
+        rq[i].pairs(q2);
+        if constexpr (GATEK) {
+            pair_t g2[2];
+            rg[i].pairs(g2);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x, y;
+                unpack(g2[j], x, y);
+                e2[i][j] = pack(expf(x), expf(y));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            qk2 = fma2(q2[j], k2[i][j], qk2);
+            pair_t kr = k2[i][j], qr = q2[j];
+            if constexpr (GATEK) {
+                if (p.decay_first) kr = mul2(kr, e2[i][j]);
+                qr = mul2(qr, e2[i][j]);
+            }
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                ak[c] = fma2(tile.S[i][j][c], kr, ak[c]);
+                aq[c] = fma2(tile.S[i][j][c], qr, aq[c]);
+            }
+        }
+    }
+    const float qk = tile.rows_sum(total(qk2), 16);
+    const float sk = tile.join(ak), sq = tile.join(aq);
+    const float r = beta * (v - (!GATEK && p.decay_first ? e * sk : sk));
+    if (tile.first()) store_o(p, oat, fmaf(qk, r, e * sq));
+    if (!write) return;
+    pair_t r2[CPL];
+    tile.spread(r, r2);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int c = 0; c < CPL; ++c)
+                tile.S[i][j][c] = fma2(k2[i][j], r2[c], mul2(tile.S[i][j][c], GATEK ? e2[i][j] : pack(e, e)));
+    tile.store(p.state + slot_out * at.page + at.off, p.V);
+}
+
+// Which sequence the thread blocks with number `mine` among the sequences take: the mine-th longest (of equal
+// ones the lower first), so that the long ones start first and the short ones fill the gaps at the end.
+constexpr int kOrderSeqs = 256;
+__device__ __forceinline__ int ordered_sequence(const RecurrentParams& p, int mine) {
+    __shared__ __align__(16) int len[kOrderSeqs];
+    __shared__ int found;
+    const int t = threadIdx.x, n = p.nseq, up = (n + 3) & ~3;
+    for (int i = t; i < up; i += 32 * kWarps) 
+        len[i] = i < n ? (int)((unsigned)__ldg(p.cu + i + 1) - (unsigned)__ldg(p.cu + i)) : INT_MIN;
+    __syncthreads();
+    for (int i = t; i < n; i += 32 * kWarps) {
+        const int l = len[i];
+        int rank = 0;
+        for (int j = 0; j < up; j += 4) {
+            const int4 x = *reinterpret_cast<const int4*>(&len[j]);
+            rank += (x.x > l || (x.x == l && j < i)) + (x.y > l || (x.y == l && j + 1 < i)) +
+                    (x.z > l || (x.z == l && j + 2 < i)) + (x.w > l || (x.w == l && j + 3 < i));
+        }
+        if (rank == mine) found = i;
+    }
+    __syncthreads();
+    return found;
+}
+
+// Any number of tokens a sequence, kTokens of them staged in shared memory at a time while the next ones load.
+template <int K, int CW, int CPL, bool GATEK, bool BF>
+__global__ void __launch_bounds__(32 * kWarps, CW == 16 ? 4 : 1) tokens_kernel(RecurrentParams p) {
+    using Cols = Tile<K, CW, CPL>;
+    constexpr int NQ = Cols::NQ, C = kTokens;
+    constexpr int KV8 = K / 8;            // threads that stage one token's k and q, eight channels each
+    constexpr int COLS = CW * kWarps;
+    static_assert(C * KV8 <= 32 * kWarps && C * COLS / 8 <= 32 * kWarps, "one piece a thread");
+
+    __shared__ __align__(16) float ks[2][C][K], qs[2][C][K];               // qs: E q for gates per channel
+    __shared__ __align__(16) float es[2][GATEK ? C : 1][GATEK ? K : 4];    // exp(g), per channel
+    __shared__ __align__(16) float kr[2][GATEK ? C : 1][GATEK ? K : 4];    // k as the read sees it
+    __shared__ __align__(16) float vs[2][C][COLS];
+    __shared__ float4 sc[2][C];   // exp(g), beta, q . k
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Place at(p, K, CW, warp);
+    if (p.ordered) at.s = ordered_sequence(p, at.s);
+    Cols tile(lane);
+
+    const int slot_in = p.slots_in ? __ldg(p.slots_in + at.s) : -1;
+    int lo, n;
+    token_range(p, at.s, lo, n);
+    const int slot_out = p.slots_out && !p.per_token ? __ldg(p.slots_out + at.s) : -1;
+    if (slot_in >= 0 && slot_in < p.num_slots)
+        tile.load(p.state + slot_in * at.page + at.off, p.V);
+    else
+        tile.zero();
+
+    // staging: thread tid brings eight key channels of token st's k, q (and gates) and eight columns of
+    // token vt's v
     const int st = tid / KV8, sk = 8 * (tid % KV8);
     const int vt = tid / (COLS / 8), vc = 8 * (tid % (COLS / 8));
-    Raw8<BF> rk, rq, rv, rgk;
+    Raw8<BF> rk, rq, rv, rg;
     float raw_g = 0.f, raw_b = 0.f;
     auto load_tokens = [&](int t0) {
-        rk.zero();
-        rq.zero();
-        if (st < TB && t0 + st < n) {
+        if (st < C && t0 + st < n) {
             const long long tok = lo + t0 + st;
-            const long long at = (tok * p.Hqk + hk) * K + sk;
-            rk.load(p.k, at);
-            rq.load(p.q, at);
-            if constexpr (GATEK) rgk.load(p.g, (tok * p.H + h) * K + sk);
-        } else if constexpr (GATEK) {
-            rgk.zero();
+            const long long a = (tok * p.Hqk + at.hk) * K + sk;
+            rk.load(p.k, a);
+            rq.load(p.q, a);
+            if constexpr (GATEK) rg.load(p.g, (tok * p.H + at.h) * K + sk);
         }
-        if (vt < TB && t0 + vt < n) rv.load(p.v, ((long long)(lo + t0 + vt) * p.H + h) * p.V + tile * COLS + vc);
-        if (tid < TB && t0 + tid < n) {
-            const long long at = (long long)(lo + t0 + tid) * p.H + h;
-            raw_b = load1<BF>(p.beta, at);
-            if constexpr (!GATEK) raw_g = load1<BF>(p.g, at);
+        if (vt < C && t0 + vt < n)
+            rv.load(p.v, ((long long)(lo + t0 + vt) * p.H + at.h) * p.V + (at.col0 - warp * CW) + vc);
+        if (tid < C && t0 + tid < n) {
+            const long long a = (long long)(lo + t0 + tid) * p.H + at.h;
+            raw_b = load1<BF>(p.beta, a);
+            if constexpr (!GATEK) raw_g = load1<BF>(p.g, a);
         }
     };
     auto store_tokens = [&](int b) {
@@ -289,11 +576,11 @@ __global__ void __launch_bounds__(32 * WARPS) recurrent_kernel(RecurrentParams p
         for (int i = 0; i < 8; ++i) qk = fmaf(fq[i], fk[i], qk);
 #pragma unroll
         for (int off = KV8 / 2; off > 0; off >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, off);
-        if (st < TB) {
+        if (st < C) {
             put8(&ks[b][st][sk], fk);
             if constexpr (GATEK) {
                 float e[8];
-                rgk.values(e);
+                rg.values(e);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     e[i] = expf(e[i]);
@@ -306,174 +593,112 @@ __global__ void __launch_bounds__(32 * WARPS) recurrent_kernel(RecurrentParams p
             put8(&qs[b][st][sk], fq);
             if (sk == 0) sc[b][st].z = qk;
         }
-        if (vt < TB) {
+        if (vt < C) {
             float f[8];
             rv.values(f);
             put8(&vs[b][vt][vc], f);
         }
-        if (tid < TB) {
+        if (tid < C) {
             sc[b][tid].x = expf(raw_g);
             sc[b][tid].y = raw_b;
         }
     };
+    rk.zero();
+    rq.zero();
+    rv.zero();
+    rg.zero();
     if (n > 0) load_tokens(0);
 
-    // nothing is written before the lengths and the slots are known to be good
-    bool write_state = slot_out >= 0 && slot_out < p.num_slots;
-    if (p.owner) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (__ldcg(p.cu_bad)) return;
-        if (write_state && __ldcg(p.owner + slot_out) != s) {
-            write_state = false;
-            if (tid == 0) report(p.err, kTagSlotShared);
-        }
-    } else {
-        if (p.cu) {
-            bool bad = tid == 0 && (__ldg(p.cu) != 0 || __ldg(p.cu + p.nseq) != p.T);
-            for (int j = tid; j < p.nseq; j += THREADS) bad |= __ldg(p.cu + j + 1) < __ldg(p.cu + j);
-            if (__syncthreads_or(bad)) {
-                if (tid == 0) report(p.err, kTagLengths);
-                return;
-            }
-        }
-        if (write_state && p.nseq > 1) {
-            bool shared = false;
-            for (int j = tid; j < p.nseq; j += THREADS)
-                shared |= j != s && (__ldg(p.slots_out + j) == slot_out ||
-                                     (p.slots_in && __ldg(p.slots_in + j) == slot_out));
-            if (__syncthreads_or(shared)) {
-                write_state = false;
-                if (tid == 0) report(p.err, kTagSlotShared);
-            }
-        }
-    }
-    if (tid == 0 && (!in_ok || slot_out >= p.num_slots)) report(p.err, kTagSlotRange);
-    if (!in_ok) return;
+    bool write;
+    // (every warp of the block comes to the same verdict on the call and the sequence)
+    if (!admitted(p, at, slot_in, slot_out, lane, write)) return;
 
-    auto store_state = [&](int slot) {
-        float* dst = p.state + slot * page + lane_off;
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float* row = dst + (long long)(4 * (i * RG + rg) + 2 * j) * p.V;
-                float4 a, b;
-                unpack(S[i][j][0], a.x, b.x);
-                unpack(S[i][j][1], a.y, b.y);
-                unpack(S[i][j][2], a.z, b.z);
-                unpack(S[i][j][3], a.w, b.w);
-                *reinterpret_cast<float4*>(row) = a;
-                *reinterpret_cast<float4*>(row + p.V) = b;
-            }
-        }
-    };
-
-    const bool up16 = lane & 16, up8 = lane & 8;
-    const int oc = (up16 ? 2 : 0) + (up8 ? 1 : 0);   // this lane's column once the sums are joined
-    const bool writes_o = (lane & 7 & ~(CL - 1)) == 0;
-    for (int t0 = 0, b = 0; t0 < n; t0 += TB, b ^= 1) {
+    const int oc = tile.col(tile.own());   // this lane's column once sums are joined
+    const bool first = tile.first();
+    const long long ostep = (long long)p.H * p.V;
+    long long oat = ((long long)lo * p.H + at.h) * p.V + at.col0 + oc;
+    for (int t0 = 0, b = 0; t0 < n; t0 += C, b ^= 1) {
         // (buffer b was last read before the barrier of the block in between)
         store_tokens(b);
         __syncthreads();
-        if (t0 + TB < n) load_tokens(t0 + TB);
-        const int m = min(TB, n - t0);
+        if (t0 + C < n) load_tokens(t0 + C);
+        const int m = min(C, n - t0);
+#pragma unroll 1
         for (int t = 0; t < m; ++t) {
-            // the sums over the rows: of this lane's, then of the lanes that hold the same columns
-            pair_t ak[4] = {0, 0, 0, 0}, aq[4] = {0, 0, 0, 0};
+            const float4 g4 = sc[b][t];   // exp(g), beta, q . k
+            const float vt_ = vs[b][t][warp * CW + oc];
+            pair_t ak[CPL] = {}, aq[CPL] = {};
             const float* kread = GATEK ? kr[b][t] : ks[b][t];
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
-                const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(kread + 4 * (i * RG + rg));
-                const ulonglong2 q2 = *reinterpret_cast<const ulonglong2*>(&qs[b][t][4 * (i * RG + rg)]);
+                const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(kread + tile.row(i));
+                const ulonglong2 q2 = *reinterpret_cast<const ulonglong2*>(&qs[b][t][tile.row(i)]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    ak[c] = fma2(S[i][0][c], k2.x, ak[c]);
-                    aq[c] = fma2(S[i][0][c], q2.x, aq[c]);
+                for (int c = 0; c < CPL; ++c) {
+                    ak[c] = fma2(tile.S[i][0][c], k2.x, ak[c]);
+                    aq[c] = fma2(tile.S[i][0][c], q2.x, aq[c]);
                 }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    ak[c] = fma2(S[i][1][c], k2.y, ak[c]);
-                    aq[c] = fma2(S[i][1][c], q2.y, aq[c]);
+                for (int c = 0; c < CPL; ++c) {
+                    ak[c] = fma2(tile.S[i][1][c], k2.y, ak[c]);
+                    aq[c] = fma2(tile.S[i][1][c], q2.y, aq[c]);
                 }
             }
-            float dk[4], dq[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                dk[c] = total(ak[c]);
-                dq[c] = total(aq[c]);
-            }
-            auto join = [&](const float (&d)[4]) {   // lane l ends with its column oc's whole sum
-                float x = up16 ? d[2] : d[0], y = up16 ? d[3] : d[1];
-                x += __shfl_xor_sync(0xffffffffu, up16 ? d[0] : d[2], 16);
-                y += __shfl_xor_sync(0xffffffffu, up16 ? d[1] : d[3], 16);
-                float z = up8 ? y : x;
-                z += __shfl_xor_sync(0xffffffffu, up8 ? x : y, 8);
-#pragma unroll
-                for (int off = 4; off >= CL; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-                return z;
-            };
-            const float sk_ = join(dk), sq_ = join(dq);
-            const float4 g4 = sc[b][t];   // exp(g), beta, q . k
+            const float sk_ = tile.join(ak), sq_ = tile.join(aq);
             const float e = GATEK ? 1.f : g4.x;
-            const float read = !GATEK && p.decay_first ? e * sk_ : sk_;
-            const float r = g4.y * (vs[b][t][warp * CW + 4 * cl + oc] - read);
-            if (writes_o) {
-                const long long at = ((long long)(lo + t0 + t) * p.H + h) * p.V + c0 + oc;
-                const float o = fmaf(g4.z, r, e * sq_);
-                if (p.out_bf16)
-                    reinterpret_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(o);
-                else
-                    reinterpret_cast<float*>(p.o)[at] = o;
-            }
-            // r of all four columns, then the update
-            const float ro = __shfl_xor_sync(0xffffffffu, r, 8);
-            const float x = up8 ? ro : r, y = up8 ? r : ro;
-            const float xo = __shfl_xor_sync(0xffffffffu, x, 16), yo = __shfl_xor_sync(0xffffffffu, y, 16);
-            const float rc[4] = {up16 ? xo : x, up16 ? yo : y, up16 ? x : xo, up16 ? y : yo};
-            pair_t r2[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) r2[c] = pack(rc[c], rc[c]);
+            const float r = g4.y * (vt_ - (!GATEK && p.decay_first ? e * sk_ : sk_));
+            if (first) store_o(p, oat, fmaf(g4.z, r, e * sq_));
+            oat += ostep;
+            pair_t r2[CPL];
+            tile.spread(r, r2);
             const pair_t e2 = pack(e, e);
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
-                const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&ks[b][t][4 * (i * RG + rg)]);
+                const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&ks[b][t][tile.row(i)]);
                 pair_t ex = e2, ey = e2;
                 if constexpr (GATEK) {
-                    const ulonglong2 ek = *reinterpret_cast<const ulonglong2*>(&es[b][t][4 * (i * RG + rg)]);
+                    const ulonglong2 ek = *reinterpret_cast<const ulonglong2*>(&es[b][t][tile.row(i)]);
                     ex = ek.x;
                     ey = ek.y;
                 }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    S[i][0][c] = fma2(k2.x, r2[c], mul2(S[i][0][c], ex));
-                    S[i][1][c] = fma2(k2.y, r2[c], mul2(S[i][1][c], ey));
+                for (int c = 0; c < CPL; ++c) {
+                    tile.S[i][0][c] = fma2(k2.x, r2[c], mul2(tile.S[i][0][c], ex));
+                    tile.S[i][1][c] = fma2(k2.y, r2[c], mul2(tile.S[i][1][c], ey));
                 }
             }
             if (p.per_token && p.slots_out) {
                 const int slot = __ldg(p.slots_out + lo + t0 + t);
                 if (slot >= p.num_slots) {
-                    if (tid == 0) report(p.err, kTagSlotRange);
+                    if (lane == 0) report(p.err, kTagSlotRange);
                 } else if (slot >= 0) {
-                    if (!p.owner || __ldcg(p.owner + slot) == s)
-                        store_state(slot);
-                    else if (tid == 0)
+                    if (!p.owner || __ldcg(p.owner + slot) == at.s)
+                        tile.store(p.state + slot * at.page + at.off, p.V);
+                    else if (lane == 0)
                         report(p.err, kTagSlotShared);
                 }
             }
         }
     }
-    if (write_state) store_state(slot_out);
+    if (write) tile.store(p.state + slot_out * at.page + at.off, p.V);
 }
 
-template <int K, int CW, int WARPS>
+template <int K, int CW, int CPL, bool ONE>
 cudaError_t launch(const RecurrentParams& p, bool gate_k, bool bf16, cudaStream_t s) {
-    const void* fn = gate_k ? (bf16 ? (const void*)recurrent_kernel<K, CW, WARPS, true, true>
-                                    : (const void*)recurrent_kernel<K, CW, WARPS, true, false>)
-                            : (bf16 ? (const void*)recurrent_kernel<K, CW, WARPS, false, true>
-                                    : (const void*)recurrent_kernel<K, CW, WARPS, false, false>);
+    const void* fn;
+    if constexpr (ONE)
+        fn = gate_k ? (bf16 ? (const void*)decode_kernel<K, CW, CPL, true, true>
+                            : (const void*)decode_kernel<K, CW, CPL, true, false>)
+                    : (bf16 ? (const void*)decode_kernel<K, CW, CPL, false, true>
+                            : (const void*)decode_kernel<K, CW, CPL, false, false>);
+    else
+        fn = gate_k ? (bf16 ? (const void*)tokens_kernel<K, CW, CPL, true, true>
+                            : (const void*)tokens_kernel<K, CW, CPL, true, false>)
+                    : (bf16 ? (const void*)tokens_kernel<K, CW, CPL, false, true>
+                            : (const void*)tokens_kernel<K, CW, CPL, false, false>);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((long long)p.nseq * p.H * (p.V / (CW * WARPS))));
-    cfg.blockDim = dim3(32 * WARPS);
+    cfg.gridDim = dim3((unsigned)((long long)p.nseq * p.H * (p.V / (CW * kWarps))));
+    cfg.blockDim = dim3(32 * kWarps);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -485,13 +710,18 @@ cudaError_t launch(const RecurrentParams& p, bool gate_k, bool bf16, cudaStream_
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// The split. One token a sequence: 16 columns a warp always (half a warp's 64 B of a row; at 8 columns the
+// same time up to four sequences of 32 heads, more beyond: 49.7 against 59.9 us at 64 of them). More
+// tokens: 16 columns a warp, four of them a lane, when that fills the SMs with twelve warps each; below that
+// 8 columns, one a lane, where a token's sums cross fewer lanes: 18.9 against 25.1 us for two sequences of
+// 8 heads and up to 63 tokens, 51.7 against 47.6 us for 16 of 16 heads, 187 against 115 for 32 of 32 (K = V = 128).
+constexpr int kWideWarpsPerSm = 12;
 template <int K>
 cudaError_t launch_k(const RecurrentParams& p, bool gate_k, bool bf16, int sms, cudaStream_t s) {
-    const long long warps = (long long)p.nseq * p.H * (p.V / 32);
-    if (warps >= 8LL * sms)
-        return p.V == 64 ? launch<K, 32, 2>(p, gate_k, bf16, s) : launch<K, 32, 4>(p, gate_k, bf16, s);
-    if (warps >= 4LL * sms) return launch<K, 16, 4>(p, gate_k, bf16, s);
-    return launch<K, 8, 4>(p, gate_k, bf16, s);
+    if (p.T == 1 && !p.cu && !p.per_token) return launch<K, 16, 4, true>(p, gate_k, bf16, s);
+    const long long warps = (long long)p.nseq * p.H * (p.V / 16);
+    return warps >= (long long)kWideWarpsPerSm * sms ? launch<K, 16, 4, false>(p, gate_k, bf16, s)
+                                                     : launch<K, 8, 1, false>(p, gate_k, bf16, s);
 }
 
 // Each block of the rule looks for other sequences that name its slot when there are at most this many
@@ -566,6 +796,7 @@ gdn_status gdn_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, const int*
     c.out_bf16 = p->out_dtype == GDN_DTYPE_BF16;
     c.decay_first = p->decay_first;
     c.per_token = per_token;
+    c.ordered = cu_seqlens && nseq <= kOrderSeqs && nseq > 1;
     if (nseq > kInlineSeqs || (per_token && nseq > 1)) {
         int* owner = reinterpret_cast<int*>(ws + kWsHeader);
         int* cu_bad = reinterpret_cast<int*>(ws + kWsVerdict);

@@ -352,23 +352,21 @@ def gdn_chunk_bwd_timed(q, k, v, g, beta, h0, dO, dht, dq, dk, dv, dg, dbeta, dh
                                      _stream(stream), arr), "gdn_chunk_bwd_timed")
 
 
-def _on_device(**tensors):
+def _on_device(*tensors):
     """Raises ValueError unless every tensor (or None) lies contiguous on the current CUDA device:
     the library takes plain pointers and launches on that device."""
     import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} is not contiguous")
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    for i, t in enumerate(tensors):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            if t.get_device() != dev:
+                raise ValueError(f"tensor argument {i} is on {t.device}, not on the current CUDA device")
+            raise ValueError(f"tensor argument {i} is not contiguous")
 
 
 def _is(name, t, dtype, shape):
     """Raises ValueError unless t (or None) has this dtype and shape."""
-    if t is not None and (t.dtype != dtype or t.shape != shape):
+    if t is not None and (t.dtype is not dtype or t.shape != shape):
         raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, not {dtype} {tuple(shape)}")
 
 
@@ -392,8 +390,7 @@ def gdn_recurrent_fwd(q, k, v, g, beta, state, slots_in, slots_out, o, workspace
     B, T, H, V = v.shape
     Hqk, K = k.shape[2], k.shape[3]
     nseq = B if cu_seqlens is None else int(cu_seqlens.numel()) - 1
-    _on_device(q=q, k=k, v=v, g=g, beta=beta, state=state, slots_in=slots_in, slots_out=slots_out,
-               o=o, workspace=workspace, cu_seqlens=cu_seqlens)
+    _on_device(q, k, v, g, beta, state, slots_in, slots_out, o, workspace, cu_seqlens)
     gate_k = g.dim() == 4
     _is("q", q, k.dtype, (B, T, Hqk, K))
     _is("k", k, k.dtype, (B, T, Hqk, K))
@@ -450,7 +447,7 @@ def _room(workspace):
 def gdn_cache_copy(pages, src, dst, workspace, stream=None):
     """pages [layers, num_pages, ...]: page dst[i] := page src[i] in every layer (zeros for a
     negative src, nothing for a negative dst); src, dst int32 GPU tensors."""
-    _on_device(pages=pages, src=src, dst=dst, workspace=workspace)
+    _on_device(pages, src, dst, workspace)
     _indexes(src=src, dst=dst)
     if src.numel() != dst.numel():
         raise ValueError("src and dst differ in length")
@@ -462,7 +459,7 @@ def gdn_cache_fork(pages, refs, parents, children, workspace, share=False, strea
     """A copy of page parents[i] (zeros for a negative one) in the next of the lowest-numbered free
     pages (refs 0), its number in children[i] (-1: refused); share: the parent gains a user
     instead. refs, parents, children int32 GPU tensors."""
-    _on_device(pages=pages, refs=refs, parents=parents, children=children, workspace=workspace)
+    _on_device(pages, refs, parents, children, workspace)
     _indexes(refs=refs, parents=parents, children=children)
     if parents.numel() != children.numel() or refs.numel() != pages.shape[1]:
         raise ValueError("one child a parent and one count a page are wanted")
@@ -473,7 +470,7 @@ def gdn_cache_fork(pages, refs, parents, children, workspace, share=False, strea
 
 def gdn_cache_free(refs, pages, workspace, stream=None):
     """One user less of every page named in `pages` (int32; negative entries are skipped)."""
-    _on_device(refs=refs, pages=pages, workspace=workspace)
+    _on_device(refs, pages, workspace)
     _indexes(refs=refs, pages=pages)
     _check(lib().gdn_cache_free(refs.numel(), _ptr(refs), pages.numel(), _ptr(pages),
                                 *_room(workspace), _stream(stream)), "gdn_cache_free")
@@ -483,7 +480,7 @@ def gdn_cache_compact(pages, refs, table, remap, live, workspace, stream=None):
     """The pages in use move to the front of the cache; table (or None) is rewritten to the new
     numbers, remap [num_pages] (or None) and live [1] (or None) receive every page's new number
     and how many are in use."""
-    _on_device(pages=pages, refs=refs, table=table, remap=remap, live=live, workspace=workspace)
+    _on_device(pages, refs, table, remap, live, workspace)
     _indexes(refs=refs, table=table, remap=remap, live=live)
     num = pages.shape[1]
     if refs.numel() != num or (remap is not None and remap.numel() != num) or (
@@ -508,7 +505,7 @@ def _rows(x, y_like, params, **rest):
 def gdn_norm_fwd(x, w, b, z, y, eps=1e-6, rms=True, stream=None):
     """y = ((x - m) s w + b) z sigmoid(z) row by row: x, z, y [..., N], w, b [N] fp32 (w, b, z may
     be None); rms: the root-mean-square norm (m = 0), else the layer norm. z has y's type."""
-    _on_device(x=x, w=w, b=b, z=z, y=y)
+    _on_device(x, w, b, z, y)
     rows, N = _rows(x, y, dict(w=w, b=b), z=z, y=y)
     _check(lib().gdn_norm_fwd(rows, N, _dtype_code(x), _dtype_code(y), int(rms), eps, _ptr(x), _ptr(w),
                               _ptr(b), _ptr(z), _ptr(y), _stream(stream)), "gdn_norm_fwd")
@@ -526,7 +523,7 @@ def alloc_norm_bwd_workspace(rows: int, N: int, device="cuda"):
 def gdn_norm_bwd(x, w, b, z, dy, dx, dz, dw, db, workspace, eps=1e-6, rms=True, stream=None):
     """Gradients of gdn_norm_fwd for dy (z's and y's type): dx (x's type), dz (None skips it), dw, db
     [N] fp32 (None skips either)."""
-    _on_device(x=x, w=w, b=b, z=z, dy=dy, dx=dx, dz=dz, dw=dw, db=db, workspace=workspace)
+    _on_device(x, w, b, z, dy, dx, dz, dw, db, workspace)
     rows, N = _rows(x, dy, dict(w=w, b=b, dw=dw, db=db), z=z, dy=dy, dz=dz)
     _is("dx", dx, x.dtype, x.shape)
     _check(lib().gdn_norm_bwd(rows, N, _dtype_code(x), _dtype_code(dy), int(rms), eps, _ptr(x), _ptr(w),

@@ -268,19 +268,26 @@ def test_bad_lengths_write_nothing(cu, claims):
 
 
 def test_token_by_token_equals_one_call():
-    # one call over 20 tokens, and 20 calls of one token in place: the same arithmetic, bit for bit
+    # one call over 20 tokens (in blocks of eight), and 20 calls of one token in place. The two round in
+    # another order; each lies within TOL_F32 of the same 64-bit values (the arithmetic at the top), so
+    # they lie within twice that of one another.
     d = make([20] * 3, 4, 2, 128, 128)
     slots = d["order"][:3]
     whole, err = call(d, slots, slots)
     assert err == (0, 0)
     state, ws = d["state"].clone(), gdn.alloc_recurrent_workspace(d["state"].shape[0])
-    o = torch.empty_like(d["o"][:, :1])
+    o = torch.empty_like(d["o"])
     for t in range(20):
         part = {n: d[n][:, t:t + 1].contiguous() for n in ("q", "k", "v", "g", "beta")}
-        part.update(o=o, cu=None, state=d["state"])
+        part.update(o=torch.empty_like(o[:, :1]), cu=None, state=d["state"])
         call(part, slots, slots, ws=ws, state=state)
-        assert torch.equal(o, d["o"][:, t:t + 1]), t
-    assert torch.equal(state, whole)
+        o[:, t:t + 1] = part["o"]
+    assert rel_err(np64(o), np64(d["o"])) <= 2 * TOL_F32
+    assert rel_err(np64(state[slots]), np64(whole[slots])) <= 2 * TOL_F32
+    o_ref, ref = reference(d, slots, slots)
+    check_state(d, state, ref, slots)
+    d["o"] = o
+    check_o(d, o_ref)
 
 
 def test_decay_of_zero_and_poisoned_slots():
