@@ -141,8 +141,8 @@ def _ptr(t):
 
 def _stream(stream):
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the current stream's handle, without a stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -387,17 +387,19 @@ def gdn_recurrent_fwd(q, k, v, g, beta, state, slots_in, slots_out, o, workspace
     sequences. slots_in, slots_out: int32 GPU tensors (or None), one entry a sequence; with
     per_token slots_out has one entry a token. Negative entries: a zero state, not written."""
     import torch
-    B, T, H, V = v.shape
-    Hqk, K = k.shape[2], k.shape[3]
-    nseq = B if cu_seqlens is None else int(cu_seqlens.numel()) - 1
+    vshape, kshape, dt = v.shape, k.shape, k.dtype
+    B, T, H, V = vshape
+    _, _, Hqk, K = kshape
+    nseq = B if cu_seqlens is None else cu_seqlens.numel() - 1
     _on_device(q, k, v, g, beta, state, slots_in, slots_out, o, workspace, cu_seqlens)
     gate_k = g.dim() == 4
-    _is("q", q, k.dtype, (B, T, Hqk, K))
-    _is("k", k, k.dtype, (B, T, Hqk, K))
-    _is("v", v, k.dtype, v.shape)
-    _is("g", g, k.dtype, (B, T, H, K) if gate_k else (B, T, H))
-    _is("beta", beta, k.dtype, (B, T, H))
-    _is("o", o, o.dtype, v.shape)
+    gshape = (B, T, H, K) if gate_k else (B, T, H)
+    _is("q", q, dt, (B, T, Hqk, K))
+    _is("k", k, dt, (B, T, Hqk, K))
+    _is("v", v, dt, vshape)
+    _is("g", g, dt, gshape)
+    _is("beta", beta, dt, gshape[:3])
+    _is("o", o, o.dtype, vshape)
     slots = 0
     if state is not None:
         slots = state.shape[0]
@@ -406,12 +408,11 @@ def gdn_recurrent_fwd(q, k, v, g, beta, state, slots_in, slots_out, o, workspace
     _is("slots_out", slots_out, torch.int32, (B * T if per_token else nseq,))
     if cu_seqlens is not None:
         _is("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,))
-    prob = Problem(B, T, H, K, V, 64, _dtype_code(k), _dtype_code(o), int(decay_first), int(gate_k))
-    _check(lib().gdn_recurrent_fwd(ctypes.byref(prob), Hqk, nseq, _ptr(cu_seqlens), _ptr(q), _ptr(k),
-                                   _ptr(v), _ptr(g), _ptr(beta), _ptr(state), slots, _ptr(slots_in),
-                                   _ptr(slots_out), int(per_token), _ptr(o), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)),
-           "gdn_recurrent_fwd")
+    prob = Problem(B, T, H, K, V, 64, _dtype_code(k), _dtype_code(o), decay_first, gate_k)
+    _check(lib().gdn_recurrent_fwd(ctypes.byref(prob), Hqk, nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(),
+                                   v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state), slots,
+                                   _ptr(slots_in), _ptr(slots_out), per_token, o.data_ptr(), *_room(workspace),
+                                   _stream(stream)), "gdn_recurrent_fwd")
 
 
 def alloc_cache_workspace(num_pages: int, n: int = 0, device="cuda"):
