@@ -3,10 +3,10 @@
 //
 // A row x of N values (a head's output, or a hidden state): m its mean (0 for the root-mean-square
 // norm), s = 1 / sqrt(mean((x - m)^2) + eps), y = ((x - m) s w + b) z sigmoid(z). One pass over memory:
-// a row sits in its group's registers while its sums are formed (the squares after the mean, so
-// nothing cancels), and the next row is on its way meanwhile.
+// a row sits in its group's registers while its sums are formed, and the next row is on its way meanwhile.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "gdn_norm.cuh"
 
@@ -14,146 +14,130 @@ namespace gdn {
 namespace norm {
 namespace {
 
-constexpr int kFwdThreadsPerSm = 2048;
+// GB: threads of a row's block; 0: rows of at most 512 values, several to a block of 256 threads
+template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
+struct Fwd {
+    using Rows = std::conditional_t<GATED, Ring<VEC, R, XB, YB>, Ring<VEC, R, XB>>;
+};
 
-template <bool BLOCK, bool VEC, bool XB, bool YB, bool GATED>
-__global__ void __launch_bounds__(BLOCK ? kMaxThreads : 256) fwd_kernel(Params p) {
-    __shared__ float part[2][3][32];
+template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
+__global__ void __launch_bounds__(GB ? GB : 256) fwd_kernel(Params p) {
+    using Rows = typename Fwd<GB, R, VEC, XB, YB, GATED>::Rows;
+    extern __shared__ __align__(16) char stages[];
+    __shared__ float part[2][64];
     int half = 0;
-    const int G = BLOCK ? blockDim.x : p.g;
+    const int G = GB ? GB : p.g;
     const int t = threadIdx.x % G;
-    const int per_warp = BLOCK ? 1 : 32 / G;              // rows a warp holds at once
-    const int sub = BLOCK ? 0 : (threadIdx.x & 31) / G;   // which of them is this thread's
-    const int c = first_col<VEC>(0, t, G), step = col_step<VEC>(G);
-    const long long stride = (long long)gridDim.x * (blockDim.x / G);
+    const int rows_block = GB ? 1 : 256 / G;              // rows a block holds at once, and a warp
+    const int rows_warp = GB ? 1 : 32 / G;
+    const int sub = GB ? 0 : (threadIdx.x & 31) / G;      // which of the warp's is this thread's
+    const int step = col_step<VEC>(G);
+    const long long stride = (long long)gridDim.x * rows_block;
     // (the trip count is the same for all threads of a warp, and of a block where that holds one row)
-    long long row0 = (long long)blockIdx.x * (blockDim.x / G) + (BLOCK ? 0 : (threadIdx.x >> 5) * per_warp);
+    long long row0 = (long long)blockIdx.x * rows_block + (GB ? 0 : (threadIdx.x >> 5) * rows_warp);
 
-    float w[8], b[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int col = c + e * step;
-        w[e] = p.w && col < p.N ? __ldg(p.w + col) : 1.f;
-        b[e] = p.b && col < p.N ? __ldg(p.b + col) : 0.f;
-    }
-    Eight<XB, VEC> nx;
-    Eight<YB, VEC> nz;
-    auto fetch = [&](long long row) {
-        const int n = row < p.rows ? p.N : 0;
-        nx.load(p.x, row * p.N, c, step, n);
-        if constexpr (GATED) nz.load(p.z, row * p.N, c, step, n);
+    const Rows ring{(unsigned)__cvta_generic_to_shared(stages), G, t, (int)threadIdx.x, GB ? GB : 256, p.N, p.rows};
+    auto fetch = [&](int stage, long long row) {
+        ring.template fetch<0>(stage, p.x, row);
+        if constexpr (GATED) ring.template fetch<1>(stage, p.z, row);
+        Rows::commit();
     };
-    fetch(row0 + sub);
-    for (; row0 < p.rows; row0 += stride) {
-        const long long row = row0 + sub;
-        float x[8], z[8];
-        nx.values(x);
-        if constexpr (GATED) nz.values(z);
-        fetch(row + stride);
-        if (!p.rms) {
-            float s[1] = {0.f};
+#pragma unroll 1
+    for (int k = 0; k < Rows::kAhead; ++k) fetch(k, row0 + sub + k * stride);
+    pair_t w[R][4], b[R][4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] += x[e];
-            group_sum<BLOCK>(s, G, part, half);
-            const float mean = s[0] * p.inv_n;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = c + e * step < p.N ? x[e] - mean : 0.f;
-        }
-        float q[1] = {0.f};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[0] = fmaf(x[e], x[e], q[0]);
-        group_sum<BLOCK>(q, G, part, half);
-        const float rstd = rsqrtf(fmaf(q[0], p.inv_n, p.eps));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = fmaf(x[e] * rstd, w[e], b[e]);
-            if constexpr (GATED) x[e] *= z[e] * sigmoid(z[e]);
-        }
-        Eight<YB, VEC>::store(p.y, row * p.N, c, step, row < p.rows ? p.N : 0, x);
+    for (int i = 0; i < R; ++i) {
+        parameter<VEC>(w[i], p.w, first_col<VEC>(i, t, G), step, p.N, 1.f);
+        parameter<VEC>(b[i], p.b, first_col<VEC>(i, t, G), step, p.N, 0.f);
     }
-}
-
-// Rows of more than 4096 values, one a block: the weights come from the cache, as holding them as well would
-// take the registers of the row.
-template <int R, bool VEC, bool XB, bool YB, bool GATED>
-__global__ void __launch_bounds__(kMaxThreads) wide_fwd_kernel(Params p) {
-    __shared__ float part[2][3][32];
-    int half = 0;
-    const int G = kMaxThreads, t = threadIdx.x, step = col_step<VEC>(G);
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        Eight<XB, VEC> rx[R];
-        Eight<YB, VEC> rz[R];
+    for (int stage = 0; row0 < p.rows; row0 += stride, stage = stage == Rows::kAhead ? 0 : stage + 1) {
+        const long long row = row0 + sub;
+        Rows::template wait<GB>();
+        fetch(stage == 0 ? Rows::kAhead : stage - 1, row + Rows::kAhead * stride);
+        pair_t x[R][4], sq = 0, sx = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            rx[i].load(p.x, row * p.N, first_col<VEC>(i, t, G), step, p.N);
-            if constexpr (GATED) rz[i].load(p.z, row * p.N, first_col<VEC>(i, t, G), step, p.N);
-        }
-        float mean = 0.f;
-        if (!p.rms) {
-            float s[1] = {0.f};
+            ring.template read<0>(stage, i, row, x[i]);
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                float x[8];
-                rx[i].values(x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[0] += x[e];
-            }
-            group_sum<true>(s, G, part, half);
-            mean = s[0] * p.inv_n;
-        }
-        float q[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            float x[8];
-            rx[i].values(x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float xm = first_col<VEC>(i, t, G) + e * step < p.N ? x[e] - mean : 0.f;
-                q[0] = fmaf(xm, xm, q[0]);
+            for (int k = 0; k < 4; ++k) {
+                sq = fma2(x[i][k], x[i][k], sq);
+                sx = add2(sx, x[i][k]);
             }
         }
-        group_sum<true>(q, G, part, half);
-        const float rstd = rsqrtf(fmaf(q[0], p.inv_n, p.eps));
+        float mean = 0.f, var;
+        if (p.rms) {
+            float q[1] = {total(sq)};
+            group_sum<GB>(q, G, part, half);
+            var = q[0] * p.inv_n;
+        } else {
+            float s[2] = {total(sq), total(sx)};
+            group_sum<GB>(s, G, part, half);
+            mean = s[1] * p.inv_n;
+            var = fmaf(-mean, mean, s[0] * p.inv_n);
+            const bool again = large_mean(mean, var);
+            if (GB ? again : __any_sync(0xffffffffu, again)) {
+                float q[1] = {0.f};
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    float v[8];
+                    single(x[i], v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float xm = first_col<VEC>(i, t, G) + e * step < p.N ? v[e] - mean : 0.f;
+                        q[0] = fmaf(xm, xm, q[0]);
+                    }
+                }
+                group_sum<GB>(q, G, part, half);
+                var = q[0] * p.inv_n;
+            }
+        }
+        const float rstd = rsqrtf(var + p.eps);
+        const pair_t scale = both(rstd), level = both(-mean * rstd);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int c = first_col<VEC>(i, t, G);
-            float x[8], z[8];
-            rx[i].values(x);
-            if constexpr (GATED) rz[i].values(z);
+            float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int col = c + e * step;
-                const float w = p.w && col < p.N ? __ldg(p.w + col) : 1.f;
-                const float b = p.b && col < p.N ? __ldg(p.b + col) : 0.f;
-                x[e] = fmaf((x[e] - mean) * rstd, w, b);
-                if constexpr (GATED) x[e] *= z[e] * sigmoid(z[e]);
+            for (int k = 0; k < 4; ++k) x[i][k] = fma2(fma2(x[i][k], scale, level), w[i][k], b[i][k]);
+            single(x[i], y);
+            if constexpr (GATED) {
+                float z[8];
+                ring.template read<1>(stage, i, row, z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] *= z[e] * sigmoid(z[e]);
             }
-            Eight<YB, VEC>::store(p.y, row * p.N, c, step, p.N, x);
+            store8<YB, VEC>(p.y, row * p.N, c, step, row < p.rows ? p.N : 0, y);
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int R, bool BLOCK, bool VEC, bool XB, bool YB, bool GATED>
-void fwd(const Params& p, const Shape& s, int blocks, cudaStream_t st) {
-    if constexpr (R == 1)
-        fwd_kernel<BLOCK, VEC, XB, YB, GATED><<<blocks, s.threads, 0, st>>>(p);
-    else
-        wide_fwd_kernel<R, VEC, XB, YB, GATED><<<blocks, s.threads, 0, st>>>(p);
+template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
+cudaError_t fwd(const Params& p, const Shape& s, int sms, cudaStream_t st) {
+    using Rows = typename Fwd<GB, R, VEC, XB, YB, GATED>::Rows;
+    static std::atomic<int> known{0};
+    const auto kernel = fwd_kernel<GB, R, VEC, XB, YB, GATED>;
+    constexpr int threads = GB ? GB : 256;
+    const int smem = Rows::bytes(threads, s.g);
+    const int resident = resident_blocks(kernel, threads, smem, known);
+    if (resident < 1) return cudaErrorLaunchOutOfResources;
+    const long long per = threads / s.g;
+    const int blocks = (int)std::min((p.rows + per - 1) / per, (long long)resident * sms);
+    kernel<<<blocks, threads, smem, st>>>(p);
+    return cudaGetLastError();
 }
-template <int R, bool BLOCK, bool VEC, bool XB, bool YB>
-void fwd_gated(const Params& p, const Shape& s, int blocks, cudaStream_t st) {
-    p.z ? fwd<R, BLOCK, VEC, XB, YB, true>(p, s, blocks, st) : fwd<R, BLOCK, VEC, XB, YB, false>(p, s, blocks, st);
+template <int GB, int R, bool VEC>
+cudaError_t fwd_types(const Params& p, const Shape& s, bool xb, bool yb, int sms, cudaStream_t st) {
+    if (p.z) {
+        if (xb) return yb ? fwd<GB, R, VEC, true, true, true>(p, s, sms, st) : fwd<GB, R, VEC, true, false, true>(p, s, sms, st);
+        return yb ? fwd<GB, R, VEC, false, true, true>(p, s, sms, st) : fwd<GB, R, VEC, false, false, true>(p, s, sms, st);
+    }
+    if (xb) return yb ? fwd<GB, R, VEC, true, true, false>(p, s, sms, st) : fwd<GB, R, VEC, true, false, false>(p, s, sms, st);
+    return yb ? fwd<GB, R, VEC, false, true, false>(p, s, sms, st) : fwd<GB, R, VEC, false, false, false>(p, s, sms, st);
 }
-template <int R, bool BLOCK, bool VEC>
-void fwd_types(const Params& p, const Shape& s, bool xb, bool yb, int blocks, cudaStream_t st) {
-    if (xb)
-        yb ? fwd_gated<R, BLOCK, VEC, true, true>(p, s, blocks, st) : fwd_gated<R, BLOCK, VEC, true, false>(p, s, blocks, st);
-    else
-        yb ? fwd_gated<R, BLOCK, VEC, false, true>(p, s, blocks, st) : fwd_gated<R, BLOCK, VEC, false, false>(p, s, blocks, st);
-}
-template <int R, bool BLOCK>
-void fwd_vec(const Params& p, const Shape& s, bool xb, bool yb, int blocks, cudaStream_t st) {
-    s.vec ? fwd_types<R, BLOCK, true>(p, s, xb, yb, blocks, st) : fwd_types<R, BLOCK, false>(p, s, xb, yb, blocks, st);
+template <int GB, int R>
+cudaError_t fwd_vec(const Params& p, const Shape& s, bool xb, bool yb, int sms, cudaStream_t st) {
+    return s.vec ? fwd_types<GB, R, true>(p, s, xb, yb, sms, st) : fwd_types<GB, R, false>(p, s, xb, yb, sms, st);
 }
 
 gdn_status check(long long rows, int N, int x_dtype, int y_dtype, int rms, float eps, const void* x,
@@ -172,15 +156,11 @@ bool misaligned(const void* ptr) { return reinterpret_cast<uintptr_t>(ptr) & 15u
 }  // namespace
 
 cudaError_t launch_fwd(const Params& p, const Shape& s, bool xb, bool yb, int sms, cudaStream_t st) {
-    const long long per = s.threads / s.g;
-    const int blocks = (int)std::min((p.rows + per - 1) / per, (long long)sms * (kFwdThreadsPerSm / s.threads));
-    if (!s.block)
-        fwd_vec<1, false>(p, s, xb, yb, blocks, st);
-    else if (s.r == 1)
-        fwd_vec<1, true>(p, s, xb, yb, blocks, st);
-    else
-        fwd_vec<2, true>(p, s, xb, yb, blocks, st);
-    return cudaGetLastError();
+    if (s.g <= 32) return s.r == 1 ? fwd_vec<0, 1>(p, s, xb, yb, sms, st) : fwd_vec<0, 2>(p, s, xb, yb, sms, st);
+    if (s.g == 64) return fwd_vec<64, 2>(p, s, xb, yb, sms, st);
+    if (s.g == 128) return fwd_vec<128, 2>(p, s, xb, yb, sms, st);
+    if (s.g == 256) return fwd_vec<256, 2>(p, s, xb, yb, sms, st);
+    return fwd_vec<512, 2>(p, s, xb, yb, sms, st);
 }
 
 }  // namespace norm
@@ -253,7 +233,7 @@ gdn_status gdn_norm_bwd(long long rows, int N, int x_dtype, int y_dtype, int rms
     p.inv_n = 1.f / N;
     const int sms = std::min(std::max(1, current_sm_count()), kSmBound);
     const cudaError_t e = launch_bwd(p, s, x_dtype == GDN_DTYPE_BF16, y_dtype == GDN_DTYPE_BF16,
-                                     bwd_blocks(rows, s, sms), dw, db, reinterpret_cast<cudaStream_t>(stream));
+                                     sms, dw, db, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -1,18 +1,22 @@
-// gdn_norm.cuh -- what the normalisation's two passes share: rows dealt to groups of threads, loads and
-// stores of eight values in any of the storage types, sums over a group.
+// gdn_norm.cuh -- what the normalisation's two passes share: rows dealt to groups of threads, rows staged in
+// shared memory ahead of their use, stores, sums over a group.
 #pragma once
+
+#include <algorithm>
+#include <atomic>
 
 #include <cuda_bf16.h>
 
 #include "gdn_internal.h"
+#include "gdn_pair.cuh"
 
 namespace gdn {
 namespace norm {
 
 // A row of N values belongs to a group of G threads: a part of a warp (G <= 32, a power of two) or a whole
-// block; every thread holds R times eight of its values (one up to N = 4096, two beyond, at G = 512). Where N % 8 == 0 the eight are consecutive and
-// move as vectors (16-byte aligned rows); else they are G apart, so that a warp's single loads and
-// stores still cover consecutive values.
+// block; every thread holds R times eight of its values: one up to N = 256, two beyond (what a row costs besides its
+// values -- the exchange, the addresses -- is then shared by twice as many). Where N % 8 == 0 the eight are consecutive and move as vectors (16-byte aligned rows); else they are G apart, so
+// that a warp's single accesses still cover consecutive values.
 struct Params {
     const void* x;
     const float* w;      // null: ones
@@ -28,43 +32,56 @@ struct Params {
     float eps, inv_n;
 };
 
-template <bool BF, bool VEC>
-struct Eight;
+constexpr int kMaxN = 8192;
+constexpr int kMaxThreads = 512;
+constexpr int kSmBound = 256;           // SMs of any device that sizes a workspace
 
-template <bool BF>
-struct Eight<BF, true> {
-    uint4 u[BF ? 1 : 2];
-    __device__ __forceinline__ void load(const void* base, long long row0, int c, int step, int n) {
-        (void)step;
-        if (c < n) {
-            const uint4* p = reinterpret_cast<const uint4*>((const char*)base + (row0 + c) * (BF ? 2 : 4));
-            u[0] = __ldcs(p);
-            if constexpr (!BF) u[1] = __ldcs(p + 1);
-        } else {
-            u[0] = make_uint4(0, 0, 0, 0);
-            if constexpr (!BF) u[1] = make_uint4(0, 0, 0, 0);
+// The first column of thread t's i-th eight values, and the distance between them.
+template <bool VEC>
+__device__ __forceinline__ int first_col(int i, int t, int G) {
+    return VEC ? (i * G + t) * 8 : i * 8 * G + t;
+}
+template <bool VEC>
+__device__ __forceinline__ int col_step(int G) {
+    return VEC ? 1 : G;
+}
+
+__device__ __forceinline__ pair_t both(float x) { return pack(x, x); }
+__device__ __forceinline__ float total(pair_t x) {
+    float lo, hi;
+    unpack(x, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ void single(const pair_t (&p)[4], float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack(p[i], f[2 * i], f[2 * i + 1]);
+}
+// a parameter's eight values of this thread's columns
+template <bool VEC>
+__device__ __forceinline__ void parameter(pair_t (&f)[4], const float* from, int c, int step, int n, float none) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = both(none);
+    if (!from) return;
+    if constexpr (VEC) {
+        if (c >= n) return;
+        const float4 a = __ldg(reinterpret_cast<const float4*>(from + c));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(from + c + 4));
+        f[0] = pack(a.x, a.y);
+        f[1] = pack(a.z, a.w);
+        f[2] = pack(b.x, b.y);
+        f[3] = pack(b.z, b.w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c0 = c + 2 * i * step, c1 = c0 + step;
+            f[i] = pack(c0 < n ? __ldg(from + c0) : none, c1 < n ? __ldg(from + c1) : none);
         }
     }
-    __device__ __forceinline__ void values(float (&f)[8]) const {
-        const unsigned a[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
-        if constexpr (BF) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(a[i] << 16);
-                f[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-            }
-        } else {
-            const unsigned d[4] = {u[1].x, u[1].y, u[1].z, u[1].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[i] = __uint_as_float(a[i]);
-                f[4 + i] = __uint_as_float(d[i]);
-            }
-        }
-    }
-    static __device__ __forceinline__ void store(void* base, long long row0, int c, int step, int n,
-                                                 const float (&f)[8]) {
-        (void)step;
+}
+
+template <bool BF, bool VEC>
+__device__ __forceinline__ void store8(void* base, long long row0, int c, int step, int n, const float (&f)[8]) {
+    if constexpr (VEC) {
         if (c >= n) return;
         uint4* p = reinterpret_cast<uint4*>((char*)base + (row0 + c) * (BF ? 2 : 4));
         if constexpr (BF) {
@@ -81,31 +98,7 @@ struct Eight<BF, true> {
             __stcs(p + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
                                      __float_as_uint(f[7])));
         }
-    }
-};
-
-template <bool BF>
-struct Eight<BF, false> {
-    float v[8];
-    __device__ __forceinline__ void load(const void* base, long long row0, int c, int step, int n) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int at = c + e * step;
-            v[e] = 0.f;
-            if (at < n) {
-                if constexpr (BF)
-                    v[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[row0 + at]);
-                else
-                    v[e] = reinterpret_cast<const float*>(base)[row0 + at];
-            }
-        }
-    }
-    __device__ __forceinline__ void values(float (&f)[8]) const {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = v[e];
-    }
-    static __device__ __forceinline__ void store(void* base, long long row0, int c, int step, int n,
-                                                 const float (&f)[8]) {
+    } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int at = c + e * step;
@@ -117,78 +110,234 @@ struct Eight<BF, false> {
             }
         }
     }
+}
+
+// The threads of a row meet: GB of them, the block's (threadIdx.x / GB)-th, or (GB == 0) a part of a warp.
+template <int GB>
+__device__ __forceinline__ void group_barrier() {
+    if constexpr (GB == 0)
+        __syncwarp();
+    else
+        asm volatile("barrier.sync %0, %1;" ::"r"(1 + threadIdx.x / GB), "n"(GB) : "memory");
+}
+
+// Rows on their way: a ring of kDepth stages in shared memory, filled by asynchronous 16-byte copies kDepth - 1
+// rows ahead, so that an SM has some 100 KB under way whatever the registers allow. Vectors: every thread
+// copies and reads its own pieces, and needs no one else. Odd row lengths: a row starts anywhere within 16
+// bytes, so the group copies the aligned pieces that cover it (the last one of the tensor cut short at its
+// end) and reads single values at the row's offset, after a barrier.
+template <bool VEC, int R, bool... BF>
+struct Ring {
+    static constexpr bool kBf[] = {BF...};
+    static constexpr int kTensors = sizeof...(BF);
+    static constexpr int es(int t) { return kBf[t] ? 2 : 4; }
+    static constexpr int pieces(int t) { return R * es(t) / 2; }   // of a thread
+    static constexpr int first_piece(int t) { return t == 0 ? 0 : first_piece(t - 1) + pieces(t - 1); }
+    static constexpr int kPieces = first_piece(kTensors - 1) + pieces(kTensors - 1);
+    static constexpr int kAhead = 12 / kPieces < 1 ? 1 : 12 / kPieces > 6 ? 6 : 12 / kPieces;   // 192 B a thread
+    static constexpr int kDepth = kAhead + 1;
+    static constexpr int kSlack = 2;   // odd rows: pieces more than the values take, a group and tensor
+    static constexpr int bytes(int threads, int G) {
+        return VEC ? kDepth * kPieces * threads * 16
+                   : kDepth * (kPieces * threads + kSlack * kTensors * (threads / G)) * 16;
+    }
+
+    unsigned base;   // shared memory
+    int G, t, tid, threads, N;
+    long long rows;
+
+    template <int T>
+    __device__ __forceinline__ unsigned region(int stage) const {   // odd rows: of this group
+        constexpr int kFirst = first_piece(T), kMine = pieces(T);
+        const int groups = threads / G;
+        return base + 16u * (stage * (kPieces * threads + kSlack * kTensors * groups) +
+                             (kFirst * threads + kSlack * T * groups) + (tid / G) * (kMine * G + kSlack));
+    }
+    template <int T>
+    __device__ __forceinline__ unsigned piece(int stage, int k) const {   // vectors: of this thread
+        constexpr int kFirst = first_piece(T);
+        return base + 16u * ((stage * kPieces + kFirst + k) * threads + tid);
+    }
+    static __device__ __forceinline__ void copy(unsigned to, const void* from, int n) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+    }
+    template <int T>
+    __device__ __forceinline__ void fetch(int stage, const void* from, long long row) const {
+        constexpr int E = es(T);
+        const char* src = reinterpret_cast<const char*>(from);
+        if constexpr (VEC) {
+            const int c = first_col<true>(0, t, G);
+            const char* at = src + (row * N + c) * E;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const bool in = c + i * 8 * G < N && row < rows;
+#pragma unroll
+                for (int k = 0; k < E / 2; ++k)
+                    copy(piece<T>(stage, i * (E / 2) + k), in ? at + i * 8 * G * E + 16 * k : src, in ? 16 : 0);
+            }
+        } else if (row < rows) {
+            const long long lo = row * N * E, end = rows * N * E, a = lo & ~15LL;
+            const int n = (int)((lo + (long long)N * E - a + 15) / 16);
+            const unsigned to = region<T>(stage);
+            for (int k = t; k < n; k += G)
+                copy(to + 16u * k, src + a + 16 * k, (int)min(16LL, end - (a + 16 * k)));
+        }
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // the oldest row's copies are complete (and, odd rows, everyone's; also, everyone has read the row before)
+    template <int GB>
+    static __device__ __forceinline__ void wait() {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        if constexpr (!VEC) group_barrier<GB>();
+    }
+    // this thread's i-th eight of a staged row
+    template <int T>
+    __device__ __forceinline__ void read(int stage, int i, long long row, float (&f)[8]) const {
+        constexpr int E = es(T);
+        if constexpr (VEC) {
+            unsigned u[E * 2];
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(u[4 * k]), "=r"(u[4 * k + 1]), "=r"(u[4 * k + 2]), "=r"(u[4 * k + 3])
+                             : "r"(piece<T>(stage, i * (E / 2) + k)));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] = E == 4 ? __uint_as_float(u[E == 4 ? e : 0])
+                              : __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+        } else {
+            const unsigned at = region<T>(stage) + (unsigned)((row * N * E) & 15);
+            const int n = row < rows ? N : 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = first_col<false>(i, t, G) + e * G;
+                f[e] = 0.f;
+                if (c < n) {
+                    if constexpr (E == 2) {
+                        unsigned short h;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + 2u * c));
+                        f[e] = __uint_as_float((unsigned)h << 16);
+                    } else {
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[e]) : "r"(at + 4u * c));
+                    }
+                }
+            }
+        }
+    }
+    template <int T>
+    __device__ __forceinline__ void read(int stage, int i, long long row, pair_t (&p)[4]) const {
+        float f[8];
+        read<T>(stage, i, row, f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = pack(f[2 * k], f[2 * k + 1]);
+    }
 };
 
-// The first column of thread t's i-th eight values, and the distance between them.
-template <bool VEC>
-__device__ __forceinline__ int first_col(int i, int t, int G) {
-    return VEC ? (i * G + t) * 8 : i * 8 * G + t;
-}
-template <bool VEC>
-__device__ __forceinline__ int col_step(int G) {
-    return VEC ? 1 : G;
-}
-
-// Sums of M values over the group, the same in each of its threads. Blocks: every call uses the other half of
-// `part`, whose readers are behind the barrier of the call in between.
-template <bool BLOCK, int M>
-__device__ __forceinline__ void group_sum(float (&x)[M], int G, float (*part)[3][32], int& half) {
-    const int first = BLOCK ? 16 : G / 2;
+// Sums of M (1, 2 or 4) values over the group, the same in each of its threads. G threads (a
+// multiple of 32), or (G == 0) g of a warp. Where there are several values the lanes first halve them among themselves, so that
+// four values take not much more than one. Several warps: every call uses the other half of `part` (this
+// group's), whose readers are behind the barrier of the call in between.
+template <int G, int M>
+__device__ __forceinline__ void group_sum(float (&x)[M], int g, float (*part)[64], int& half) {
+    const int lane = threadIdx.x & 31;
+    int off = G ? 16 : g / 2;
 #pragma unroll
-    for (int m = 0; m < M; ++m)
-        for (int off = first; off > 0; off >>= 1) x[m] += __shfl_xor_sync(0xffffffffu, x[m], off);
-    if constexpr (BLOCK) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    for (int n = M / 2; n >= 1; n /= 2, off /= 2) {
+        const bool up = lane & off;
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-            if (lane == 0) part[half][m][warp] = x[m];
-        __syncthreads();
+        for (int m = 0; m < n; ++m) {
+            const float keep = up ? x[m + n] : x[m], send = up ? x[m] : x[m + n];
+            x[m] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+    }
+    float one = x[0];
+    if constexpr (G == 0) {
+        for (; off > 0; off /= 2) one += __shfl_xor_sync(0xffffffffu, one, off);
+        // value m is with the lanes whose upper bits say m
+        const int base = lane & ~(g - 1);
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-            x[m] = lane < warps ? part[half][m][lane] : 0.f;
+        for (int m = 0; m < M; ++m) x[m] = M == 1 ? one : __shfl_sync(0xffffffffu, one, base + m * (g / M));
+    } else {
+        constexpr int WARPS = G / 32, ALL = M * WARPS;
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) x[m] += __shfl_xor_sync(0xffffffffu, x[m], off);
+        for (int o = 16 / M; o > 0; o /= 2) one += __shfl_xor_sync(0xffffffffu, one, o);
+        if (lane % (32 / M) == 0) part[half][lane / (32 / M) * WARPS + (threadIdx.x >> 5) % WARPS] = one;
+        group_barrier<G>();
+        if constexpr (ALL <= 32) {
+            one = part[half][lane % ALL];
+#pragma unroll
+            for (int o = WARPS / 2; o > 0; o /= 2) one += __shfl_xor_sync(0xffffffffu, one, o);
+#pragma unroll
+            for (int m = 0; m < M; ++m) x[m] = __shfl_sync(0xffffffffu, one, m * WARPS);
+        } else {   // 16 warps, four values: two to a lane
+            float two = part[half][lane + 32];
+            one = part[half][lane];
+#pragma unroll
+            for (int o = WARPS / 2; o > 0; o /= 2) {
+                one += __shfl_xor_sync(0xffffffffu, one, o);
+                two += __shfl_xor_sync(0xffffffffu, two, o);
+            }
+#pragma unroll
+            for (int m = 0; m < M; ++m) x[m] = __shfl_sync(0xffffffffu, m < 2 ? one : two, (m & 1) * WARPS);
         }
         half ^= 1;
     }
 }
 
-// (exp may overflow to infinity: the quotient is then 0)
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
+// The layer norm's mean and variance come from one exchange, as sums of x and x^2. The variance is then a
+// difference, which loses a few bits while the mean is within two standard deviations of zero; a row with
+// a larger mean goes round once more for the sum of (x - mean)^2.
+__device__ __forceinline__ bool large_mean(float mean, float var) { return mean * mean > 4.f * var; }
 
-// How a call is laid out: threads of a row and of a block, eights of a thread, blocks at most.
+// 1 / (1 + exp(-z)) from the hardware's approximations of 2^x and 1 / x (2 and 1 ulp, subnormals as zero): the
+// rounding of z log2(e) adds |z| / 2 ulp of the exponential. 2^x may overflow to infinity: the quotient is
+// then 0.
+__device__ __forceinline__ float sigmoid(float z) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * z));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+
+// How a call is laid out: threads of a row (8 to 512), eights of a thread.
 struct Shape {
-    bool block, vec;
-    int g, threads, r;
+    bool vec;
+    int g, r;
 };
 inline Shape shape_of(int N) {
     Shape s{};
     s.vec = N % 8 == 0;
     const int eights = (N + 7) / 8;
-    s.r = eights > 512 ? 2 : 1;
-    int g = 8;
-    while (g * s.r < eights) g *= 2;
-    s.block = g > 32;
-    s.g = g;
-    s.threads = s.block ? g : 256;
+    s.r = eights > 32 ? 2 : 1;
+    s.g = 8;
+    while (s.g * s.r < eights) s.g *= 2;
     return s;
 }
-constexpr int kMaxN = 8192;
-constexpr int kMaxThreads = 512;
-constexpr int kSmBound = 256;           // SMs of any device that sizes a workspace
-constexpr int kThreadsPerSm = 1024;     // of the backward's grid
 
-// blocks of the backward on `sms` SMs
+// blocks (of kMaxThreads threads, one an SM) of the backward on `sms` SMs, at most
 inline long long bwd_blocks(long long rows, const Shape& s, int sms) {
-    const long long per = s.threads / s.g;
-    const long long need = (rows + per - 1) / per;
-    const long long most = (long long)sms * (kThreadsPerSm / s.threads);
-    return need < most ? need : most;
+    const long long per = kMaxThreads / s.g, need = (rows + per - 1) / per;
+    return need < sms ? need : sms;
+}
+
+// Blocks of a kernel that are on an SM at once with `smem` bytes each, asked once for each kernel (and again when
+// smem changes): `known` holds the last answer and its smem in KiB. 0: an error.
+template <class Kernel>
+int resident_blocks(Kernel* kernel, int threads, int smem, std::atomic<int>& known) {
+    constexpr int kMost = 200 * 1024;   // above any call's
+    const int kib = (smem + 1023) / 1024, have = known.load(std::memory_order_relaxed);
+    if (have != 0 && have / 256 == kib) return have % 256;
+    int per_sm = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, kib * 1024) != cudaSuccess)
+        return 0;
+    known.store(kib * 256 + per_sm, std::memory_order_relaxed);
+    return per_sm;
 }
 
 cudaError_t launch_fwd(const Params& p, const Shape& s, bool xb, bool yb, int sms, cudaStream_t st);
 // ... with dw and db (null: not wanted) summed over the rows; rows == 0 gives zeros
-cudaError_t launch_bwd(const Params& p, const Shape& s, bool xb, bool yb, long long blocks, float* dw, float* db,
+cudaError_t launch_bwd(const Params& p, const Shape& s, bool xb, bool yb, int sms, float* dw, float* db,
                        cudaStream_t st);
 
 }  // namespace norm

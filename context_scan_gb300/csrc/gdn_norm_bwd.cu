@@ -9,241 +9,188 @@
 // forward. A row is read once and stays in registers. The rows' sums dw, db go over a thread's own rows in
 // registers, then over the block's groups and the blocks in a fixed order: no atomics, the same
 // result every time.
+#include <type_traits>
+
 #include "gdn_norm.cuh"
 
 namespace gdn {
 namespace norm {
 namespace {
 
-// d, and for the gate dyg = dy sigmoid(z) (1 + z (1 - sigmoid(z))), from dy (in d) and z
-__device__ __forceinline__ void gate(float (&d)[8], float (&dyg)[8], const float (&z)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float sg = sigmoid(z[e]);
-        dyg[e] = d[e] * sg * fmaf(z[e], 1.f - sg, 1.f);
-        d[e] *= z[e] * sg;
-    }
+// from d = dy: d = dy z sigmoid(z), dyg = dy sigmoid(z) (1 + z (1 - sigmoid(z)))
+__device__ __forceinline__ void gate(pair_t& d, pair_t& dyg, pair_t z) {
+    float z0, z1;
+    unpack(z, z0, z1);
+    const pair_t sg = pack(sigmoid(z0), sigmoid(z1)), one = both(1.f);
+    const pair_t dsg = mul2(d, sg);
+    dyg = mul2(dsg, fma2(z, fma2(sg, both(-1.f), one), one));
+    d = mul2(dsg, z);
 }
 
-template <bool BLOCK, bool VEC, bool XB, bool YB, bool GATED>
-__global__ void __launch_bounds__(BLOCK ? kMaxThreads : 256) bwd_kernel(Params p) {
-    __shared__ float part[2][3][32];
+// A block of kMaxThreads threads; GB of them to a row, 0: a part of a warp (rows of at most 512 values)
+template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
+struct Bwd {
+    using Rows = std::conditional_t<GATED, Ring<VEC, R, XB, YB, YB>, Ring<VEC, R, XB, YB>>;
+};
+
+template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
+__global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
+    using Rows = typename Bwd<GB, R, VEC, XB, YB, GATED>::Rows;
+    extern __shared__ __align__(16) char stages[];
+    __shared__ float parts[GB ? kMaxThreads / GB : 1][2][64];
+    float(*part)[64] = parts[GB ? threadIdx.x / GB : 0];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int half = 0;
-    const int G = BLOCK ? blockDim.x : p.g;
+    const int G = GB ? GB : p.g;
     const int t = threadIdx.x % G;
-    const int per_warp = BLOCK ? 1 : 32 / G;              // rows a warp holds at once
-    const int sub = BLOCK ? 0 : (threadIdx.x & 31) / G;   // which of them is this thread's
-    const int c = first_col<VEC>(0, t, G), step = col_step<VEC>(G);
-    const long long stride = (long long)gridDim.x * (blockDim.x / G);
-    long long row0 = (long long)blockIdx.x * (blockDim.x / G) + (BLOCK ? 0 : (threadIdx.x >> 5) * per_warp);
+    const int rows_block = kMaxThreads / G;               // rows a block holds at once, and a warp
+    const int rows_warp = GB ? 1 : 32 / G;
+    const int sub = GB ? 0 : (threadIdx.x & 31) / G;      // which of the warp's is this thread's
+    const int step = col_step<VEC>(G);
+    const long long stride = (long long)gridDim.x * rows_block;
+    // (the trip count is the same for all threads of a warp, and of a group)
+    long long row0 = (long long)blockIdx.x * rows_block + (GB ? threadIdx.x / G : (threadIdx.x >> 5) * rows_warp);
 
-    float w[8], b[8], dw[8], db[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int col = c + e * step;
-        w[e] = p.w && col < p.N ? __ldg(p.w + col) : 1.f;
-        if constexpr (GATED) b[e] = p.b && col < p.N ? __ldg(p.b + col) : 0.f;
-        dw[e] = db[e] = 0.f;
-    }
-    Eight<XB, VEC> nx;
-    Eight<YB, VEC> nz, nd;
-    auto fetch = [&](long long row) {
-        const int n = row < p.rows ? p.N : 0;
-        nx.load(p.x, row * p.N, c, step, n);
-        nd.load(p.dy, row * p.N, c, step, n);
-        if constexpr (GATED) nz.load(p.z, row * p.N, c, step, n);
+    const Rows ring{(unsigned)__cvta_generic_to_shared(stages), G, t, (int)threadIdx.x, kMaxThreads, p.N, p.rows};
+    auto fetch = [&](int stage, long long row) {
+        ring.template fetch<0>(stage, p.x, row);
+        ring.template fetch<1>(stage, p.dy, row);
+        if constexpr (GATED) ring.template fetch<2>(stage, p.z, row);
+        Rows::commit();
     };
-    fetch(row0 + sub);
-    for (; row0 < p.rows; row0 += stride) {
+#pragma unroll 1
+    for (int k = 0; k < Rows::kAhead; ++k) fetch(k, row0 + sub + k * stride);
+    pair_t w[4], b[4], dw2[R][4] = {}, db2[R][4] = {};
+    if constexpr (R == 1) {
+        parameter<VEC>(w, p.w, first_col<VEC>(0, t, G), step, p.N, 1.f);
+        if constexpr (GATED) parameter<VEC>(b, p.b, first_col<VEC>(0, t, G), step, p.N, 0.f);
+    }
+    for (int stage = 0; row0 < p.rows; row0 += stride, stage = stage == Rows::kAhead ? 0 : stage + 1) {
         const long long row = row0 + sub;
-        float x[8], d[8], dyg[8];
-        nx.values(x);
-        nd.values(d);
-        if constexpr (GATED) {
-            float z[8];
-            nz.values(z);
-            gate(d, dyg, z);
-        }
-        fetch(row + stride);
-        if (!p.rms) {
-            float s[1] = {0.f};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] += x[e];
-            group_sum<BLOCK>(s, G, part, half);
-            const float mean = s[0] * p.inv_n;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = c + e * step < p.N ? x[e] - mean : 0.f;
-        }
-        float s[3] = {0.f, 0.f, 0.f};   // of xm^2, d w xm, d w
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float dxh = d[e] * w[e];
-            s[0] = fmaf(x[e], x[e], s[0]);
-            s[1] = fmaf(dxh, x[e], s[1]);
-            s[2] += dxh;
-        }
-        group_sum<BLOCK>(s, G, part, half);
-        const float rstd = rsqrtf(fmaf(s[0], p.inv_n, p.eps));
-        const float along = rstd * rstd * s[1] * p.inv_n;
-        const float mean_d = p.rms ? 0.f : s[2] * p.inv_n;
-        const int n = row < p.rows ? p.N : 0;
-        float dx[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float xh = x[e] * rstd;
-            dx[e] = rstd * (fmaf(d[e], w[e], -mean_d) - x[e] * along);
-            if constexpr (GATED) dyg[e] *= fmaf(xh, w[e], b[e]);
-            if (row < p.rows) {   // (with eps = 0 the rows behind the last one are not finite)
-                dw[e] = fmaf(d[e], xh, dw[e]);
-                db[e] += d[e];
-            }
-        }
-        Eight<XB, VEC>::store(p.y, row * p.N, c, step, n, dx);
-        if constexpr (GATED)
-            if (p.dz) Eight<YB, VEC>::store(p.dz, row * p.N, c, step, n, dyg);
-    }
-    if (!p.partial) return;
-    float* out = p.partial + (long long)blockIdx.x * 2 * p.N;
-    if constexpr (BLOCK) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int col = c + e * step;
-            if (col < p.N) {
-                out[col] = dw[e];
-                out[p.N + col] = db[e];
-            }
-        }
-    } else {
-        // over a warp's rows by exchange, over the block's eight warps through shared memory
-        __shared__ float sum[8][2][256];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            for (int off = 16; off >= G; off >>= 1) {
-                dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], off);
-                db[e] += __shfl_xor_sync(0xffffffffu, db[e], off);
-            }
-            if (sub == 0) {
-                sum[threadIdx.x >> 5][0][c + e * step] = dw[e];
-                sum[threadIdx.x >> 5][1][c + e * step] = db[e];
-            }
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * p.N; i += blockDim.x) {
-            const int which = i >= p.N, col = which ? i - p.N : i;
-            float a = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) a += sum[k][which][col];
-            out[i] = a;
-        }
-    }
-}
-
-// Rows of more than 4096 values, one a block: what is loaded stays in registers as stored and is worked out
-// again after the sums; the weights come from the cache, and a thread's sums of dw and db stand in
-// shared memory, each column with the one thread that has it in every row.
-template <int R, bool VEC, bool XB, bool YB, bool GATED>
-__global__ void __launch_bounds__(kMaxThreads) wide_bwd_kernel(Params p) {
-    extern __shared__ float acc[];   // dw [N], db [N]
-    __shared__ float part[2][3][32];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int half = 0;
-    const int G = kMaxThreads, t = threadIdx.x, step = col_step<VEC>(G);
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int col = first_col<VEC>(i, t, G) + e * step;
-            if (p.partial && col < p.N) acc[col] = acc[p.N + col] = 0.f;
-        }
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        Eight<XB, VEC> rx[R];
-        Eight<YB, VEC> rz[R], rd[R];
+        Rows::template wait<GB>();
+        fetch(stage == 0 ? Rows::kAhead : stage - 1, row + Rows::kAhead * stride);
+        pair_t x[R][4], d[R][4], dxh[R][4], dyg[R][4];
+        pair_t xx = 0, dx_ = 0, ds = 0, xs = 0;   // sums of x^2, d w x, d w, x
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int c = first_col<VEC>(i, t, G);
-            rx[i].load(p.x, row * p.N, c, step, p.N);
-            rd[i].load(p.dy, row * p.N, c, step, p.N);
-            if constexpr (GATED) rz[i].load(p.z, row * p.N, c, step, p.N);
-        }
-        float mean = 0.f;
-        if (!p.rms) {
-            float s[1] = {0.f};
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                float x[8];
-                rx[i].values(x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[0] += x[e];
-            }
-            group_sum<true>(s, G, part, half);
-            mean = s[0] * p.inv_n;
-        }
-        auto terms = [&](int i, float (&x)[8], float (&d)[8], float (&dyg)[8]) {
-            rx[i].values(x);
-            rd[i].values(d);
+            ring.template read<0>(stage, i, row, x[i]);
+            ring.template read<1>(stage, i, row, d[i]);
             if constexpr (GATED) {
-                float z[8];
-                rz[i].values(z);
-                gate(d, dyg, z);
+                pair_t z[4];
+                ring.template read<2>(stage, i, row, z);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) gate(d[i][k], dyg[i][k], z[k]);
             }
+            if constexpr (R > 1) parameter<VEC>(w, p.w, first_col<VEC>(i, t, G), step, p.N, 1.f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] = first_col<VEC>(i, t, G) + e * step < p.N ? x[e] - mean : 0.f;
-        };
-        auto weight = [&](const float* a, int col, float none) {
-            return a && col < p.N ? __ldg(a + col) : none;
-        };
-        float s[3] = {0.f, 0.f, 0.f};   // of xm^2, d w xm, d w
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            float x[8], d[8], dyg[8];
-            terms(i, x, d, dyg);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float dxh = d[e] * weight(p.w, first_col<VEC>(i, t, G) + e * step, 1.f);
-                s[0] = fmaf(x[e], x[e], s[0]);
-                s[1] = fmaf(dxh, x[e], s[1]);
-                s[2] += dxh;
+            for (int k = 0; k < 4; ++k) {
+                dxh[i][k] = mul2(d[i][k], w[k]);
+                xx = fma2(x[i][k], x[i][k], xx);
+                dx_ = fma2(dxh[i][k], x[i][k], dx_);
+                ds = add2(ds, dxh[i][k]);
+                xs = add2(xs, x[i][k]);
             }
         }
-        group_sum<true>(s, G, part, half);
-        const float rstd = rsqrtf(fmaf(s[0], p.inv_n, p.eps));
-        const float along = rstd * rstd * s[1] * p.inv_n;
-        const float mean_d = p.rms ? 0.f : s[2] * p.inv_n;
+        float mean = 0.f, mean_d = 0.f, var, cross;   // cross: mean(d w xm)
+        if (p.rms) {
+            float q[2] = {total(xx), total(dx_)};
+            group_sum<GB>(q, G, part, half);
+            var = q[0] * p.inv_n;
+            cross = q[1] * p.inv_n;
+        } else {
+            float s[4] = {total(xx), total(dx_), total(ds), total(xs)};
+            group_sum<GB>(s, G, part, half);
+            mean = s[3] * p.inv_n;
+            mean_d = s[2] * p.inv_n;
+            var = fmaf(-mean, mean, s[0] * p.inv_n);
+            cross = fmaf(-mean, mean_d, s[1] * p.inv_n);
+            const bool again = large_mean(mean, var);
+            if (GB ? again : __any_sync(0xffffffffu, again)) {
+                float q[2] = {0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    float v[8], f[8];
+                    single(x[i], v);
+                    single(dxh[i], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float xm = first_col<VEC>(i, t, G) + e * step < p.N ? v[e] - mean : 0.f;
+                        q[0] = fmaf(xm, xm, q[0]);
+                        q[1] = fmaf(f[e], xm, q[1]);
+                    }
+                }
+                group_sum<GB>(q, G, part, half);
+                var = q[0] * p.inv_n;
+                cross = q[1] * p.inv_n;
+            }
+        }
+        // (0 for rows behind the last one, whose sums then add nothing even with eps = 0)
+        const float rstd = row < p.rows ? rsqrtf(var + p.eps) : 0.f;
+        // with xh = xm s: dx = s d w - s mean(d w) - xh s^2 mean(d w xm)
+        const pair_t scale = both(rstd), level = both(-mean * rstd), along = both(-rstd * rstd * cross),
+                     level_d = both(-rstd * mean_d);
+        const int n = row < p.rows ? p.N : 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int c = first_col<VEC>(i, t, G);
-            float x[8], d[8], dyg[8];
-            terms(i, x, d, dyg);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int col = c + e * step;
-                const float w = weight(p.w, col, 1.f), xh = x[e] * rstd;
-                if (p.partial && col < p.N) {
-                    acc[col] = fmaf(d[e], xh, acc[col]);
-                    acc[p.N + col] += d[e];
-                }
-                if constexpr (GATED) dyg[e] *= fmaf(xh, w, weight(p.b, col, 0.f));
-                x[e] = rstd * (fmaf(d[e], w, -mean_d) - x[e] * along);
+            if constexpr (R > 1 && GATED) {
+                parameter<VEC>(w, p.w, c, step, p.N, 1.f);
+                parameter<VEC>(b, p.b, c, step, p.N, 0.f);
             }
-            Eight<XB, VEC>::store(p.y, row * p.N, c, step, p.N, x);
+            float out[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const pair_t xh = fma2(x[i][k], scale, level);
+                if constexpr (GATED) dyg[i][k] = mul2(dyg[i][k], fma2(xh, w[k], b[k]));
+                dw2[i][k] = fma2(d[i][k], xh, dw2[i][k]);
+                db2[i][k] = add2(db2[i][k], d[i][k]);
+                x[i][k] = fma2(xh, along, fma2(dxh[i][k], scale, level_d));
+            }
+            single(x[i], out);
+            store8<XB, VEC>(p.y, row * p.N, c, step, n, out);
             if constexpr (GATED)
-                if (p.dz) Eight<YB, VEC>::store(p.dz, row * p.N, c, step, p.N, dyg);
+                if (p.dz) {
+                    single(dyg[i], out);
+                    store8<YB, VEC>(p.dz, row * p.N, c, step, n, out);
+                }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!p.partial) return;
-    float* out = p.partial + (long long)blockIdx.x * 2 * p.N;
+    // dw, db over the block's rows: first the rows of a warp, by exchange, then those of its warps or groups, through
+    // shared memory (the stages, which are not needed any more)
+    constexpr int kSets = GB ? kMaxThreads / GB : kMaxThreads / 32, kCols = (GB ? GB : 32) * 8 * R;
+    float(*sum)[2][kCols] = reinterpret_cast<float(*)[2][kCols]>(stages);
+    const int set = threadIdx.x / (GB ? GB : 32);
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
+        const int c = first_col<VEC>(i, t, G);
+        float dw[8], db[8];
+        single(dw2[i], dw);
+        single(db2[i], db);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int col = first_col<VEC>(i, t, G) + e * step;
-            if (col < p.N) {
-                out[col] = acc[col];
-                out[p.N + col] = acc[p.N + col];
+            if constexpr (GB == 0)
+                for (int off = 16; off >= G; off >>= 1) {
+                    dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], off);
+                    db[e] += __shfl_xor_sync(0xffffffffu, db[e], off);
+                }
+            if (sub == 0) {
+                sum[set][0][c + e * step] = dw[e];
+                sum[set][1][c + e * step] = db[e];
             }
         }
+    }
+    __syncthreads();
+    float* out = p.partial + (long long)blockIdx.x * 2 * p.N;
+    for (int i = threadIdx.x; i < 2 * p.N; i += kMaxThreads) {
+        const int which = i >= p.N, col = which ? i - p.N : i;
+        float a = 0.f;
+#pragma unroll
+        for (int k = 0; k < kSets; ++k) a += sum[k][which][col];
+        out[i] = a;
+    }
 }
 
 // dw and db from the blocks' sums: 32 columns a block, 32 threads to a column.
@@ -255,8 +202,23 @@ __global__ void __launch_bounds__(1024) columns_kernel(const float* partial, int
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!out) return;
     float a = 0.f;
-    if (c < N)
-        for (int i = k; i < blocks; i += 32) a += __ldcg(partial + ((long long)i * 2 + blockIdx.y) * N + c);
+    if (c < N) {
+        const float* from = partial + (long long)blockIdx.y * N + c;
+        int i = k;
+        for (; i + 7 * 32 < blocks; i += 8 * 32) {   // eight loads on their way
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __ldcg(from + (long long)(i + 32 * j) * 2 * N);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a += v[j];
+        }
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = i + 32 * j < blocks ? __ldcg(from + (long long)(i + 32 * j) * 2 * N) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a += v[j];
+    }
     sum[k][lane] = a;
     __syncthreads();
     a = sum[lane][k];   // thread (lane, k): the lane-th part of column k
@@ -266,49 +228,52 @@ __global__ void __launch_bounds__(1024) columns_kernel(const float* partial, int
     if (lane == 0 && col < N) out[col] = a;
 }
 
-template <int R, bool BLOCK, bool VEC, bool XB, bool YB, bool GATED>
+template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
 cudaError_t bwd(const Params& p, const Shape& s, int blocks, cudaStream_t st) {
-    if constexpr (R == 1) {
-        bwd_kernel<BLOCK, VEC, XB, YB, GATED><<<blocks, s.threads, 0, st>>>(p);
-    } else {
-        const int smem = p.partial ? 2 * p.N * (int)sizeof(float) : 0;
-        const cudaError_t e = cudaFuncSetAttribute(wide_bwd_kernel<R, VEC, XB, YB, GATED>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        wide_bwd_kernel<R, VEC, XB, YB, GATED><<<blocks, s.threads, smem, st>>>(p);
-    }
+    using Rows = typename Bwd<GB, R, VEC, XB, YB, GATED>::Rows;
+    static_assert(Rows::bytes(kMaxThreads, 32) >= kMaxThreads * 8 * R * 2 * 4, "the sums fit where the rows were");
+    static std::atomic<int> known{0};
+    const auto kernel = bwd_kernel<GB, R, VEC, XB, YB, GATED>;
+    const int smem = Rows::bytes(kMaxThreads, s.g);
+    if (resident_blocks(kernel, kMaxThreads, smem, known) < 1) return cudaErrorLaunchOutOfResources;
+    kernel<<<blocks, kMaxThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
-template <int R, bool BLOCK, bool VEC, bool XB, bool YB>
-cudaError_t bwd_gated(const Params& p, const Shape& s, int blocks, cudaStream_t st) {
-    return p.z ? bwd<R, BLOCK, VEC, XB, YB, true>(p, s, blocks, st)
-               : bwd<R, BLOCK, VEC, XB, YB, false>(p, s, blocks, st);
-}
-template <int R, bool BLOCK, bool VEC>
+template <int GB, int R, bool VEC>
 cudaError_t bwd_types(const Params& p, const Shape& s, bool xb, bool yb, int blocks, cudaStream_t st) {
+    if (p.z) {
+        if (xb)
+            return yb ? bwd<GB, R, VEC, true, true, true>(p, s, blocks, st)
+                      : bwd<GB, R, VEC, true, false, true>(p, s, blocks, st);
+        return yb ? bwd<GB, R, VEC, false, true, true>(p, s, blocks, st)
+                  : bwd<GB, R, VEC, false, false, true>(p, s, blocks, st);
+    }
     if (xb)
-        return yb ? bwd_gated<R, BLOCK, VEC, true, true>(p, s, blocks, st)
-                  : bwd_gated<R, BLOCK, VEC, true, false>(p, s, blocks, st);
-    return yb ? bwd_gated<R, BLOCK, VEC, false, true>(p, s, blocks, st)
-              : bwd_gated<R, BLOCK, VEC, false, false>(p, s, blocks, st);
+        return yb ? bwd<GB, R, VEC, true, true, false>(p, s, blocks, st)
+                  : bwd<GB, R, VEC, true, false, false>(p, s, blocks, st);
+    return yb ? bwd<GB, R, VEC, false, true, false>(p, s, blocks, st)
+              : bwd<GB, R, VEC, false, false, false>(p, s, blocks, st);
 }
-template <int R, bool BLOCK>
+template <int GB, int R>
 cudaError_t bwd_vec(const Params& p, const Shape& s, bool xb, bool yb, int blocks, cudaStream_t st) {
-    return s.vec ? bwd_types<R, BLOCK, true>(p, s, xb, yb, blocks, st)
-                 : bwd_types<R, BLOCK, false>(p, s, xb, yb, blocks, st);
+    return s.vec ? bwd_types<GB, R, true>(p, s, xb, yb, blocks, st)
+                 : bwd_types<GB, R, false>(p, s, xb, yb, blocks, st);
 }
 
 }  // namespace
 
-cudaError_t launch_bwd(const Params& p_in, const Shape& s, bool xb, bool yb, long long nblocks, float* dw,
-                       float* db, cudaStream_t st) {
+cudaError_t launch_bwd(const Params& p_in, const Shape& s, bool xb, bool yb, int sms, float* dw, float* db,
+                       cudaStream_t st) {
     Params p = p_in;
     if (!dw && !db) p.partial = nullptr;
-    const int blocks = (int)nblocks;
+    const int blocks = (int)bwd_blocks(p.rows, s, sms);
     if (blocks > 0) {
-        const cudaError_t e = !s.block ? bwd_vec<1, false>(p, s, xb, yb, blocks, st)
-                              : s.r == 1 ? bwd_vec<1, true>(p, s, xb, yb, blocks, st)
-                                         : bwd_vec<2, true>(p, s, xb, yb, blocks, st);
+        const cudaError_t e = s.g <= 32    ? (s.r == 1 ? bwd_vec<0, 1>(p, s, xb, yb, blocks, st)
+                                                       : bwd_vec<0, 2>(p, s, xb, yb, blocks, st))
+                              : s.g == 64  ? bwd_vec<64, 2>(p, s, xb, yb, blocks, st)
+                              : s.g == 128 ? bwd_vec<128, 2>(p, s, xb, yb, blocks, st)
+                              : s.g == 256 ? bwd_vec<256, 2>(p, s, xb, yb, blocks, st)
+                                           : bwd_vec<512, 2>(p, s, xb, yb, blocks, st);
         if (e != cudaSuccess) return e;
     }
     if (!p.partial) return cudaSuccess;

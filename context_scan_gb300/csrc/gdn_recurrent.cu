@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 
 #include "gdn_internal.h"
+#include "gdn_pair.cuh"
 
 namespace gdn {
 namespace {
@@ -58,26 +59,6 @@ struct RecurrentParams {
     int ordered;           // the longest sequences first (ordered_sequence)
 };
 
-using pair_t = unsigned long long;   // two fp32 values of one column, rows 2 i and 2 i + 1
-
-__device__ __forceinline__ pair_t pack(float lo, float hi) {
-    pair_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack(pair_t x, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) {
-    pair_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
-    pair_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ float total(pair_t x) {
     float lo, hi;
     unpack(x, lo, hi);

@@ -490,7 +490,7 @@ GDN_API gdn_status gdn_norm_fwd(long long rows, int N, int x_dtype, int y_dtype,
                                 const void* x, const float* w, const float* b, const void* z,
                                 void* y, void* stream);
 
-/* Workspace bytes for gdn_norm_bwd: the blocks' sums of dw and db (at most 33 MiB). It needs no
+/* Workspace bytes for gdn_norm_bwd: the blocks' sums of dw and db (at most 17 MiB). It needs no
  * initial value. Returns 0 for rows or N outside the set above. */
 GDN_API size_t gdn_norm_bwd_workspace_bytes(long long rows, int N);
 

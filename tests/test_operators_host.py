@@ -143,7 +143,7 @@ def test_norm_workspace(L):
     assert W(-1, 8) == 0 and W(1, 0) == 0 and W(1, 8193) == 0
     assert W(0, 64) == 256
     assert W(1, 64) == 256 + 512                      # one block's sums of dw and db
-    assert max(W(1 << 24, n) for n in (1, 128, 256, 257, 2048, 4096, 8192)) <= 33 << 20   # 2 * 8192 * 4 B * 512 blocks
+    assert max(W(1 << 24, n) for n in (1, 128, 256, 257, 2048, 4096, 8192)) <= 17 << 20   # 2 * 8192 * 4 B * 256 blocks
 
 
 def test_norm_binding_refuses_tensors_off_the_device(L):
