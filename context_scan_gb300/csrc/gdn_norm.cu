@@ -52,11 +52,12 @@ __global__ void __launch_bounds__(GB ? GB : 256) fwd_kernel(Params p) {
     }
     for (int stage = 0; row0 < p.rows; row0 += stride, stage = stage == Rows::kAhead ? 0 : stage + 1) {
         const long long row = row0 + sub;
-        Rows::template wait<GB>();
+        Rows::template wait<GB, GB>();
         fetch(stage == 0 ? Rows::kAhead : stage - 1, row + Rows::kAhead * stride);
         pair_t x[R][4], sq = 0, sx = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+            if (GB && !warp_has<VEC>(i, t, G, p.N)) continue;
             ring.template read<0>(stage, i, row, x[i]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -67,11 +68,11 @@ __global__ void __launch_bounds__(GB ? GB : 256) fwd_kernel(Params p) {
         float mean = 0.f, var;
         if (p.rms) {
             float q[1] = {total(sq)};
-            group_sum<GB>(q, G, part, half);
+            group_sum<GB, GB>(q, G, part, half);
             var = q[0] * p.inv_n;
         } else {
             float s[2] = {total(sq), total(sx)};
-            group_sum<GB>(s, G, part, half);
+            group_sum<GB, GB>(s, G, part, half);
             mean = s[1] * p.inv_n;
             var = fmaf(-mean, mean, s[0] * p.inv_n);
             const bool again = large_mean(mean, var);
@@ -79,6 +80,7 @@ __global__ void __launch_bounds__(GB ? GB : 256) fwd_kernel(Params p) {
                 float q[1] = {0.f};
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
+                    if (GB && !warp_has<VEC>(i, t, G, p.N)) continue;
                     float v[8];
                     single(x[i], v);
 #pragma unroll
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(GB ? GB : 256) fwd_kernel(Params p) {
                         q[0] = fmaf(xm, xm, q[0]);
                     }
                 }
-                group_sum<GB>(q, G, part, half);
+                group_sum<GB, GB>(q, G, part, half);
                 var = q[0] * p.inv_n;
             }
         }
@@ -95,6 +97,7 @@ __global__ void __launch_bounds__(GB ? GB : 256) fwd_kernel(Params p) {
         const pair_t scale = both(rstd), level = both(-mean * rstd);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+            if (GB && !warp_has<VEC>(i, t, G, p.N)) continue;
             const int c = first_col<VEC>(i, t, G);
             float y[8];
 #pragma unroll

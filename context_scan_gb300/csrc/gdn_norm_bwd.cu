@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
     }
     for (int stage = 0; row0 < p.rows; row0 += stride, stage = stage == Rows::kAhead ? 0 : stage + 1) {
         const long long row = row0 + sub;
-        Rows::template wait<GB>();
+        Rows::template wait<GB, kMaxThreads>();
         fetch(stage == 0 ? Rows::kAhead : stage - 1, row + Rows::kAhead * stride);
         pair_t x[R][4], d[R][4], dxh[R][4], dyg[R][4];
         pair_t xx = 0, dx_ = 0, ds = 0, xs = 0;   // sums of x^2, d w x, d w, x
@@ -94,12 +94,12 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
         float mean = 0.f, mean_d = 0.f, var, cross;   // cross: mean(d w xm)
         if (p.rms) {
             float q[2] = {total(xx), total(dx_)};
-            group_sum<GB>(q, G, part, half);
+            group_sum<GB, kMaxThreads>(q, G, part, half);
             var = q[0] * p.inv_n;
             cross = q[1] * p.inv_n;
         } else {
             float s[4] = {total(xx), total(dx_), total(ds), total(xs)};
-            group_sum<GB>(s, G, part, half);
+            group_sum<GB, kMaxThreads>(s, G, part, half);
             mean = s[3] * p.inv_n;
             mean_d = s[2] * p.inv_n;
             var = fmaf(-mean, mean, s[0] * p.inv_n);
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
                 float q[2] = {0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    float v[8], f[8];
+                            float v[8], f[8];
                     single(x[i], v);
                     single(dxh[i], f);
 #pragma unroll
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
                         q[1] = fmaf(f[e], xm, q[1]);
                     }
                 }
-                group_sum<GB>(q, G, part, half);
+                group_sum<GB, kMaxThreads>(q, G, part, half);
                 var = q[0] * p.inv_n;
                 cross = q[1] * p.inv_n;
             }
