@@ -56,7 +56,8 @@ struct RecurrentParams {
     DeviceError* err;
     int nseq, T, H, Hqk, V, num_slots;
     int out_bf16, decay_first, per_token;
-    int ordered;           // the longest sequences first (ordered_sequence)
+    int ordered;           // the longest sequences first (ordered_sequence), by lengths in steps of
+    int order_shift;       // 2^order_shift tokens
 };
 
 __device__ __forceinline__ float total(pair_t x) {
@@ -473,29 +474,59 @@ __global__ void __launch_bounds__(32 * kWarps, CW == 16 ? 4 : 1) decode_kernel(R
     tile.store(p.state + slot_out * at.page + at.off, p.V);
 }
 
-// Which sequence the thread blocks with number `mine` among the sequences take: the mine-th longest (of equal
-// ones the lower first), so that the long ones start first and the short ones fill the gaps at the end.
-constexpr int kOrderSeqs = 256;
+// Which sequence the thread blocks with number `mine` among the sequences take: the mine-th in the order of falling
+// length (in steps of 2^shift tokens; equal ones by number), so that the long ones start first and the
+// short ones fill the gaps at the end. Every block sorts for itself, by counting.
+constexpr int kBuckets = 128;
 __device__ __forceinline__ int ordered_sequence(const RecurrentParams& p, int mine) {
-    __shared__ __align__(16) int len[kOrderSeqs];
+    __shared__ __align__(16) int count[kBuckets];
     __shared__ int found;
-    const int t = threadIdx.x, n = p.nseq, up = (n + 3) & ~3;
-    for (int i = t; i < up; i += 32 * kWarps) 
-        len[i] = i < n ? (int)((unsigned)__ldg(p.cu + i + 1) - (unsigned)__ldg(p.cu + i)) : INT_MIN;
+    const int t = threadIdx.x, lane = t & 31;
+    auto bucket = [&](int i) {   // the longest in bucket 0
+        const int l = (int)((unsigned)__ldg(p.cu + i + 1) - (unsigned)__ldg(p.cu + i)) >> p.order_shift;
+        return kBuckets - 1 - min(max(l, 0), kBuckets - 1);
+    };
+    count[t] = 0;
     __syncthreads();
-    for (int i = t; i < n; i += 32 * kWarps) {
-        const int l = len[i];
-        int rank = 0;
-        for (int j = 0; j < up; j += 4) {
-            const int4 x = *reinterpret_cast<const int4*>(&len[j]);
-            rank += (x.x > l || (x.x == l && j < i)) + (x.y > l || (x.y == l && j + 1 < i)) +
-                    (x.z > l || (x.z == l && j + 2 < i)) + (x.w > l || (x.w == l && j + 3 < i));
+    for (int i = t; i < p.nseq; i += 32 * kWarps) atomicAdd(&count[bucket(i)], 1);
+    __syncthreads();
+    if (t < 32) {
+        // the bucket that holds number `mine`, and which of it that is
+        const int4 c = *reinterpret_cast<const int4*>(&count[4 * lane]);
+        const int sum = c.x + c.y + c.z + c.w;
+        int before = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, before, off);
+            if (lane >= off) before += y;
         }
-        if (rank == mine) found = i;
+        before -= sum;
+        const int at = 31 - __clz(__ballot_sync(0xffffffffu, before <= mine));   // the last lane that starts at or before
+        int left = mine - before, b = 4 * lane;
+        const int n[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (b == 4 * lane + j && left >= n[j]) {
+                left -= n[j];
+                ++b;
+            }
+        b = __shfl_sync(0xffffffffu, b, at);
+        left = __shfl_sync(0xffffffffu, left, at);
+        // the left-th of the bucket's sequences
+        for (int i0 = 0; i0 < p.nseq; i0 += 32) {
+            const unsigned in = __ballot_sync(0xffffffffu, i0 + lane < p.nseq && bucket(min(i0 + lane, p.nseq - 1)) == b);
+            if (left < __popc(in)) {
+                const bool me = (in >> lane & 1u) && __popc(in & ((1u << lane) - 1u)) == left;
+                if (me) found = i0 + lane;
+                break;
+            }
+            left -= __popc(in);
+        }
     }
     __syncthreads();
     return found;
 }
+static_assert(kBuckets == 32 * kWarps, "a thread for each bucket");
 
 // Any number of tokens a sequence, kTokens of them staged in shared memory at a time while the next ones load.
 template <int K, int CW, int CPL, bool GATEK, bool BF>
@@ -708,6 +739,7 @@ cudaError_t launch_k(const RecurrentParams& p, bool gate_k, bool bf16, int sms, 
 // Each block of the rule looks for other sequences that name its slot when there are at most this many
 // sequences; above it, and where states are kept after every token, claim_kernel does so once.
 constexpr int kInlineSeqs = 512;
+constexpr int kOrderSeqs = 1024, kOrderTokens = 12;
 
 gdn_status check(const gdn_problem* p, int Hqk, int nseq, const int* cu, int num_slots, int per_token) {
     if (!p) return GDN_ERR_INVALID_ARG;
@@ -776,8 +808,16 @@ gdn_status gdn_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, const int*
     c.num_slots = num_slots;
     c.out_bf16 = p->out_dtype == GDN_DTYPE_BF16;
     c.decay_first = p->decay_first;
+    if (p->T == 1 && !cu_seqlens) per_token = 0;   // the state after the token is the final one
     c.per_token = per_token;
-    c.ordered = cu_seqlens && nseq <= kOrderSeqs && nseq > 1;
+    // The longest sequences first, where there is something to gain: several tokens a sequence on average, and more
+    // blocks than the SMs hold at once. 37 sequences of up to 63 tokens, H = 16: 97 us without, 74 with;
+    // 212 of 1 to 8: 132 without, 138 with.
+    const int average = cu_seqlens ? p->T / nseq : 0;
+    c.ordered = nseq > 1 && nseq <= kOrderSeqs && average >= kOrderTokens &&
+                (long long)nseq * p->H * (p->V / 64) > 4LL * current_sm_count();
+    for (; (4LL * average) >> c.order_shift >= kBuckets; ++c.order_shift) {
+    }
     if (nseq > kInlineSeqs || (per_token && nseq > 1)) {
         int* owner = reinterpret_cast<int*>(ws + kWsHeader);
         int* cu_bad = reinterpret_cast<int*>(ws + kWsVerdict);

@@ -157,6 +157,20 @@ def test_in_place(name):
     check_state(d, after, ref, slots)
 
 
+def test_long_sequences_start_first():
+    # lengths that the order of long sequences covers: ties, empty ones, more than one warp's worth of them, one far
+    # beyond the last bucket; every sequence is run exactly once
+    for lens in ([(i * 37) % 61 for i in range(300)], [0] * 40 + [500] + [20] * 200, [12] * 200 + [13] * 100):
+        d = make(lens, 3, 1, 64, 64, seed=len(lens), packed=True)
+        n = len(lens)
+        slots = d["order"][:n]
+        after, err = call(d, slots, slots)
+        assert err == (0, 0)
+        o_ref, ref = reference(d, slots, slots)
+        check_o(d, o_ref)
+        check_state(d, after, ref, slots)
+
+
 @pytest.mark.parametrize("name", ["one_token_one_seq", "one_token_batch", "ragged", "ragged_large",
                                   "k64_v128", "gate_k", "no_tokens_at_all", "one_packed"])
 def test_state_after_every_token(name):
