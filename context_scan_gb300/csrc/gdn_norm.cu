@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(GB ? GB : 256) fwd_kernel(Params p) {
 template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
 cudaError_t fwd(const Params& p, const Shape& s, int sms, cudaStream_t st) {
     using Rows = typename Fwd<GB, R, VEC, XB, YB, GATED>::Rows;
-    static std::atomic<int> known{0};
+    static std::atomic<int> known[kDevices];
     const auto kernel = fwd_kernel<GB, R, VEC, XB, YB, GATED>;
     constexpr int threads = GB ? GB : 256;
     const int smem = Rows::bytes(threads, s.g);

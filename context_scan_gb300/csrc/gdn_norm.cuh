@@ -343,18 +343,22 @@ inline long long bwd_blocks(long long rows, const Shape& s, int sms) {
     return need < sms ? need : sms;
 }
 
-// Blocks of a kernel that are on an SM at once with `smem` bytes each, asked once for each kernel (and again when
-// smem changes): `known` holds the last answer and its smem in KiB. 0: an error.
+// Blocks of a kernel that are on an SM at once with `smem` bytes each, asked (and the shared memory allowed) once for
+// each kernel and device, and again when smem changes: `known` holds the last answer and its smem in KiB. 0: an
+// error.
+constexpr int kDevices = 64;
 template <class Kernel>
-int resident_blocks(Kernel* kernel, int threads, int smem, std::atomic<int>& known) {
+int resident_blocks(Kernel* kernel, int threads, int smem, std::atomic<int> (&known)[kDevices]) {
     constexpr int kMost = 200 * 1024;   // above any call's
-    const int kib = (smem + 1023) / 1024, have = known.load(std::memory_order_relaxed);
+    int dev = 0, per_sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::atomic<int>& last = known[dev % kDevices];
+    const int kib = (smem + 1023) / 1024, have = last.load(std::memory_order_relaxed);
     if (have != 0 && have / 256 == kib) return have % 256;
-    int per_sm = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, kib * 1024) != cudaSuccess)
         return 0;
-    known.store(kib * 256 + per_sm, std::memory_order_relaxed);
+    last.store(kib * 256 + per_sm, std::memory_order_relaxed);
     return per_sm;
 }
 

@@ -232,7 +232,7 @@ template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
 cudaError_t bwd(const Params& p, const Shape& s, int blocks, cudaStream_t st) {
     using Rows = typename Bwd<GB, R, VEC, XB, YB, GATED>::Rows;
     static_assert(Rows::bytes(kMaxThreads, 32) >= kMaxThreads * 8 * R * 2 * 4, "the sums fit where the rows were");
-    static std::atomic<int> known{0};
+    static std::atomic<int> known[kDevices];
     const auto kernel = bwd_kernel<GB, R, VEC, XB, YB, GATED>;
     const int smem = Rows::bytes(kMaxThreads, s.g);
     if (resident_blocks(kernel, kMaxThreads, smem, known) < 1) return cudaErrorLaunchOutOfResources;

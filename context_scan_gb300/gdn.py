@@ -393,21 +393,17 @@ def gdn_recurrent_fwd(q, k, v, g, beta, state, slots_in, slots_out, o, workspace
     nseq = B if cu_seqlens is None else cu_seqlens.numel() - 1
     _on_device(q, k, v, g, beta, state, slots_in, slots_out, o, workspace, cu_seqlens)
     gate_k = g.dim() == 4
-    gshape = (B, T, H, K) if gate_k else (B, T, H)
-    _is("q", q, dt, (B, T, Hqk, K))
-    _is("k", k, dt, (B, T, Hqk, K))
-    _is("v", v, dt, vshape)
-    _is("g", g, dt, gshape)
-    _is("beta", beta, dt, gshape[:3])
-    _is("o", o, o.dtype, vshape)
-    slots = 0
-    if state is not None:
-        slots = state.shape[0]
-        _is("state", state, torch.float32, (slots, H, K, V))
-    _is("slots_in", slots_in, torch.int32, (nseq,))
-    _is("slots_out", slots_out, torch.int32, (B * T if per_token else nseq,))
-    if cu_seqlens is not None:
-        _is("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,))
+    slots = 0 if state is None else state.shape[0]
+    want = (("q", q, dt, kshape), ("v", v, dt, (B, T, H, V)), ("o", o, o.dtype, vshape),
+            ("g", g, dt, (B, T, H, K) if gate_k else (B, T, H)), ("beta", beta, dt, (B, T, H)),
+            ("state", state, torch.float32, (slots, H, K, V)), ("slots_in", slots_in, torch.int32, (nseq,)),
+            ("slots_out", slots_out, torch.int32, (B * T if per_token else nseq,)),
+            ("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,)))
+    for name, t, dtype, shape in want:
+        if t is not None and (t.dtype is not dtype or t.shape != shape):
+            _is(name, t, dtype, shape)   # names what is wrong
+    if kshape[:2] != (B, T):
+        raise ValueError(f"k is {tuple(kshape)}, v {tuple(vshape)}")
     prob = Problem(B, T, H, K, V, 64, _dtype_code(k), _dtype_code(o), decay_first, gate_k)
     _check(lib().gdn_recurrent_fwd(ctypes.byref(prob), Hqk, nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(),
                                    v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state), slots,
