@@ -18,12 +18,12 @@
 //    thread keep 128 KB of states on their way per SM. 256 sequences, H = 32, K = V = 128:
 //    172 us, 6.3 TB/s (93 % of a copy); tokens_kernel took 214 us there.
 //  - tokens_kernel, any number of tokens: bound by traffic up to a few tokens (48 sequences of 1 to 8
-//    tokens, every state kept: 95 us, 5.9 TB/s), then by the fp32 pipe, which the two-wide
+//    tokens, every state kept: 94 us, 6.0 TB/s), then by the fp32 pipe, which the two-wide
 //    multiply-adds hold for two cycles each, and by the passes' latencies (37 sequences of up to 63
-//    tokens, H = 16, per-channel gates: 79 us; 103 us without the order of ordered_sequence).
-//    A block form over eight tokens (all products with the state first, then a triangular solve in each
-//    lane) and one with the next token's sums formed beside the update both took longer there (113
-//    and 83 us): what they save in waiting they spend in instructions.
+//    tokens, H = 16, per-channel gates: 71 us, the pipe busy for 35 of them; 95 us without the order of
+//    ordered_sequence). A block form over eight tokens (all products with the state first, then a triangular
+//    solve in each lane) and one with the next token's sums formed beside the update both took longer
+//    there: what they save in waiting they spend in instructions.
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -727,11 +727,17 @@ cudaError_t launch(const RecurrentParams& p, bool gate_k, bool bf16, cudaStream_
 // tokens: 16 columns a warp, four of them a lane, when that fills the SMs with twelve warps each; below that
 // 8 columns, one a lane, where a token's sums cross fewer lanes: 18.9 against 25.1 us for two sequences of
 // 8 heads and up to 63 tokens, 51.7 against 47.6 us for 16 of 16 heads, 187 against 115 for 32 of 32 (K = V = 128).
-constexpr int kWideWarpsPerSm = 12;
+// Many tokens a sequence on average and K = V = 128: 32 columns a warp, two blocks an SM, whose exchanges and addresses
+// serve twice the columns: 113 against 119 us for 64 sequences of up to 63 tokens, H = 16 (98 against 94 us for 48
+// of 1 to 8 with every state kept).
+constexpr int kWideWarpsPerSm = 12, kManyTokens = 12;
 template <int K>
-cudaError_t launch_k(const RecurrentParams& p, bool gate_k, bool bf16, int sms, cudaStream_t s) {
+cudaError_t launch_k(const RecurrentParams& p, int average, bool gate_k, bool bf16, int sms, cudaStream_t s) {
     if (p.T == 1 && !p.cu && !p.per_token) return launch<K, 16, 4, true>(p, gate_k, bf16, s);
     const long long warps = (long long)p.nseq * p.H * (p.V / 16);
+    if constexpr (K == 128)
+        if (p.V == 128 && average >= kManyTokens && warps >= (long long)kWideWarpsPerSm * sms)
+            return launch<K, 32, 4, false>(p, gate_k, bf16, s);
     return warps >= (long long)kWideWarpsPerSm * sms ? launch<K, 16, 4, false>(p, gate_k, bf16, s)
                                                      : launch<K, 8, 1, false>(p, gate_k, bf16, s);
 }
@@ -739,7 +745,7 @@ cudaError_t launch_k(const RecurrentParams& p, bool gate_k, bool bf16, int sms, 
 // Each block of the rule looks for other sequences that name its slot when there are at most this many
 // sequences; above it, and where states are kept after every token, claim_kernel does so once.
 constexpr int kInlineSeqs = 512;
-constexpr int kOrderSeqs = 1024, kOrderTokens = 12;
+constexpr int kOrderSeqs = 1024;
 
 gdn_status check(const gdn_problem* p, int Hqk, int nseq, const int* cu, int num_slots, int per_token) {
     if (!p) return GDN_ERR_INVALID_ARG;
@@ -811,10 +817,10 @@ gdn_status gdn_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, const int*
     if (p->T == 1 && !cu_seqlens) per_token = 0;   // the state after the token is the final one
     c.per_token = per_token;
     // The longest sequences first, where there is something to gain: several tokens a sequence on average, and more
-    // blocks than the SMs hold at once. 37 sequences of up to 63 tokens, H = 16: 97 us without, 74 with;
-    // 212 of 1 to 8: 132 without, 138 with.
-    const int average = cu_seqlens ? p->T / nseq : 0;
-    c.ordered = nseq > 1 && nseq <= kOrderSeqs && average >= kOrderTokens &&
+    // blocks than the SMs hold at once. 37 sequences of up to 63 tokens, H = 16: 95 us without, 72 with;
+    // a few tokens each leave less to gain than the sorting costs.
+    const int average = cu_seqlens ? p->T / nseq : p->T;
+    c.ordered = cu_seqlens && nseq > 1 && nseq <= kOrderSeqs && average >= kManyTokens &&
                 (long long)nseq * p->H * (p->V / 64) > 4LL * current_sm_count();
     for (; (4LL * average) >> c.order_shift >= kBuckets; ++c.order_shift) {
     }
@@ -829,8 +835,8 @@ gdn_status gdn_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, const int*
     }
     const bool bf16 = p->in_dtype == GDN_DTYPE_BF16;
     const int sms = current_sm_count();
-    if ((p->K == 64 ? launch_k<64>(c, p->gate_k, bf16, sms, s)
-                    : launch_k<128>(c, p->gate_k, bf16, sms, s)) != cudaSuccess)
+    if ((p->K == 64 ? launch_k<64>(c, average, p->gate_k, bf16, sms, s)
+                    : launch_k<128>(c, average, p->gate_k, bf16, sms, s)) != cudaSuccess)
         return GDN_ERR_CUDA;
     return GDN_OK;
 }

@@ -121,6 +121,8 @@ CASES = {
     "gate_k": ([4, 0, 30, 9], 4, 2, 128, 128, dict(gate_k=True)),
     "gate_k_fp32_k64": ([4, 10, 9], 4, 2, 64, 64, dict(gate_k=True, dtype=F32)),
     "gate_k_large": ([3] * 320, 4, 4, 128, 128, dict(gate_k=True)),
+    "many_tokens_wide": ([30, 2, 17] * 30, 8, 4, 128, 128, {}),
+    "many_tokens_wide_fp32_gate_k": ([24] * 64, 8, 8, 128, 128, dict(gate_k=True, dtype=F32)),
     "no_tokens_at_all": ([0, 0], 2, 1, 128, 128, dict(packed=True)),
     "no_tokens_unpacked": ([0, 0, 0], 2, 1, 64, 64, dict(packed=False)),
     "one_packed": ([10], 2, 1, 128, 128, dict(packed=True)),
