@@ -15,8 +15,14 @@ namespace norm {
 
 // A row of N values belongs to a group of G threads: a part of a warp (G <= 32, a power of two) or a whole
 // block; every thread holds R times eight of its values: one up to N = 256, two beyond (what a row costs besides its
-// values -- the exchange, the addresses -- is then shared by twice as many). Where N % 8 == 0 the eight are consecutive and move as vectors (16-byte aligned rows); else they are G apart, so
-// that a warp's single accesses still cover consecutive values.
+// values -- the exchange, the addresses -- is then shared by twice as many). How the eight lie, L:
+//  8  side by side, 16 bytes of bf16 an access; N % 8 == 0, all types bf16
+//  4  two fours, 4 G apart: 16 bytes of fp32 or 8 of bf16 an access, a warp's side by side (with eight side by
+//     side fp32 leaves every other 16 bytes to the next access: 87 against 73 us for 29200 rows of 2000);
+//     N % 4 == 0
+//  2  four pairs, 2 G apart, for any N. With N odd every other row starts between two pairs' places; a group takes
+//     rows of one kind only, and on the odd ones its pairs start one column earlier (the first one's first
+//     value is none).
 struct Params {
     const void* x;
     const float* w;      // null: ones
@@ -36,22 +42,22 @@ constexpr int kMaxN = 8192;
 constexpr int kMaxThreads = 512;
 constexpr int kSmBound = 256;           // SMs of any device that sizes a workspace
 
-// The first column of thread t's i-th eight values, and the distance between them.
-template <bool VEC>
-__device__ __forceinline__ int first_col(int i, int t, int G) {
-    return VEC ? (i * G + t) * 8 : i * 8 * G + t;
+// The first column of thread t's i-th eight values (-1: none), and the column of its e-th value; odd: the row starts at
+// an odd value.
+template <int L>
+__device__ __forceinline__ int first_col(int i, int t, int G, int odd) {
+    return L * (i * (8 / L) * G + t) - (L == 2 ? odd : 0);
 }
-template <bool VEC>
-__device__ __forceinline__ int col_step(int G) {
-    return VEC ? 1 : G;
-}
+template <int L>
+__device__ __forceinline__ int col_of(int c, int G, int e) { return c + (e / L) * L * G + e % L; }
+__device__ __forceinline__ bool has(int col, int n) { return (unsigned)col < (unsigned)n; }
 
 // Whether any lane of this thread's warp has columns among the i-th eights. (The forward leaves out those that
 // have none: 45 -> 40 us for 29200 rows of 2000 in bf16; the backward, whose registers are full, took longer with
 // such branches, 63 -> 78 us.)
-template <bool VEC>
+template <int L>
 __device__ __forceinline__ bool warp_has(int i, int t, int G, int n) {
-    return i == 0 || first_col<VEC>(i, t & ~31, G) < n;
+    return i == 0 || first_col<L>(i, t & ~31, G, 0) < n + 1;
 }
 
 __device__ __forceinline__ pair_t both(float x) { return pack(x, x); }
@@ -65,12 +71,12 @@ __device__ __forceinline__ void single(const pair_t (&p)[4], float (&f)[8]) {
     for (int i = 0; i < 4; ++i) unpack(p[i], f[2 * i], f[2 * i + 1]);
 }
 // a parameter's eight values of this thread's columns
-template <bool VEC>
-__device__ __forceinline__ void parameter(pair_t (&f)[4], const float* from, int c, int step, int n, float none) {
+template <int L>
+__device__ __forceinline__ void parameter(pair_t (&f)[4], const float* from, int c, int G, int n, float none) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = both(none);
     if (!from) return;
-    if constexpr (VEC) {
+    if constexpr (L == 8) {
         if (c >= n) return;
         const float4 a = __ldg(reinterpret_cast<const float4*>(from + c));
         const float4 b = __ldg(reinterpret_cast<const float4*>(from + c + 4));
@@ -78,48 +84,79 @@ __device__ __forceinline__ void parameter(pair_t (&f)[4], const float* from, int
         f[1] = pack(a.z, a.w);
         f[2] = pack(b.x, b.y);
         f[3] = pack(b.z, b.w);
+    } else if constexpr (L == 4) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c0 = col_of<L>(c, G, 4 * k);
+            if (c0 >= n) continue;
+            const float4 a = __ldg(reinterpret_cast<const float4*>(from + c0));
+            f[2 * k] = pack(a.x, a.y);
+            f[2 * k + 1] = pack(a.z, a.w);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c0 = c + 2 * i * step, c1 = c0 + step;
-            f[i] = pack(c0 < n ? __ldg(from + c0) : none, c1 < n ? __ldg(from + c1) : none);
+            const int c0 = col_of<L>(c, G, 2 * i);
+            f[i] = pack(has(c0, n) ? __ldg(from + c0) : none, has(c0 + 1, n) ? __ldg(from + c0 + 1) : none);
         }
     }
 }
 
-template <bool BF, bool VEC>
-__device__ __forceinline__ void store8(void* base, long long row0, int c, int step, int n, const float (&f)[8]) {
-    if constexpr (VEC) {
-        if (c >= n) return;
-        uint4* p = reinterpret_cast<uint4*>((char*)base + (row0 + c) * (BF ? 2 : 4));
-        if constexpr (BF) {
-            unsigned a[4];
+__device__ __forceinline__ unsigned bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const unsigned*>(&h);
+}
+
+template <bool BF, int L>
+__device__ __forceinline__ void store8(void* base, long long row0, int c, int G, int n, const float (&f)[8]) {
+    if constexpr (L == 8) {
+        static_assert(BF, "eight side by side are bf16");
+        if (c < n)
+            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + row0 + c) =
+                make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+    } else if constexpr (L == 4) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                a[i] = *reinterpret_cast<const unsigned*>(&h);
-            }
-            __stcs(p, make_uint4(a[0], a[1], a[2], a[3]));
-        } else {
-            __stcs(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                 __float_as_uint(f[3])));
-            __stcs(p + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
-                                     __float_as_uint(f[7])));
+        for (int k = 0; k < 2; ++k) {
+            const int c0 = col_of<4>(c, G, 4 * k);
+            if (c0 >= n) continue;
+            if constexpr (BF)
+                *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(base) + row0 + c0) =
+                    make_uint2(bf16_pair(f[4 * k], f[4 * k + 1]), bf16_pair(f[4 * k + 2], f[4 * k + 3]));
+            else
+                *reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + row0 + c0) =
+                    make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
         }
     } else {
-        auto one = [&](int e) {
-            if constexpr (BF)
-                reinterpret_cast<__nv_bfloat16*>(base)[row0 + c + e * step] = __float2bfloat16_rn(f[e]);
-            else
-                reinterpret_cast<float*>(base)[row0 + c + e * step] = f[e];
-        };
-        if (step > 32 && c + 7 * step < n) {   // (as they are read)
+        // (bf16 rows of more than 512: 53 -> 46 us for 29200 rows of 1999; the other ones lose by the branch)
+        if (BF && G > 32 && c >= 0 && c + 6 * G + 1 < n) {   // all but the row's ends, without a look at each
 #pragma unroll
-            for (int e = 0; e < 8; ++e) one(e);
-        } else {
+            for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(base) + row0 + c + 2 * k * G) =
+                    __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+            return;
+        }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e * step < n) one(e);
+        for (int k = 0; k < 4; ++k) {
+            const int c0 = c + 2 * k * G;
+            const long long at = row0 + c0;   // even
+            if constexpr (BF) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+                __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(base) + at;
+                if (has(c0, n) && c0 + 1 < n)
+                    *reinterpret_cast<__nv_bfloat162*>(to) = h;
+                else if (has(c0, n))
+                    to[0] = h.x;
+                else if (has(c0 + 1, n))
+                    to[1] = h.y;
+            } else {
+                float* to = reinterpret_cast<float*>(base) + at;
+                if (has(c0, n) && c0 + 1 < n)
+                    *reinterpret_cast<float2*>(to) = make_float2(f[2 * k], f[2 * k + 1]);
+                else if (has(c0, n))
+                    to[0] = f[2 * k];
+                else if (has(c0 + 1, n))
+                    to[1] = f[2 * k + 1];
+            }
         }
     }
 }
@@ -137,58 +174,60 @@ __device__ __forceinline__ void group_barrier() {
 }
 
 // Rows on their way: a ring of kDepth stages in shared memory, filled by asynchronous 16-byte copies kDepth - 1
-// rows ahead, so that an SM has some 100 KB under way whatever the registers allow. Vectors: every thread
-// copies and reads its own pieces, and needs no one else. Odd row lengths: a row starts anywhere within 16
-// bytes, so the group copies the aligned pieces that cover it (the last one of the tensor cut short at its
-// end) and reads single values at the row's offset, after a barrier.
-template <bool VEC, int R, bool... BF>
+// rows ahead, so that an SM has enough under way whatever the registers allow: about AHEAD pieces of 16 bytes a
+// thread. L = 8 and 4: every thread copies and reads its own pieces, and needs no one else. L = 2: a row starts
+// anywhere within 16 bytes, so the group copies the aligned pieces that cover it (the last one of the tensor cut short
+// at its end) and reads pairs at the row's offset, after a barrier.
+template <int L, int R, int AHEAD, bool... BF>
 struct Ring {
+    static constexpr bool kOwn = L != 2;   // a thread reads what it copied
     static constexpr bool kBf[] = {BF...};
     static constexpr int kTensors = sizeof...(BF);
     static constexpr int es(int t) { return kBf[t] ? 2 : 4; }
     static constexpr int pieces(int t) { return R * es(t) / 2; }   // of a thread
     static constexpr int first_piece(int t) { return t == 0 ? 0 : first_piece(t - 1) + pieces(t - 1); }
     static constexpr int kPieces = first_piece(kTensors - 1) + pieces(kTensors - 1);
-    static constexpr int kAhead = 12 / kPieces < 1 ? 1 : 12 / kPieces > 6 ? 6 : 12 / kPieces;   // 192 B a thread
+    static constexpr int kAhead = AHEAD / kPieces < 1 ? 1 : AHEAD / kPieces > 6 ? 6 : AHEAD / kPieces;   // rows
     static constexpr int kDepth = kAhead + 1;
-    static constexpr int kSlack = 2;   // odd rows: pieces more than the values take, a group and tensor
+    static constexpr int kSlack = 2;   // L = 2: pieces more than the values take, a group and tensor
     static constexpr int bytes(int threads, int G) {
-        return VEC ? kDepth * kPieces * threads * 16
+        return kOwn ? kDepth * kPieces * threads * 16
                    : kDepth * (kPieces * threads + kSlack * kTensors * (threads / G)) * 16;
     }
 
     unsigned base;   // shared memory
-    int G, t, tid, threads, N;
+    int G, t, tid, threads, N, odd;
     long long rows;
 
     template <int T>
-    __device__ __forceinline__ unsigned region(int stage) const {   // odd rows: of this group
+    __device__ __forceinline__ unsigned region(int stage) const {   // L = 2: of this group
         constexpr int kFirst = first_piece(T), kMine = pieces(T);
         const int groups = threads / G;
         return base + 16u * (stage * (kPieces * threads + kSlack * kTensors * groups) +
                              (kFirst * threads + kSlack * T * groups) + (tid / G) * (kMine * G + kSlack));
     }
     template <int T>
-    __device__ __forceinline__ unsigned piece(int stage, int k) const {   // vectors: of this thread
+    __device__ __forceinline__ unsigned piece(int stage, int k) const {   // of this thread
         constexpr int kFirst = first_piece(T);
         return base + 16u * ((stage * kPieces + kFirst + k) * threads + tid);
     }
+    template <int BYTES>
     static __device__ __forceinline__ void copy(unsigned to, const void* from, int n) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(BYTES), "r"(n) : "memory");
     }
     template <int T>
     __device__ __forceinline__ void fetch(int stage, const void* from, long long row) const {
         constexpr int E = es(T);
         const char* src = reinterpret_cast<const char*>(from);
-        if constexpr (VEC) {
-            const int c = first_col<true>(0, t, G);
+        if constexpr (kOwn) {
+            constexpr int B = L * E < 16 ? L * E : 16;   // of a copy: 16, or 8 for four of bf16
+            const int c = first_col<L>(0, t, G, 0);
             const char* at = src + (row * N + c) * E;
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const bool in = c + i * 8 * G < N && row < rows;
-#pragma unroll
-                for (int k = 0; k < E / 2; ++k)
-                    copy(piece<T>(stage, i * (E / 2) + k), in ? at + i * 8 * G * E + 16 * k : src, in ? 16 : 0);
+            for (int j = 0; j < R * 8 / L; ++j) {   // L columns each, L G apart
+                const bool in = c + j * L * G < N && row < rows;
+                static_assert(L * E <= 16, "one copy");
+                copy<B>(piece<T>(stage, j * B / 16) + j * B % 16, in ? at + j * L * G * E : src, in ? B : 0);
             }
         } else if (row < rows) {
             const long long lo = row * N * E, a = lo & ~15LL;
@@ -198,21 +237,21 @@ struct Ring {
             const unsigned to = region<T>(stage) + 16u * t;
 #pragma unroll
             for (int j = 0; j <= pieces(T); ++j)
-                if (t + j * G < n) copy(to + 16u * j * G, at + 16 * j * G, min(16, left - 16 * (t + j * G)));
+                if (t + j * G < n) copy<16>(to + 16u * j * G, at + 16 * j * G, min(16, left - 16 * (t + j * G)));
         }
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-    // the oldest row's copies are complete (and, odd rows, everyone's; also, everyone has read the row before)
+    // the oldest row's copies are complete (and, L = 2, everyone's; also, everyone has read the row before)
     template <int GB, int BLOCK>
     static __device__ __forceinline__ void wait() {
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-        if constexpr (!VEC) group_barrier<GB, BLOCK>();
+        if constexpr (!kOwn) group_barrier<GB, BLOCK>();
     }
     // this thread's i-th eight of a staged row
     template <int T>
     __device__ __forceinline__ void read(int stage, int i, long long row, float (&f)[8]) const {
         constexpr int E = es(T);
-        if constexpr (VEC) {
+        if constexpr (kOwn) {
             unsigned u[E * 2];
 #pragma unroll
             for (int k = 0; k < E / 2; ++k)
@@ -224,26 +263,36 @@ struct Ring {
                 f[e] = E == 4 ? __uint_as_float(u[E == 4 ? e : 0])
                               : __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
         } else {
-            const int c = first_col<false>(i, t, G), n = row < rows ? N : 0;
+            const int c = first_col<2>(i, t, G, odd), step = 2 * G, n = row < rows ? N : 0;
             const unsigned at = region<T>(stage) + (unsigned)((row * N * E) & 15) + E * c;
-            auto one = [&](int e) {
-                if constexpr (E == 2) {
-                    unsigned short h;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + 2u * e * G));
-                    f[e] = __uint_as_float((unsigned)h << 16);
-                } else {
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[e]) : "r"(at + 4u * e * G));
-                }
-            };
-            if (G > 32 && c + 7 * G < n) {   // all but the row's last ones, without a look at each
+            if constexpr (E == 2) {
+                if (step > 64 && c >= 0 && c + 3 * step + 1 < n) {   // (as they are written)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) one(e);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    f[e] = 0.f;
-                    if (c + e * G < n) one(e);
+                    for (int k = 0; k < 4; ++k) {
+                        unsigned u;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(at + 2u * k * step));
+                        f[2 * k] = __uint_as_float(u << 16);
+                        f[2 * k + 1] = __uint_as_float(u & 0xffff0000u);
+                    }
+                    return;
                 }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {   // (an end pair's other value is another row's)
+                const int c0 = c + k * step;
+                float lo = 0.f, hi = 0.f;
+                if (c0 < n) {
+                    if constexpr (E == 2) {
+                        unsigned u;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(at + 2u * k * step));
+                        lo = __uint_as_float(u << 16);
+                        hi = __uint_as_float(u & 0xffff0000u);
+                    } else {
+                        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(lo), "=f"(hi) : "r"(at + 4u * k * step));
+                    }
+                }
+                f[2 * k] = has(c0, n) ? lo : 0.f;
+                f[2 * k + 1] = c0 + 1 < n ? hi : 0.f;
             }
         }
     }
@@ -324,12 +373,10 @@ __device__ __forceinline__ float sigmoid(float z) {
 
 // How a call is laid out: threads of a row (8 to 512), eights of a thread.
 struct Shape {
-    bool vec;
     int g, r;
 };
 inline Shape shape_of(int N) {
     Shape s{};
-    s.vec = N % 8 == 0;
     const int eights = (N + 7) / 8;
     s.r = eights > 32 ? 2 : 1;
     s.g = 8;
@@ -337,10 +384,11 @@ inline Shape shape_of(int N) {
     return s;
 }
 
-// blocks (of kMaxThreads threads, one an SM) of the backward on `sms` SMs, at most
+// blocks (of kMaxThreads threads, one an SM) of the backward on `sms` >= 2 SMs
 inline long long bwd_blocks(long long rows, const Shape& s, int sms) {
     const long long per = kMaxThreads / s.g, need = (rows + per - 1) / per;
-    return need < sms ? need : sms;
+    if (need <= sms) return need;
+    return per == 1 ? sms & ~1 : sms;   // (an even number of rows at once: a group's rows start alike)
 }
 
 // Blocks of a kernel that are on an SM at once with `smem` bytes each, asked (and the shared memory allowed) once for

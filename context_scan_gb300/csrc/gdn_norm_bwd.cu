@@ -27,15 +27,41 @@ __device__ __forceinline__ void gate(pair_t& d, pair_t& dyg, pair_t z) {
     d = mul2(dsg, z);
 }
 
+// Eight columns' sums to shared memory, 16 bytes a store where the columns allow. (One by one, eight side by side
+// would meet in the same banks: 2 us at 2048 columns. So do the lanes t and t + 4 that put their first fours at the
+// same time, so one of them begins with its second.)
+template <int L>
+__device__ __forceinline__ void put_sums(float* to, int c, int G, int n, const float (&f)[8], int t) {
+    if constexpr (L == 2) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int col = col_of<L>(c, G, e);
+            if (has(col, n)) to[col] = f[e];
+        }
+    } else {
+        const int turn = L == 8 ? (t >> 2) & 1 : 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const bool second = k != turn;
+            const int col = second ? col_of<L>(c, G, 4) : c;
+            if (col < n)
+                *reinterpret_cast<float4*>(to + col) = second ? make_float4(f[4], f[5], f[6], f[7])
+                                                              : make_float4(f[0], f[1], f[2], f[3]);
+        }
+    }
+}
+
 // A block of kMaxThreads threads; GB of them to a row, 0: a part of a warp (rows of at most 512 values)
-template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
+template <int GB, int R, int L, bool XB, bool YB, bool GATED>
 struct Bwd {
-    using Rows = std::conditional_t<GATED, Ring<VEC, R, XB, YB, YB>, Ring<VEC, R, XB, YB>>;
+    // (29200 rows of 2000 in bf16: 68.0, 67.9, 62.4, 63.9 and 67.0 us with 4, 6, 8, 12 and 20)
+    static constexpr int kAhead = 8;
+    using Rows = std::conditional_t<GATED, Ring<L, R, kAhead, XB, YB, YB>, Ring<L, R, kAhead, XB, YB>>;
 };
 
-template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
+template <int GB, int R, int L, bool XB, bool YB, bool GATED>
 __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
-    using Rows = typename Bwd<GB, R, VEC, XB, YB, GATED>::Rows;
+    using Rows = typename Bwd<GB, R, L, XB, YB, GATED>::Rows;
     extern __shared__ __align__(16) char stages[];
     __shared__ float parts[GB ? kMaxThreads / GB : 1][2][64];
     float(*part)[64] = parts[GB ? threadIdx.x / GB : 0];
@@ -46,12 +72,12 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
     const int rows_block = kMaxThreads / G;               // rows a block holds at once, and a warp
     const int rows_warp = GB ? 1 : 32 / G;
     const int sub = GB ? 0 : (threadIdx.x & 31) / G;      // which of the warp's is this thread's
-    const int step = col_step<VEC>(G);
     const long long stride = (long long)gridDim.x * rows_block;
     // (the trip count is the same for all threads of a warp, and of a group)
     long long row0 = (long long)blockIdx.x * rows_block + (GB ? threadIdx.x / G : (threadIdx.x >> 5) * rows_warp);
 
-    const Rows ring{(unsigned)__cvta_generic_to_shared(stages), G, t, (int)threadIdx.x, kMaxThreads, p.N, p.rows};
+    const int odd = L == 2 ? (int)((row0 + sub) * p.N & 1) : 0;
+    const Rows ring{(unsigned)__cvta_generic_to_shared(stages), G, t, (int)threadIdx.x, kMaxThreads, p.N, odd, p.rows};
     auto fetch = [&](int stage, long long row) {
         ring.template fetch<0>(stage, p.x, row);
         ring.template fetch<1>(stage, p.dy, row);
@@ -62,8 +88,8 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
     for (int k = 0; k < Rows::kAhead; ++k) fetch(k, row0 + sub + k * stride);
     pair_t w[4], b[4], dw2[R][4] = {}, db2[R][4] = {};
     if constexpr (R == 1) {
-        parameter<VEC>(w, p.w, first_col<VEC>(0, t, G), step, p.N, 1.f);
-        if constexpr (GATED) parameter<VEC>(b, p.b, first_col<VEC>(0, t, G), step, p.N, 0.f);
+        parameter<L>(w, p.w, first_col<L>(0, t, G, odd), G, p.N, 1.f);
+        if constexpr (GATED) parameter<L>(b, p.b, first_col<L>(0, t, G, odd), G, p.N, 0.f);
     }
     for (int stage = 0; row0 < p.rows; row0 += stride, stage = stage == Rows::kAhead ? 0 : stage + 1) {
         const long long row = row0 + sub;
@@ -81,7 +107,7 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) gate(d[i][k], dyg[i][k], z[k]);
             }
-            if constexpr (R > 1) parameter<VEC>(w, p.w, first_col<VEC>(i, t, G), step, p.N, 1.f);
+            if constexpr (R > 1) parameter<L>(w, p.w, first_col<L>(i, t, G, odd), G, p.N, 1.f);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 dxh[i][k] = mul2(d[i][k], w[k]);
@@ -109,12 +135,12 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
                 float q[2] = {0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                            float v[8], f[8];
+                    float v[8], f[8];
                     single(x[i], v);
                     single(dxh[i], f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float xm = first_col<VEC>(i, t, G) + e * step < p.N ? v[e] - mean : 0.f;
+                        const float xm = has(col_of<L>(first_col<L>(i, t, G, odd), G, e), p.N) ? v[e] - mean : 0.f;
                         q[0] = fmaf(xm, xm, q[0]);
                         q[1] = fmaf(f[e], xm, q[1]);
                     }
@@ -132,10 +158,10 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
         const int n = row < p.rows ? p.N : 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int c = first_col<VEC>(i, t, G);
+            const int c = first_col<L>(i, t, G, odd);
             if constexpr (R > 1 && GATED) {
-                parameter<VEC>(w, p.w, c, step, p.N, 1.f);
-                parameter<VEC>(b, p.b, c, step, p.N, 0.f);
+                parameter<L>(w, p.w, c, G, p.N, 1.f);
+                parameter<L>(b, p.b, c, G, p.N, 0.f);
             }
             float out[8];
 #pragma unroll
@@ -147,48 +173,36 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
                 x[i][k] = fma2(xh, along, fma2(dxh[i][k], scale, level_d));
             }
             single(x[i], out);
-            store8<XB, VEC>(p.y, row * p.N, c, step, n, out);
+            store8<XB, L>(p.y, row * p.N, c, G, n, out);
             if constexpr (GATED)
                 if (p.dz) {
                     single(dyg[i], out);
-                    store8<YB, VEC>(p.dz, row * p.N, c, step, n, out);
+                    store8<YB, L>(p.dz, row * p.N, c, G, n, out);
                 }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!p.partial) return;
-    // dw, db over the block's rows: first the rows of a warp, by exchange, then those of its warps or groups, through
-    // shared memory (the stages, which are not needed any more)
-    constexpr int kSets = GB ? kMaxThreads / GB : kMaxThreads / 32, kCols = (GB ? GB : 32) * 8 * R;
-    float(*sum)[2][kCols] = reinterpret_cast<float(*)[2][kCols]>(stages);
-    const int set = threadIdx.x / (GB ? GB : 32);
+    // dw, db over the rows of the block's groups, through shared memory (the stages, which are not needed any more)
+    const int width = 8 * R * G, set = threadIdx.x / G;
+    float* sum = reinterpret_cast<float*>(stages);   // [groups][2][width]
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int c = first_col<VEC>(i, t, G);
+        const int c = first_col<L>(i, t, G, odd);
         float dw[8], db[8];
         single(dw2[i], dw);
         single(db2[i], db);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (GB == 0)
-                for (int off = 16; off >= G; off >>= 1) {
-                    dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], off);
-                    db[e] += __shfl_xor_sync(0xffffffffu, db[e], off);
-                }
-            if (sub == 0) {
-                sum[set][0][c + e * step] = dw[e];
-                sum[set][1][c + e * step] = db[e];
-            }
-        }
+        put_sums<L>(sum + 2 * set * width, c, G, p.N, dw, t);
+        put_sums<L>(sum + (2 * set + 1) * width, c, G, p.N, db, t);
     }
     __syncthreads();
     float* out = p.partial + (long long)blockIdx.x * 2 * p.N;
     for (int i = threadIdx.x; i < 2 * p.N; i += kMaxThreads) {
         const int which = i >= p.N, col = which ? i - p.N : i;
         float a = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSets; ++k) a += sum[k][which][col];
+#pragma unroll 4
+        for (int k = 0; k < rows_block; ++k) a += sum[(2 * k + which) * width + col];
         out[i] = a;
     }
 }
@@ -228,36 +242,36 @@ __global__ void __launch_bounds__(1024) columns_kernel(const float* partial, int
     if (lane == 0 && col < N) out[col] = a;
 }
 
-template <int GB, int R, bool VEC, bool XB, bool YB, bool GATED>
+template <int GB, int R, int L, bool XB, bool YB, bool GATED>
 cudaError_t bwd(const Params& p, const Shape& s, int blocks, cudaStream_t st) {
-    using Rows = typename Bwd<GB, R, VEC, XB, YB, GATED>::Rows;
-    static_assert(Rows::bytes(kMaxThreads, 32) >= kMaxThreads * 8 * R * 2 * 4, "the sums fit where the rows were");
+    using Rows = typename Bwd<GB, R, L, XB, YB, GATED>::Rows;
     static std::atomic<int> known[kDevices];
-    const auto kernel = bwd_kernel<GB, R, VEC, XB, YB, GATED>;
-    const int smem = Rows::bytes(kMaxThreads, s.g);
+    const auto kernel = bwd_kernel<GB, R, L, XB, YB, GATED>;
+    const int smem = std::max(Rows::bytes(kMaxThreads, s.g), kMaxThreads * 8 * R * 2 * (int)sizeof(float));   // (the sums at the end)
     if (resident_blocks(kernel, kMaxThreads, smem, known) < 1) return cudaErrorLaunchOutOfResources;
     kernel<<<blocks, kMaxThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
-template <int GB, int R, bool VEC>
+template <int GB, int R, int L>
 cudaError_t bwd_types(const Params& p, const Shape& s, bool xb, bool yb, int blocks, cudaStream_t st) {
-    if (p.z) {
+    if (xb && yb)
+        return p.z ? bwd<GB, R, L, true, true, true>(p, s, blocks, st) : bwd<GB, R, L, true, true, false>(p, s, blocks, st);
+    if constexpr (L < 8) {
         if (xb)
-            return yb ? bwd<GB, R, VEC, true, true, true>(p, s, blocks, st)
-                      : bwd<GB, R, VEC, true, false, true>(p, s, blocks, st);
-        return yb ? bwd<GB, R, VEC, false, true, true>(p, s, blocks, st)
-                  : bwd<GB, R, VEC, false, false, true>(p, s, blocks, st);
+            return p.z ? bwd<GB, R, L, true, false, true>(p, s, blocks, st)
+                       : bwd<GB, R, L, true, false, false>(p, s, blocks, st);
+        if (yb)
+            return p.z ? bwd<GB, R, L, false, true, true>(p, s, blocks, st)
+                       : bwd<GB, R, L, false, true, false>(p, s, blocks, st);
+        return p.z ? bwd<GB, R, L, false, false, true>(p, s, blocks, st)
+                   : bwd<GB, R, L, false, false, false>(p, s, blocks, st);
     }
-    if (xb)
-        return yb ? bwd<GB, R, VEC, true, true, false>(p, s, blocks, st)
-                  : bwd<GB, R, VEC, true, false, false>(p, s, blocks, st);
-    return yb ? bwd<GB, R, VEC, false, true, false>(p, s, blocks, st)
-              : bwd<GB, R, VEC, false, false, false>(p, s, blocks, st);
+    return cudaErrorInvalidValue;
 }
 template <int GB, int R>
-cudaError_t bwd_vec(const Params& p, const Shape& s, bool xb, bool yb, int blocks, cudaStream_t st) {
-    return s.vec ? bwd_types<GB, R, true>(p, s, xb, yb, blocks, st)
-                 : bwd_types<GB, R, false>(p, s, xb, yb, blocks, st);
+cudaError_t bwd_layout(const Params& p, const Shape& s, bool xb, bool yb, int blocks, cudaStream_t st) {
+    if (p.N % 8 == 0 && xb && yb) return bwd_types<GB, R, 8>(p, s, xb, yb, blocks, st);
+    return p.N % 4 == 0 ? bwd_types<GB, R, 4>(p, s, xb, yb, blocks, st) : bwd_types<GB, R, 2>(p, s, xb, yb, blocks, st);
 }
 
 }  // namespace
@@ -268,12 +282,12 @@ cudaError_t launch_bwd(const Params& p_in, const Shape& s, bool xb, bool yb, int
     if (!dw && !db) p.partial = nullptr;
     const int blocks = (int)bwd_blocks(p.rows, s, sms);
     if (blocks > 0) {
-        const cudaError_t e = s.g <= 32    ? (s.r == 1 ? bwd_vec<0, 1>(p, s, xb, yb, blocks, st)
-                                                       : bwd_vec<0, 2>(p, s, xb, yb, blocks, st))
-                              : s.g == 64  ? bwd_vec<64, 2>(p, s, xb, yb, blocks, st)
-                              : s.g == 128 ? bwd_vec<128, 2>(p, s, xb, yb, blocks, st)
-                              : s.g == 256 ? bwd_vec<256, 2>(p, s, xb, yb, blocks, st)
-                                           : bwd_vec<512, 2>(p, s, xb, yb, blocks, st);
+        const cudaError_t e = s.g <= 32    ? (s.r == 1 ? bwd_layout<0, 1>(p, s, xb, yb, blocks, st)
+                                                       : bwd_layout<0, 2>(p, s, xb, yb, blocks, st))
+                              : s.g == 64  ? bwd_layout<64, 2>(p, s, xb, yb, blocks, st)
+                              : s.g == 128 ? bwd_layout<128, 2>(p, s, xb, yb, blocks, st)
+                              : s.g == 256 ? bwd_layout<256, 2>(p, s, xb, yb, blocks, st)
+                                           : bwd_layout<512, 2>(p, s, xb, yb, blocks, st);
         if (e != cudaSuccess) return e;
     }
     if (!p.partial) return cudaSuccess;

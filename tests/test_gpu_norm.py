@@ -114,7 +114,7 @@ def compare(d, rms, xt, yt):
 # single values; more rows than one round of the grid holds
 SIZES = [(1, 1), (5, 2), (3, 7), (9, 8), (33, 40), (700, 64), (257, 100), (1000, 128), (12, 129), (3000, 16),
          (77, 255), (400, 256), (5, 257), (64, 512), (41, 1000), (300, 1999), (700, 2048), (3, 4095),
-         (170, 4096), (9, 4097), (400, 5000), (5, 8191), (330, 8192), (12000, 128), (2600, 300)]
+         (170, 4096), (9, 4097), (400, 5000), (5, 8191), (330, 8192), (12000, 128), (2600, 300), (50, 20), (61, 1996), (40, 1998)]
 
 
 @pytest.mark.parametrize("rms", [True, False])
@@ -126,7 +126,8 @@ def test_fp32_in_bf16_out(rows, n, gated, rms):
 
 
 @pytest.mark.parametrize("xt,yt", [(BF, BF), (BF, F32), (F32, F32)])
-@pytest.mark.parametrize("rows,n", [(37, 128), (65, 96), (20, 131), (33, 1032), (17, 999), (9, 6000), (7, 4999)])
+@pytest.mark.parametrize("rows,n", [(37, 128), (65, 96), (20, 131), (33, 1032), (17, 999), (9, 6000), (7, 4999),
+                                    (50, 20), (61, 1996), (40, 1998), (400, 2001), (700, 125)])
 def test_types(rows, n, xt, yt):
     for gated in (True, False):
         for rms in (True, False):
