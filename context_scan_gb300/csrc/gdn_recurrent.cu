@@ -727,10 +727,15 @@ cudaError_t launch(const RecurrentParams& p, bool gate_k, bool bf16, cudaStream_
 // tokens: 16 columns a warp, four of them a lane, when that fills the SMs with twelve warps each; below that
 // 8 columns, one a lane, where a token's sums cross fewer lanes: 18.9 against 25.1 us for two sequences of
 // 8 heads and up to 63 tokens, 51.7 against 47.6 us for 16 of 16 heads, 187 against 115 for 32 of 32 (K = V = 128).
+// Few warps: a token's time is then one warp's chain of instructions, which is shorter with fewer rows a lane although the
+// sums cross more lanes. 8, 4 and 2 columns, one a lane, K = V = 128, 63 tokens, cold: 29.2, 27.1 and 25.1 us for one sequence
+// of 8 heads, 27.1, 25.1 and 25.1 for two, 33.3, 33.3 and 41.5 for eight (of up to 63), 45.6, 47.6 and 64.0 for eight of 16
+// heads; 39.4, 37.3 and 31.2 us for five of 130 tokens, 2 heads, K = V = 64.
 // Many tokens a sequence on average and K = V = 128: 32 columns a warp, two blocks an SM, whose exchanges and addresses
 // serve twice the columns: 113 against 119 us for 64 sequences of up to 63 tokens, H = 16 (98 against 94 us for 48
 // of 1 to 8 with every state kept).
 constexpr int kWideWarpsPerSm = 12, kManyTokens = 12;
+constexpr int kQuarterWarpsPerSm = 8, kEighthWarpsPerSm = 4;   // of 4 and 2 columns, at most
 template <int K>
 cudaError_t launch_k(const RecurrentParams& p, int average, bool gate_k, bool bf16, int sms, cudaStream_t s) {
     if (p.T == 1 && !p.cu && !p.per_token) return launch<K, 16, 4, true>(p, gate_k, bf16, s);
@@ -738,8 +743,10 @@ cudaError_t launch_k(const RecurrentParams& p, int average, bool gate_k, bool bf
     if constexpr (K == 128)
         if (p.V == 128 && average >= kManyTokens && warps >= (long long)kWideWarpsPerSm * sms)
             return launch<K, 32, 4, false>(p, gate_k, bf16, s);
-    return warps >= (long long)kWideWarpsPerSm * sms ? launch<K, 16, 4, false>(p, gate_k, bf16, s)
-                                                     : launch<K, 8, 1, false>(p, gate_k, bf16, s);
+    if (warps >= (long long)kWideWarpsPerSm * sms) return launch<K, 16, 4, false>(p, gate_k, bf16, s);
+    if (8 * warps <= (long long)kEighthWarpsPerSm * sms) return launch<K, 2, 1, false>(p, gate_k, bf16, s);
+    if (4 * warps <= (long long)kQuarterWarpsPerSm * sms) return launch<K, 4, 1, false>(p, gate_k, bf16, s);
+    return launch<K, 8, 1, false>(p, gate_k, bf16, s);
 }
 
 // Each block of the rule looks for other sequences that name its slot when there are at most this many

@@ -125,6 +125,14 @@ CASES = {
     "many_tokens_wide_fp32_gate_k": ([24] * 64, 8, 8, 128, 128, dict(gate_k=True, dtype=F32)),
     "no_tokens_at_all": ([0, 0], 2, 1, 128, 128, dict(packed=True)),
     "no_tokens_unpacked": ([0, 0, 0], 2, 1, 64, 64, dict(packed=False)),
+    # (2, 4 and 8 columns a warp by the number of warps, on some 150 SMs)
+    "few_gate_k": ([9, 31], 3, 1, 128, 128, dict(gate_k=True)),
+    "few_fp32": ([25], 8, 8, 128, 128, dict(dtype=F32)),
+    "some_k64": ([5, 16, 33, 0, 12], 5, 1, 64, 64, dict(gate_k=True)),
+    "some_k128_v64": ([5, 16, 33, 0, 12], 8, 2, 128, 64, {}),
+    "some_fp32": ([40, 7], 16, 8, 128, 128, dict(dtype=F32)),
+    "more_k64": ([8, 3, 17, 26] * 5, 4, 4, 64, 64, {}),
+    "more_gate_k": ([8, 3, 17, 26] * 2, 8, 2, 128, 128, dict(gate_k=True)),
     "one_packed": ([10], 2, 1, 128, 128, dict(packed=True)),
 }
 
