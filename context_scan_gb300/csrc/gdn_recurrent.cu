@@ -12,18 +12,20 @@
 // Every column of the state is independent given k, q and the gates. A warp owns CW columns of one
 // head, all K rows of them in registers (Tile below), so the state is read from memory once, when the
 // sequence starts, and written once, when it ends (or after every token when the caller keeps
-// them all). Two kernels, whose measurements stand beside the rule that picks the split (launch_k):
+// them all). Three kernels, whose measurements stand beside the rule that picks one (launch_k):
 //  - decode_kernel, one token a sequence: bound by the memory traffic of the states. A warp needs
 //    nothing of another one, so it waits for nothing but its own loads; four blocks of 128 registers a
 //    thread keep 128 KB of states on their way per SM. 256 sequences, H = 32, K = V = 128:
 //    172 us, 6.3 TB/s (93 % of a copy); tokens_kernel took 214 us there.
-//  - tokens_kernel, any number of tokens: bound by traffic up to a few tokens (48 sequences of 1 to 8
-//    tokens, every state kept: 94 us, 6.0 TB/s), then by the fp32 pipe, which the two-wide
-//    multiply-adds hold for two cycles each, and by the passes' latencies (37 sequences of up to 63
-//    tokens, H = 16, per-channel gates: 71 us, the pipe busy for 35 of them; 95 us without the order of
-//    ordered_sequence). A block form over eight tokens (all products with the state first, then a triangular
-//    solve in each lane) and one with the next token's sums formed beside the update both took longer
-//    there: what they save in waiting they spend in instructions.
+//  - tokens_kernel, token by token: for a few tokens a sequence, where the traffic is still the bound (48 sequences of 1 to
+//    8 tokens, every state kept: 94 us, 6.0 TB/s).
+//  - pairs_kernel, two tokens at a time: for many tokens, bound by the fp32 pipe, which the two-wide
+//    multiply-adds hold for two cycles each, and by the passes' other instructions (37 sequences of up to 63
+//    tokens, H = 16, per-channel gates: 66 us, the pipe busy for 31 of them; 71 token by token, 95 without the
+//    order of ordered_sequence), and for few warps, bound by a token's chain of dependent instructions (5
+//    sequences of 130 tokens: 22.7 us, 28.5 token by token). Blocks of eight tokens (all products with the state
+//    first, then a triangular solve in each lane) and the next token's sums formed beside the update both took longer:
+//    what they save in waiting they spend in instructions.
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -112,11 +114,21 @@ struct Raw4 {
             u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
         }
     }
-    __device__ __forceinline__ void pairs(pair_t (&d)[2]) const {
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            d[j] = BF ? pack(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u))
-                      : pack(__uint_as_float(u[BF ? 0 : 2 * j]), __uint_as_float(u[BF ? 0 : 2 * j + 1]));
+        for (unsigned& x : u) x = 0;
+    }
+    __device__ __forceinline__ void values(float (&f)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = !BF ? __uint_as_float(u[BF ? 0 : i])
+                       : __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    }
+    __device__ __forceinline__ void pairs(pair_t (&d)[2]) const {
+        float f[4];
+        values(f);
+        d[0] = pack(f[0], f[1]);
+        d[1] = pack(f[2], f[3]);
     }
 };
 
@@ -129,6 +141,10 @@ __device__ __forceinline__ float load1(const void* base, long long at) {
 __device__ __forceinline__ void put8(float* to, const float (&f)[8]) {
     *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
     *reinterpret_cast<float4*>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+__device__ __forceinline__ void put4(float* to, const float (&f)[4]) {
+    *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
 }
 
 __device__ __forceinline__ void report(DeviceError* e, unsigned detail) {
@@ -528,7 +544,7 @@ __device__ __forceinline__ int ordered_sequence(const RecurrentParams& p, int mi
 }
 static_assert(kBuckets == 32 * kWarps, "a thread for each bucket");
 
-// Any number of tokens a sequence, kTokens of them staged in shared memory at a time while the next ones load.
+// Token by token: kTokens of them staged in shared memory at a time while the next ones load.
 template <int K, int CW, int CPL, bool GATEK, bool BF>
 __global__ void __launch_bounds__(32 * kWarps, CW == 16 ? 4 : 1) tokens_kernel(RecurrentParams p) {
     using Cols = Tile<K, CW, CPL>;
@@ -695,19 +711,251 @@ __global__ void __launch_bounds__(32 * kWarps, CW == 16 ? 4 : 1) tokens_kernel(R
     if (write) tile.store(p.state + slot_out * at.page + at.off, p.V);
 }
 
-template <int K, int CW, int CPL, bool ONE>
-cudaError_t launch(const RecurrentParams& p, bool gate_k, bool bf16, cudaStream_t s) {
-    const void* fn;
-    if constexpr (ONE)
-        fn = gate_k ? (bf16 ? (const void*)decode_kernel<K, CW, CPL, true, true>
-                            : (const void*)decode_kernel<K, CW, CPL, true, false>)
-                    : (bf16 ? (const void*)decode_kernel<K, CW, CPL, false, true>
-                            : (const void*)decode_kernel<K, CW, CPL, false, false>);
+// Any number of tokens a sequence, by twos: with S0 the state before tokens 1 and 2, c21 = k2read . k1 and so on,
+//   r1 = beta1 (v1 - k1read^T S0),        o1 = (E1 q1)^T S0 + (q1 . k1) r1,
+//   r2 = beta2 (v2 - (E1 k2read)^T S0 - (k2read . k1) r1),
+//   o2 = (E1 E2 q2)^T S0 + (E2 q2 . k1) r1 + (q2 . k2) r2,
+//   S2 = E1 E2 S0 + (E2 k1) r1^T + k2 r2^T
+// (kread = k, or E k for the decayed read): seven multiply-adds a state value where two single tokens take eight,
+// and half as many waits for a sum across lanes. kTokens tokens are staged in shared memory at a time while the next
+// ones load; a token that the last pair lacks is staged as zeros.
+template <int K, int CW, int CPL, bool GATEK, bool BF>
+__global__ void __launch_bounds__(32 * kWarps, CW == 16 ? 3 : 1) pairs_kernel(RecurrentParams p) {
+    using Cols = Tile<K, CW, CPL>;
+    constexpr int NQ = Cols::NQ, C = kTokens, P = C / 2;
+    constexpr int KV4 = K / 4;            // threads that stage one pair's k and q, four channels each
+    constexpr int COLS = CW * kWarps;
+    static_assert(P * KV4 <= 32 * kWarps && C * COLS / 8 <= 32 * kWarps, "one piece a thread");
+
+    // as the update (per channel: E2 k1, k2), the outputs (E1 q1, E1 E2 q2) and the reads (k1read, E1 k2read) take them
+    __shared__ __align__(16) float ks[2][C][K], qs[2][C][K];
+    __shared__ __align__(16) float kr[2][GATEK ? C : 1][GATEK ? K : 4];
+    __shared__ __align__(16) float es[2][GATEK ? P : 1][GATEK ? K : 4];    // E1 E2
+    __shared__ __align__(16) float vs[2][C][COLS];
+    __shared__ float2 gb[2][C];           // exp(g) (scalar gates), beta
+    __shared__ __align__(16) float dots[2][P][4];   // q1 . k1, q2 . k2, k2read . k1, E2 q2 . k1 (scalar gates: without the gates)
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Place at(p, K, CW, warp);
+    if (p.ordered) at.s = ordered_sequence(p, at.s);
+    Cols tile(lane);
+
+    const int slot_in = p.slots_in ? __ldg(p.slots_in + at.s) : -1;
+    int lo, n;
+    token_range(p, at.s, lo, n);
+    const int slot_out = p.slots_out ? __ldg(p.slots_out + at.s) : -1;
+    if (slot_in >= 0 && slot_in < p.num_slots)
+        tile.load(p.state + slot_in * at.page + at.off, p.V);
     else
-        fn = gate_k ? (bf16 ? (const void*)tokens_kernel<K, CW, CPL, true, true>
-                            : (const void*)tokens_kernel<K, CW, CPL, true, false>)
-                    : (bf16 ? (const void*)tokens_kernel<K, CW, CPL, false, true>
-                            : (const void*)tokens_kernel<K, CW, CPL, false, false>);
+        tile.zero();
+
+    // staging: thread tid brings four key channels of pair sp's k, q (and gates) and eight columns of
+    // token vt's v
+    const int sp = tid / KV4, sk = 4 * (tid % KV4);
+    const int vt = tid / (COLS / 8), vc = 8 * (tid % (COLS / 8));
+    Raw4<BF> rk[2], rq[2], rg[2];
+    Raw8<BF> rv;
+    float raw_g, raw_b;
+    auto load_tokens = [&](int t0) {
+        rv.zero();
+        raw_g = raw_b = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            rk[j].zero();
+            rq[j].zero();
+            rg[j].zero();
+            const int t = t0 + 2 * sp + j;
+            if (sp < P && t < n) {
+                const long long tok = lo + t;
+                const long long a = (tok * p.Hqk + at.hk) * K + sk;
+                rk[j].load(p.k, a);
+                rq[j].load(p.q, a);
+                if constexpr (GATEK) rg[j].load(p.g, (tok * p.H + at.h) * K + sk);
+            }
+        }
+        if (vt < C && t0 + vt < n)
+            rv.load(p.v, ((long long)(lo + t0 + vt) * p.H + at.h) * p.V + (at.col0 - warp * CW) + vc);
+        if (tid < C && t0 + tid < n) {
+            const long long a = (long long)(lo + t0 + tid) * p.H + at.h;
+            raw_b = load1<BF>(p.beta, a);
+            if constexpr (!GATEK) raw_g = load1<BF>(p.g, a);
+        }
+    };
+    auto store_tokens = [&](int b) {
+        float k1[4], k2[4], q1[4], q2[4];
+        rk[0].values(k1);
+        rk[1].values(k2);
+        rq[0].values(q1);
+        rq[1].values(q2);
+        float d[4] = {};   // q1 . k1, q2 . k2, k2read . k1, E2 q2 . k1
+        float x1[4], x2[4], e1[4], e2[4];   // k1read, k2read
+        if constexpr (GATEK) {
+            rg[0].values(e1);
+            rg[1].values(e2);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            d[0] = fmaf(q1[i], k1[i], d[0]);
+            d[1] = fmaf(q2[i], k2[i], d[1]);
+            x1[i] = k1[i];
+            x2[i] = k2[i];
+            if constexpr (GATEK) {
+                e1[i] = expf(e1[i]);
+                e2[i] = expf(e2[i]);
+                q1[i] *= e1[i];
+                q2[i] *= e2[i];
+                if (p.decay_first) {
+                    x1[i] *= e1[i];
+                    x2[i] *= e2[i];
+                }
+            }
+            d[2] = fmaf(x2[i], k1[i], d[2]);
+            d[3] = fmaf(q2[i], k1[i], d[3]);
+            if constexpr (GATEK) {
+                q2[i] *= e1[i];
+                x2[i] *= e1[i];
+                k1[i] *= e2[i];
+                e1[i] *= e2[i];
+            }
+        }
+        // the four sums over the pair's lanes, which first halve them among themselves
+        int off = KV4 / 2;
+#pragma unroll
+        for (int h = 2; h >= 1; h /= 2, off /= 2) {
+            const bool up = lane & off;
+#pragma unroll
+            for (int i = 0; i < h; ++i) {
+                const float keep = up ? d[i + h] : d[i], send = up ? d[i] : d[i + h];
+                d[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+            }
+        }
+#pragma unroll
+        for (; off > 0; off /= 2) d[0] += __shfl_xor_sync(0xffffffffu, d[0], off);
+        if (sp < P) {
+            put4(&ks[b][2 * sp][sk], k1);
+            put4(&ks[b][2 * sp + 1][sk], k2);
+            put4(&qs[b][2 * sp][sk], q1);
+            put4(&qs[b][2 * sp + 1][sk], q2);
+            if constexpr (GATEK) {
+                put4(&kr[b][2 * sp][sk], x1);
+                put4(&kr[b][2 * sp + 1][sk], x2);
+                put4(&es[b][sp][sk], e1);
+            }
+            if (sk % KV4 == 0) dots[b][sp][sk / KV4] = d[0];   // (lanes 0, KV4 / 4, KV4 / 2, 3 KV4 / 4 of the pair)
+        }
+        if (vt < C) {
+            float f[8];
+            rv.values(f);
+            put8(&vs[b][vt][vc], f);
+        }
+        if (tid < C) gb[b][tid] = make_float2(GATEK ? 1.f : expf(raw_g), raw_b);
+    };
+    load_tokens(0);
+
+    bool write;
+    // (every warp of the block comes to the same verdict on the call and the sequence)
+    if (!admitted(p, at, slot_in, slot_out, lane, write)) return;
+
+    const int oc = tile.col(tile.own());   // this lane's column once sums are joined
+    const bool first = tile.first();
+    const long long ostep = (long long)p.H * p.V;
+    long long oat = ((long long)lo * p.H + at.h) * p.V + at.col0 + oc;
+    for (int t0 = 0, b = 0; t0 < n; t0 += C, b ^= 1) {
+        // (buffer b was last read before the barrier of the block in between)
+        store_tokens(b);
+        __syncthreads();
+        if (t0 + C < n) load_tokens(t0 + C);
+        const int m = min(C, n - t0);
+#pragma unroll 1
+        for (int t = 0; t < m; t += 2) {
+            pair_t a1[CPL], a2[CPL], q1[CPL], q2[CPL];
+            const float* r1_ = GATEK ? kr[b][t] : ks[b][t];
+            const float* r2_ = GATEK ? kr[b][t + 1] : ks[b][t + 1];
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const ulonglong2 x1 = *reinterpret_cast<const ulonglong2*>(r1_ + tile.row(i));
+                const ulonglong2 y1 = *reinterpret_cast<const ulonglong2*>(&qs[b][t][tile.row(i)]);
+                const ulonglong2 x2 = *reinterpret_cast<const ulonglong2*>(r2_ + tile.row(i));
+                const ulonglong2 y2 = *reinterpret_cast<const ulonglong2*>(&qs[b][t + 1][tile.row(i)]);
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    a1[c] = i ? fma2(tile.S[i][0][c], x1.x, a1[c]) : mul2(tile.S[i][0][c], x1.x);
+                    a2[c] = i ? fma2(tile.S[i][0][c], x2.x, a2[c]) : mul2(tile.S[i][0][c], x2.x);
+                    q1[c] = i ? fma2(tile.S[i][0][c], y1.x, q1[c]) : mul2(tile.S[i][0][c], y1.x);
+                    q2[c] = i ? fma2(tile.S[i][0][c], y2.x, q2[c]) : mul2(tile.S[i][0][c], y2.x);
+                }
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    a1[c] = fma2(tile.S[i][1][c], x1.y, a1[c]);
+                    a2[c] = fma2(tile.S[i][1][c], x2.y, a2[c]);
+                    q1[c] = fma2(tile.S[i][1][c], y1.y, q1[c]);
+                    q2[c] = fma2(tile.S[i][1][c], y2.y, q2[c]);
+                }
+            }
+            // (k is read again for the update: kept in registers until then it would push the state out of them)
+            if constexpr (CPL == 4) asm volatile("" ::: "memory");
+            const float2 g1 = gb[b][t], g2 = gb[b][t + 1];   // exp(g), beta
+            const float4 d = *reinterpret_cast<const float4*>(dots[b][t / 2]);
+            const float v1 = vs[b][t][warp * CW + oc], v2 = vs[b][t + 1][warp * CW + oc];
+            float s1 = tile.join(a1), s2 = tile.join(a2), o1 = tile.join(q1), o2 = tile.join(q2);
+            float kk = d.z, q21 = d.w;
+            if constexpr (!GATEK) {
+                const float e12 = g1.x * g2.x;
+                o1 *= g1.x;
+                o2 *= e12;
+                s1 *= p.decay_first ? g1.x : 1.f;
+                s2 *= p.decay_first ? e12 : g1.x;
+                kk *= p.decay_first ? g2.x : 1.f;
+                q21 *= g2.x;
+            }
+            const bool both = t + 1 < m;
+            const float r1 = g1.y * (v1 - s1);
+            const float r2 = both ? g2.y * (v2 - fmaf(kk, r1, s2)) : 0.f;
+            if (first) {
+                store_o(p, oat, fmaf(d.x, r1, o1));
+                if (both) store_o(p, oat + ostep, fmaf(d.y, r2, fmaf(q21, r1, o2)));
+            }
+            oat += 2 * ostep;
+            pair_t u1[CPL], u2[CPL];
+            tile.spread(GATEK ? r1 : g2.x * r1, u1);
+            tile.spread(r2, u2);
+            const float e12 = g1.x * g2.x;
+            const pair_t e2 = pack(e12, e12);
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const ulonglong2 k1 = *reinterpret_cast<const ulonglong2*>(&ks[b][t][tile.row(i)]);
+                const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&ks[b][t + 1][tile.row(i)]);
+                pair_t ex = e2, ey = e2;
+                if constexpr (GATEK) {
+                    const ulonglong2 ek = *reinterpret_cast<const ulonglong2*>(&es[b][t / 2][tile.row(i)]);
+                    ex = ek.x;
+                    ey = ek.y;
+                }
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    tile.S[i][0][c] = fma2(k2.x, u2[c], fma2(k1.x, u1[c], mul2(tile.S[i][0][c], ex)));
+                    tile.S[i][1][c] = fma2(k2.y, u2[c], fma2(k1.y, u1[c], mul2(tile.S[i][1][c], ey)));
+                }
+            }
+        }
+    }
+    if (write) tile.store(p.state + slot_out * at.page + at.off, p.V);
+}
+
+enum class Kernel { kDecode, kTokens, kPairs };
+template <Kernel WHICH, int K, int CW, int CPL, bool GATEK, bool BF>
+constexpr auto kernel_of() {
+    if constexpr (WHICH == Kernel::kDecode)
+        return decode_kernel<K, CW, CPL, GATEK, BF>;
+    else if constexpr (WHICH == Kernel::kTokens)
+        return tokens_kernel<K, CW, CPL, GATEK, BF>;
+    else
+        return pairs_kernel<K, CW, CPL, GATEK, BF>;
+}
+template <Kernel WHICH, int K, int CW, int CPL>
+cudaError_t launch(const RecurrentParams& p, bool gate_k, bool bf16, cudaStream_t s) {
+    const auto fn = gate_k ? (bf16 ? kernel_of<WHICH, K, CW, CPL, true, true>() : kernel_of<WHICH, K, CW, CPL, true, false>())
+                           : (bf16 ? kernel_of<WHICH, K, CW, CPL, false, true>() : kernel_of<WHICH, K, CW, CPL, false, false>());
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((long long)p.nseq * p.H * (p.V / (CW * kWarps))));
     cfg.blockDim = dim3(32 * kWarps);
@@ -719,34 +967,39 @@ cudaError_t launch(const RecurrentParams& p, bool gate_k, bool bf16, cudaStream_
     cfg.numAttrs = p.owner ? 1 : 0;   // the dependent of claim_kernel
     RecurrentParams copy = p;
     void* args[] = {&copy};
-    return cudaLaunchKernelExC(&cfg, fn, args);
+    return cudaLaunchKernelExC(&cfg, (const void*)fn, args);
 }
 
-// The split. One token a sequence: 16 columns a warp always (half a warp's 64 B of a row; at 8 columns the
-// same time up to four sequences of 32 heads, more beyond: 49.7 against 59.9 us at 64 of them). More
-// tokens: 16 columns a warp, four of them a lane, when that fills the SMs with twelve warps each; below that
-// 8 columns, one a lane, where a token's sums cross fewer lanes: 18.9 against 25.1 us for two sequences of
-// 8 heads and up to 63 tokens, 51.7 against 47.6 us for 16 of 16 heads, 187 against 115 for 32 of 32 (K = V = 128).
-// Few warps: a token's time is then one warp's chain of instructions, which is shorter with fewer rows a lane although the
-// sums cross more lanes. 8, 4 and 2 columns, one a lane, K = V = 128, 63 tokens, cold: 29.2, 27.1 and 25.1 us for one sequence
-// of 8 heads, 27.1, 25.1 and 25.1 for two, 33.3, 33.3 and 41.5 for eight (of up to 63), 45.6, 47.6 and 64.0 for eight of 16
-// heads; 39.4, 37.3 and 31.2 us for five of 130 tokens, 2 heads, K = V = 64.
-// Many tokens a sequence on average and K = V = 128: 32 columns a warp, two blocks an SM, whose exchanges and addresses
-// serve twice the columns: 113 against 119 us for 64 sequences of up to 63 tokens, H = 16 (98 against 94 us for 48
-// of 1 to 8 with every state kept).
+// The split. One token a sequence: decode_kernel, 16 columns a warp always (half a warp's 64 B of a row; at 8 columns
+// the same time up to four sequences of 32 heads, more beyond: 49.7 against 59.9 us at 64 of them).
+// More tokens, enough columns to fill the SMs with twelve warps of 16 each:
+//  - few tokens a sequence on average: bound by the states' traffic. tokens_kernel, 16 columns a warp, four blocks an SM:
+//    240 us for 256 sequences of up to two tokens, 32 heads, against 250 by pairs;
+//  - many: pairs_kernel, and 32 columns a warp where K = V = 128, two blocks an SM, whose exchanges and addresses serve
+//    twice the columns: 310 us for 64 sequences of 40 to 63 tokens, 32 heads, per-channel gates, against 344 by
+//    single tokens and 344 by pairs at 16 columns.
+// Fewer columns: pairs_kernel with 8, 4 or 2 of them a warp, one a lane. A token's time is then a warp's chain of
+// instructions, which is shorter with fewer rows a lane although the sums cross more lanes. 8, 4 and 2 columns (by
+// single tokens), K = V = 128, 63 tokens, cold: 29.2, 27.1 and 25.1 us for one sequence of 8 heads, 27.1, 25.1
+// and 25.1 for two, 33.3, 33.3 and 41.5 for eight (of up to 63), 45.6, 47.6 and 64.0 for eight of 16 heads; 39.4, 37.3
+// and 31.2 us for five of 130 tokens, 2 heads, K = V = 64, where pairs take 25.1.
+// A state after every token: single tokens.
 constexpr int kWideWarpsPerSm = 12, kManyTokens = 12;
 constexpr int kQuarterWarpsPerSm = 8, kEighthWarpsPerSm = 4;   // of 4 and 2 columns, at most
 template <int K>
 cudaError_t launch_k(const RecurrentParams& p, int average, bool gate_k, bool bf16, int sms, cudaStream_t s) {
-    if (p.T == 1 && !p.cu && !p.per_token) return launch<K, 16, 4, true>(p, gate_k, bf16, s);
+    if (p.T == 1 && !p.cu) return launch<Kernel::kDecode, K, 16, 4>(p, gate_k, bf16, s);
     const long long warps = (long long)p.nseq * p.H * (p.V / 16);
-    if constexpr (K == 128)
-        if (p.V == 128 && average >= kManyTokens && warps >= (long long)kWideWarpsPerSm * sms)
-            return launch<K, 32, 4, false>(p, gate_k, bf16, s);
-    if (warps >= (long long)kWideWarpsPerSm * sms) return launch<K, 16, 4, false>(p, gate_k, bf16, s);
-    if (8 * warps <= (long long)kEighthWarpsPerSm * sms) return launch<K, 2, 1, false>(p, gate_k, bf16, s);
-    if (4 * warps <= (long long)kQuarterWarpsPerSm * sms) return launch<K, 4, 1, false>(p, gate_k, bf16, s);
-    return launch<K, 8, 1, false>(p, gate_k, bf16, s);
+    if (warps >= (long long)kWideWarpsPerSm * sms) {
+        if (p.per_token || average < kManyTokens) return launch<Kernel::kTokens, K, 16, 4>(p, gate_k, bf16, s);
+        if constexpr (K == 128)
+            if (p.V == 128) return launch<Kernel::kPairs, K, 32, 4>(p, gate_k, bf16, s);
+        return launch<Kernel::kPairs, K, 16, 4>(p, gate_k, bf16, s);
+    }
+    if (p.per_token) return launch<Kernel::kTokens, K, 8, 1>(p, gate_k, bf16, s);
+    if (8 * warps <= (long long)kEighthWarpsPerSm * sms) return launch<Kernel::kPairs, K, 2, 1>(p, gate_k, bf16, s);
+    if (4 * warps <= (long long)kQuarterWarpsPerSm * sms) return launch<Kernel::kPairs, K, 4, 1>(p, gate_k, bf16, s);
+    return launch<Kernel::kPairs, K, 8, 1>(p, gate_k, bf16, s);
 }
 
 // Each block of the rule looks for other sequences that name its slot when there are at most this many
@@ -821,7 +1074,7 @@ gdn_status gdn_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, const int*
     c.num_slots = num_slots;
     c.out_bf16 = p->out_dtype == GDN_DTYPE_BF16;
     c.decay_first = p->decay_first;
-    if (p->T == 1 && !cu_seqlens) per_token = 0;   // the state after the token is the final one
+    if (!slots_out || (p->T == 1 && !cu_seqlens)) per_token = 0;   // no states to keep, or the final ones
     c.per_token = per_token;
     // The longest sequences first, where there is something to gain: several tokens a sequence on average, and more
     // blocks than the SMs hold at once. 37 sequences of up to 63 tokens, H = 16: 95 us without, 72 with;
