@@ -54,8 +54,9 @@ __device__ __forceinline__ void put_sums(float* to, int c, int G, int n, const f
 // A block of kMaxThreads threads; GB of them to a row, 0: a part of a warp (rows of at most 512 values)
 template <int GB, int R, int L, bool XB, bool YB, bool GATED>
 struct Bwd {
-    // (29200 rows of 2000 in bf16: 68.0, 67.9, 62.4, 63.9 and 67.0 us with 4, 6, 8, 12 and 20)
-    static constexpr int kAhead = 8;
+    // (With 4, 6, 8, 12 and 20: 29200 rows of 2000 in bf16 68.0, 67.9, 62.4, 63.9 and 67.0 us; 262144 rows of 128 with a gate, x in
+    // fp32, 79.6, 79.6, 82.7, 82.7 and 80.5; 467200 rows of 128 in bf16 67.2, 66.2, 66.6, 67.3 and 67.3.)
+    static constexpr int kAhead = R == 1 ? 6 : 8;
     using Rows = std::conditional_t<GATED, Ring<L, R, kAhead, XB, YB, YB>, Ring<L, R, kAhead, XB, YB>>;
 };
 
