@@ -413,3 +413,24 @@ def test_after_the_prompt_in_chunks():
     o_ref, hf_ref = oracle.varlen_recurrence(x["q"], x["k"], x["v"], x["g"], x["beta"], cu, x["h0"])
     assert rel_err(np64(o_t).reshape(1, -1, H, 128), o_ref[:, tail]) <= TOL_BF16
     assert rel_err(np64(pages[2:5]), hf_ref) <= TOL_BF16
+
+
+@pytest.mark.parametrize("gate_k", [False, True])
+@pytest.mark.parametrize("lens,H", [([7, 6], 2), ([7, 6, 12], 8), ([15, 14] * 40, 8)])
+@pytest.mark.parametrize("bad", [4, 5])   # the first and the second token of a pair
+def test_later_tokens_and_other_sequences_do_not_matter(lens, H, gate_k, bad):
+    d = make(lens, H, H, 128, 128, seed=11, gate_k=gate_k)
+    n = len(lens)
+    slots_in, slots_out = d["order"][:n], d["order"][n:2 * n]
+    state, err = call(d, slots_in, slots_out)
+    o = d["o"].clone()
+    for name, value in (("q", float("nan")), ("k", float("inf")), ("v", float("nan")), ("g", float("-inf")),
+                        ("beta", float("nan"))):
+        d[name].view(-1, *d[name].shape[2:])[bad] = value
+    after, err2 = call(d, slots_in, slots_out)
+    assert err[0] == 0 and err2[0] == 0
+    new, old = (x.view(-1, *x.shape[2:]) for x in (d["o"], o))
+    assert torch.equal(new[:bad], old[:bad]) and torch.equal(new[lens[0]:], old[lens[0]:])
+    assert new[bad].isnan().any()
+    rest = [i for i in range(state.shape[0]) if i != slots_out[0]]
+    assert torch.equal(after[rest], state[rest])
