@@ -263,7 +263,7 @@ struct Ring {
                 f[e] = E == 4 ? __uint_as_float(u[E == 4 ? e : 0])
                               : __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
         } else {
-            const int c = first_col<2>(i, t, G, odd), step = 2 * G, n = row < rows ? N : 0;
+            const int c = first_col<2>(i, t, G, odd), step = 2 * G, n = G > 32 || row < rows ? N : 0;   // (a block's rows are there)
             const unsigned at = region<T>(stage) + (unsigned)((row * N * E) & 15) + E * c;
             if constexpr (E == 2) {
                 if (step > 64 && c >= 0 && c + 3 * step + 1 < n) {   // (as they are written)
@@ -395,9 +395,9 @@ inline long long bwd_blocks(long long rows, const Shape& s, int sms) {
 // each kernel and device, and again when smem changes: `known` holds the last answer and its smem in KiB. 0: an
 // error.
 constexpr int kDevices = 64;
+constexpr int kMost = 200 * 1024;   // shared memory, above any call's
 template <class Kernel>
 int resident_blocks(Kernel* kernel, int threads, int smem, std::atomic<int> (&known)[kDevices]) {
-    constexpr int kMost = 200 * 1024;   // above any call's
     int dev = 0, per_sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     std::atomic<int>& last = known[dev % kDevices];

@@ -205,7 +205,7 @@ def test_no_rows():
     assert not dw.any() and not db.any()
 
 
-@pytest.mark.parametrize("n", [128, 127, 2048, 6000])
+@pytest.mark.parametrize("n", [128, 127, 1999, 2048, 6000])
 def test_in_place_partial_and_repeated(n):
     d = {k: cuda(v) for k, v in make(900, n, BF, BF, True).items()}
     y, dx, dz, dw, db = run_both({k: v for k, v in make(900, n, BF, BF, True).items()}, True, BF, BF)
