@@ -131,6 +131,9 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
         const long long row = row0 + sub;
         Rows::template wait<GB, kMaxThreads>();
         fetch(stage == 0 ? Rows::kAhead : stage - 1, row + Rows::kAhead * stride);
+        // d w is formed twice rather than kept where w is at hand for the second time, and registers are short: 29200 gated
+        // rows in bf16, 1999 values 160 -> 130 us, 2000 138 -> 114; 1999 of x in fp32 193 -> 156.
+        constexpr bool kAgain = Plan::kShared || (R > 1 && GATED);
         pair_t x[R][4], d[R][4], dxh[R][4], dyg[R][4];
         pair_t xx = 0, dx_ = 0, ds = 0, xs = 0;   // sums of x^2, d w x, d w, x
 #pragma unroll
@@ -173,6 +176,11 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
                 for (int i = 0; i < R; ++i) {
                     float v[8], f[8];
                     single(x[i], v);
+                    if constexpr (kAgain) {
+                        parameters(w, 0, i);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) dxh[i][k] = mul2(d[i][k], w[k]);
+                    }
                     single(dxh[i], f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -195,18 +203,17 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int c = first_col<L>(i, t, G, odd);
-            if constexpr (R > 1 && GATED) {
-                parameters(w, 0, i);
-                parameters(b, 1, i);
-            }
+            if constexpr (kAgain) parameters(w, 0, i);
+            if constexpr (R > 1 && GATED) parameters(b, 1, i);
             float out[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const pair_t xh = fma2(x[i][k], scale, level);
+                const pair_t dw_ = kAgain ? mul2(d[i][k], w[k]) : dxh[i][k];
                 if constexpr (GATED) dyg[i][k] = mul2(dyg[i][k], fma2(xh, w[k], b[k]));
                 dw2[i][k] = fma2(d[i][k], xh, dw2[i][k]);
                 db2[i][k] = add2(db2[i][k], d[i][k]);
-                x[i][k] = fma2(xh, along, fma2(dxh[i][k], scale, level_d));
+                x[i][k] = fma2(xh, along, fma2(dw_, scale, level_d));
             }
             single(x[i], out);
             store8<XB, L>(p.y, row * p.N, c, G, n, out);
