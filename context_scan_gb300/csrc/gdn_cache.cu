@@ -55,13 +55,14 @@ __device__ __forceinline__ int block_scan(int x, int& sum) {
 __device__ __forceinline__ bool in_range(int p, int n) { return p >= 0 && p < n; }
 
 // Jobs of a copy: every pair at once, as if all pages were read before any is written. That holds
-// when no pair's dst is another pair's dst or src; a pair that breaks it is left out. `owner`: for
-// every page the pair that writes it, of which only the entries that the call names are touched.
+// when no pair's dst is another pair's dst or src; a pair that breaks it is left out. Pairs with dst < 0 read nothing.
+// `owner`: for every page the pair that writes it, of which only the entries that the other pairs name are touched.
 __global__ void __launch_bounds__(kThreads)
     copy_jobs_kernel(int num_pages, int n, const int* src, const int* dst, int* owner, Job* jobs,
                      DeviceError* err) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int i = threadIdx.x; i < n; i += kThreads) {
+        if (dst[i] < 0) continue;
         if (in_range(src[i], num_pages)) owner[src[i]] = kNobody;
         if (in_range(dst[i], num_pages)) owner[dst[i]] = kNobody;
     }
@@ -71,7 +72,7 @@ __global__ void __launch_bounds__(kThreads)
             atomicExch(owner + dst[i], kShared);
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads)
-        if (in_range(src[i], num_pages)) {
+        if (dst[i] >= 0 && in_range(src[i], num_pages)) {
             const int was = atomicAdd(owner + src[i], 0);
             if (was != kNobody && was != i) atomicExch(owner + src[i], kShared);
         }

@@ -441,8 +441,9 @@ GDN_API gdn_status gdn_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, co
 GDN_API size_t gdn_cache_workspace_bytes(int num_pages, int n);
 
 /* Page dst[i] := page src[i] in every layer, i < n; src[i] < 0: page dst[i] := zeros; dst[i] < 0: the
- * pair is skipped. The result is that of reading every page before writing any: a pair whose dst is
- * another pair's dst or src is left out and refused, as is one with a number >= num_pages. */
+ * pair is skipped, and its src is not read (lists padded to a fixed length). The result is that of
+ * reading every page before writing any: a pair whose dst is another pair's dst or (where that pair is not
+ * skipped) src is left out and refused, as is one with a number >= num_pages. */
 GDN_API gdn_status gdn_cache_copy(void* pages, int layers, int num_pages, size_t page_bytes, int n,
                                   const int* src, const int* dst, void* workspace,
                                   size_t workspace_bytes, void* stream);
