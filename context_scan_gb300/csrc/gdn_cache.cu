@@ -19,6 +19,7 @@ constexpr int kItems = 8;        // pages a thread of them looks at in one round
 // detail words of GDN_ERR_INVALID_ARG and GDN_ERR_NO_PAGE
 constexpr unsigned kTagPage = 0x51, kTagSharedPage = 0x52, kTagFreePage = 0x53, kTagFull = 0x54;
 constexpr int kNobody = -1, kShared = -2;
+constexpr int kMostCount = 1 << 30;   // pages of a cache, entries of a list: the kernels' int steps stay below 2^31
 
 struct Job {
     int src, dst;   // src < 0: zeros; dst < 0: nothing to do
@@ -308,6 +309,7 @@ bool off_int(const void* ptr) { return reinterpret_cast<uintptr_t>(ptr) & 3u; }
 
 gdn_status check_pages(const Pages& c, int n) {
     if (c.layers < 1 || c.num_pages < 1 || n < 0 || !c.pages) return GDN_ERR_INVALID_ARG;
+    if (c.num_pages > kMostCount || n > kMostCount) return GDN_ERR_UNSUPPORTED_SHAPE;
     if (c.page_bytes == 0 || c.page_bytes % 16 != 0 || c.page_bytes >= ((size_t)1 << 40))
         return GDN_ERR_UNSUPPORTED_SHAPE;
     if (reinterpret_cast<uintptr_t>(c.pages) & 15u) return GDN_ERR_MISALIGNED;
@@ -328,7 +330,7 @@ using namespace gdn;
 extern "C" {
 
 size_t gdn_cache_workspace_bytes(int num_pages, int n) {
-    if (num_pages < 1 || n < 0) return 0;
+    if (num_pages < 1 || n < 0 || num_pages > kMostCount || n > kMostCount) return 0;
     return cache_layout(num_pages, n).total;
 }
 
@@ -379,6 +381,7 @@ gdn_status gdn_cache_fork(void* pages, int layers, int num_pages, size_t page_by
 gdn_status gdn_cache_free(int num_pages, int* refs, int n, const int* list, void* workspace,
                           size_t workspace_bytes, void* stream) {
     if (num_pages < 1 || n < 0 || !refs || (n > 0 && !list)) return GDN_ERR_INVALID_ARG;
+    if (num_pages > kMostCount || n > kMostCount) return GDN_ERR_UNSUPPORTED_SHAPE;
     if (off_int(refs) || off_int(list)) return GDN_ERR_MISALIGNED;
     gdn_status st = check_ws(num_pages, 0, workspace, workspace_bytes);
     if (st != GDN_OK) return st;

@@ -427,7 +427,8 @@ GDN_API gdn_status gdn_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, co
  * ---------------------------------------------------------------------------------------
  * A cache is pages [layers, num_pages, page_bytes]: a page number names one page in every
  * layer's array (layer l's array is the state of gdn_recurrent_fwd; a page is H*K*V*4 bytes there,
- * but the calls below move bytes of any meaning). page_bytes % 16 == 0. Which pages are in use
+ * but the calls below move bytes of any meaning). page_bytes % 16 == 0 and < 2^40; at most 2^30 pages,
+ * and entries in a list (else GDN_ERR_UNSUPPORTED_SHAPE). Which pages are in use
  * stands in refs [num_pages] int32 on the device: a page's count of users, 0 (or less) a free page.
  * All page numbers and counts live on the device, nothing is read back to the host, and every call
  * can be captured in a CUDA graph. The index arrays are int32 DEVICE arrays of 4-byte alignment
@@ -437,7 +438,7 @@ GDN_API gdn_status gdn_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, co
 
 /* Workspace bytes for the calls below on a cache of num_pages pages and at most n pairs or requests a
  * call (n of gdn_cache_copy and gdn_cache_fork; 0 for the others). Its first 256 bytes must be zero
- * before the first call. Returns 0 for num_pages < 1 or n < 0. */
+ * before the first call. Returns 0 for num_pages < 1, n < 0 or either above 2^30. */
 GDN_API size_t gdn_cache_workspace_bytes(int num_pages, int n);
 
 /* Page dst[i] := page src[i] in every layer, i < n; src[i] < 0: page dst[i] := zeros; dst[i] < 0: the
