@@ -421,10 +421,17 @@ def alloc_cache_workspace(num_pages: int, n: int = 0, device="cuda"):
     return torch.zeros(size, dtype=torch.uint8, device=device)
 
 
+def _int(name, n):
+    """n, which the library takes as a C int (ctypes would cut it off without a word)."""
+    if n >= 2**31:
+        raise ValueError(f"{name} is {n}, more than the library counts to")
+    return n
+
+
 def _pages(pages):
     if pages.dim() < 3:
         raise ValueError("pages is [layers, num_pages, ...]")
-    layers, num = pages.shape[0], pages.shape[1]
+    layers, num = _int("the number of layers", pages.shape[0]), _int("the number of pages", pages.shape[1])
     total = pages.numel() * pages.element_size()
     return pages.data_ptr(), layers, num, total // (layers * num) if total else 0
 
@@ -435,6 +442,8 @@ def _indexes(**arrays):
     for name, t in arrays.items():
         if t is not None and (t.dtype != torch.int32 or t.dim() != 1):
             raise ValueError(f"{name} is not a one-dimensional int32 tensor")
+        if t is not None:
+            _int(f"the length of {name}", t.numel())
 
 
 def _room(workspace):
@@ -491,7 +500,7 @@ def gdn_cache_compact(pages, refs, table, remap, live, workspace, stream=None):
 def _rows(x, y_like, params, **rest):
     """(rows, N) of x [..., N]; the tensors of y's type have x's shape, the parameters are fp32 [N]."""
     import torch
-    N = x.shape[-1]
+    N = _int("the length of a row", x.shape[-1])
     for name, t in rest.items():
         _is(name, t, y_like.dtype, x.shape)
     for name, t in params.items():

@@ -1,7 +1,9 @@
 """Counts near 2^31, which the operators over the state cache step through in 31 bits, are refused on the host
 (no GPU: nothing here gets as far as a launch)."""
 import pytest
+import torch
 
+from context_scan_gb300 import gdn
 from test_operators_host import FAKE, L  # noqa: F401
 
 TOP = 2**31 - 1
@@ -18,3 +20,18 @@ def test_cache_counts_past_30_bits(L, num, n):  # noqa: F811
     assert L.gdn_cache_free(num, FAKE, n, FAKE, *ws) == 2
     W = L.gdn_cache_workspace_bytes
     assert W(num, n) == 0 and W(2**30, 0) > 0 and W(1, 2**30) > 0
+
+
+def test_binding_refuses_sizes_past_a_c_int():
+    # (on the meta device: no memory behind them)
+    def meta(*shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    with pytest.raises(ValueError, match="length of a row"):
+        gdn._rows(meta(1, 2**32 + 64), meta(1, 2**32 + 64), {})
+    with pytest.raises(ValueError, match="length of src"):
+        gdn._indexes(src=meta(2**32 + 3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="number of pages"):
+        gdn._pages(meta(1, 2**32 + 8, 4))
+    with pytest.raises(ValueError, match="number of layers"):
+        gdn._pages(meta(2**31, 8, 4))
