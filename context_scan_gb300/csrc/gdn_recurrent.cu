@@ -1006,6 +1006,7 @@ cudaError_t launch_k(const RecurrentParams& p, int average, bool gate_k, bool bf
 // sequences; above it, and where states are kept after every token, claim_kernel does so once.
 constexpr int kInlineSeqs = 512;
 constexpr int kOrderSeqs = 1024;
+constexpr int kMostTokens = INT_MAX - 4096;   // of all sequences: token numbers and the steps beyond the last one in an int
 
 gdn_status check(const gdn_problem* p, int Hqk, int nseq, const int* cu, int num_slots, int per_token) {
     if (!p) return GDN_ERR_INVALID_ARG;
@@ -1019,8 +1020,8 @@ gdn_status check(const gdn_problem* p, int Hqk, int nseq, const int* cu, int num
     if ((p->in_dtype != GDN_DTYPE_F32 && p->in_dtype != GDN_DTYPE_BF16) ||
         (p->out_dtype != GDN_DTYPE_F32 && p->out_dtype != GDN_DTYPE_BF16))
         return GDN_ERR_UNSUPPORTED_DTYPE;
-    // token numbers, and the grid at its finest split, in 31 bits
-    if ((long long)p->B * p->T >= (1LL << 31) || (long long)nseq * p->H * 4 >= (1LL << 31))
+    // (the grid at its finest split in 31 bits)
+    if ((long long)p->B * p->T > kMostTokens || (long long)nseq * p->H * 4 >= (1LL << 31))
         return GDN_ERR_UNSUPPORTED_SHAPE;
     return GDN_OK;
 }

@@ -399,6 +399,7 @@ GDN_API size_t gdn_recurrent_workspace_bytes(int num_slots);
  *   int32 DEVICE array: 0 first, T last, non-decreasing). p->chunk is not read.
  *   Heads: q, k [B,T,Hqk,K] with p->H % Hqk == 0; head h reads q/k head h / (H / Hqk). v, o
  *   [B,T,H,V]; g [B,T,H] (or [B,T,H,K], gate_k); beta [B,T,H]. K and V in {64, 128}, each.
+ *   B*T < 2^31 - 4096, nseq*H < 2^29 (else GDN_ERR_UNSUPPORTED_SHAPE).
  *   slots_in  [nseq] int32 DEVICE array: the slot each sequence starts from; a negative entry, or
  *             slots_in NULL, is a zero state.
  *   slots_out int32 DEVICE array, or NULL (no state is written): per_token == 0: [nseq], the slot

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from context_scan_gb300 import gdn
-from test_operators_host import FAKE, L  # noqa: F401
+from test_operators_host import FAKE, L, P, recurrent  # noqa: F401
 
 TOP = 2**31 - 1
 ROOM = 1 << 62
@@ -35,3 +35,14 @@ def test_binding_refuses_sizes_past_a_c_int():
         gdn._pages(meta(1, 2**32 + 8, 4))
     with pytest.raises(ValueError, match="number of layers"):
         gdn._pages(meta(2**31, 8, 4))
+
+
+@pytest.mark.parametrize("per_token", [0, 1])
+@pytest.mark.parametrize("prob,nseq,cu", [
+    (P(B=1, T=TOP), 2, FAKE), (P(B=1, T=TOP - 1023), 2, FAKE), (P(B=1, T=TOP), 1, None),
+    (P(B=TOP, T=1, H=1), TOP, None), (P(B=1, T=TOP - 4095), 3, FAKE),
+])
+def test_recurrent_tokens_near_31_bits(L, prob, nseq, cu, per_token):  # noqa: F811
+    assert recurrent(L, prob=prob, nseq=nseq, cu=cu, per_token=per_token, Hqk=1, n=ROOM) == 2
+    if cu is not None:   # (one fewer than the limit is looked at further: here, the missing workspace)
+        assert recurrent(L, prob=P(B=1, T=TOP - 4096), nseq=nseq, cu=cu, per_token=per_token, ws=None) == 5
