@@ -357,9 +357,27 @@ __device__ __forceinline__ void group_sum(float (&x)[M], int g, float (*part)[64
 }
 
 // The layer norm's mean and variance come from one exchange, as sums of x and x^2. The variance is then a
-// difference, which loses a few bits while the mean is within two standard deviations of zero; a row with
-// a larger mean goes round once more for the sum of (x - mean)^2.
+// difference: while the mean is within two standard deviations of zero its rounding errors are up to five times a
+// two-pass sum's (E[x^2] <= 5 var; 2e-7 against 1e-7 of the output at 1.9 deviations), which is fp32's own size. A row
+// with a larger mean goes round once more: that mean, which may be off by a few of its own last bits -- the sums', and 1 / N
+// is rounded --, is taken off the values, which leaves them exact where the mean is large, and the rest's mean and square
+// give what it missed. Without the rest's mean a row of one value 100 would come out as -0.005 (N = 1000, eps = 1e-6).
 __device__ __forceinline__ bool large_mean(float mean, float var) { return mean * mean > 4.f * var; }
+// mean taken off a thread's eight values (there is none in columns past the row)
+template <int L>
+__device__ __forceinline__ void centre(pair_t (&x)[4], int c, int G, int n, float mean) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c0 = col_of<L>(c, G, 2 * k);
+        const float lo = has(c0, n) ? -mean : 0.f, hi = L != 2 ? lo : has(c0 + 1, n) ? -mean : 0.f;
+        x[k] = add2(x[k], pack(lo, hi));
+    }
+}
+// from E[x^2] of values with a small mean (NaN stays)
+__device__ __forceinline__ float centred_var(float square, float mean) {
+    const float var = fmaf(-mean, mean, square);
+    return var < 0.f ? 0.f : var;
+}
 
 // 1 / (1 + exp(-z)) from the hardware's approximations of 2^x and 1 / x (2 and 1 ulp, subnormals as zero): the
 // rounding of z log2(e) adds |z| / 2 ulp of the exponential. 2^x may overflow to infinity: the quotient is

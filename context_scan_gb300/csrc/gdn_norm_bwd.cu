@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
                 xs = add2(xs, x[i][k]);
             }
         }
-        float mean = 0.f, mean_d = 0.f, var, cross;   // cross: mean(d w xm)
+        float mean = 0.f, mean_d = 0.f, var, cross;   // mean: of what x holds; cross: mean(d w xm)
         if (p.rms) {
             float q[2] = {total(xx), total(dx_)};
             group_sum<GB, kMaxThreads>(q, G, part, half);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
             cross = fmaf(-mean, mean_d, s[1] * p.inv_n);
             const bool again = large_mean(mean, var);
             if (GB ? again : __any_sync(0xffffffffu, again)) {
-                float q[2] = {0.f, 0.f};
+                float q[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     float v[8], f[8];
@@ -184,14 +184,18 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
                     single(dxh[i], f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float xm = has(col_of<L>(first_col<L>(i, t, G, odd), G, e), p.N) ? v[e] - mean : 0.f;
-                        q[0] = fmaf(xm, xm, q[0]);
-                        q[1] = fmaf(f[e], xm, q[1]);
+                        v[e] = has(col_of<L>(first_col<L>(i, t, G, odd), G, e), p.N) ? v[e] - mean : 0.f;
+                        q[0] = fmaf(v[e], v[e], q[0]);
+                        q[1] = fmaf(f[e], v[e], q[1]);
+                        q[2] += v[e];
                     }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[i][k] = pack(v[2 * k], v[2 * k + 1]);
                 }
                 group_sum<GB, kMaxThreads>(q, G, part, half);
-                var = q[0] * p.inv_n;
-                cross = q[1] * p.inv_n;
+                mean = q[2] * p.inv_n;
+                var = centred_var(q[0] * p.inv_n, mean);
+                cross = fmaf(-mean, mean_d, q[1] * p.inv_n);
             }
         }
         // (0 for rows behind the last one, whose sums then add nothing even with eps = 0)
