@@ -82,12 +82,13 @@ __global__ void __launch_bounds__(GB ? GB : 256, GB == 512 && L != 2 && XB && !G
             mean = s[1] * p.inv_n;
             var = fmaf(-mean, mean, s[0] * p.inv_n);
             const bool again = large_mean(mean, var);
-            if (GB ? again : __any_sync(0xffffffffu, again)) {
+            if (GB ? again : __any_sync(0xffffffffu, again)) {   // (a warp's other rows stay as they are)
+                const float off = GB || again ? mean : 0.f;
                 sq = sx = 0;
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     if (GB && !warp_has<L>(i, t, G, p.N)) continue;
-                    centre<L>(x[i], first_col<L>(i, t, G, odd), G, p.N, mean);
+                    centre<L>(x[i], first_col<L>(i, t, G, odd), G, p.N, off);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         sq = fma2(x[i][k], x[i][k], sq);
@@ -96,8 +97,10 @@ __global__ void __launch_bounds__(GB ? GB : 256, GB == 512 && L != 2 && XB && !G
                 }
                 float q[2] = {total(sq), total(sx)};
                 group_sum<GB, GB>(q, G, part, half);
-                mean = q[1] * p.inv_n;
-                var = centred_var(q[0] * p.inv_n, mean);
+                if (GB || again) {
+                    mean = q[1] * p.inv_n;
+                    var = centred_var(q[0] * p.inv_n, mean);
+                }
             }
         }
         const float rstd = rsqrtf(var + p.eps);

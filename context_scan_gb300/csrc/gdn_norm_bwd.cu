@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
             var = fmaf(-mean, mean, s[0] * p.inv_n);
             cross = fmaf(-mean, mean_d, s[1] * p.inv_n);
             const bool again = large_mean(mean, var);
-            if (GB ? again : __any_sync(0xffffffffu, again)) {
+            if (GB ? again : __any_sync(0xffffffffu, again)) {   // (a warp's other rows stay as they are)
+                const float off = GB || again ? mean : 0.f;
                 float q[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
                     single(dxh[i], f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        v[e] = has(col_of<L>(first_col<L>(i, t, G, odd), G, e), p.N) ? v[e] - mean : 0.f;
+                        v[e] = has(col_of<L>(first_col<L>(i, t, G, odd), G, e), p.N) ? v[e] - off : 0.f;
                         q[0] = fmaf(v[e], v[e], q[0]);
                         q[1] = fmaf(f[e], v[e], q[1]);
                         q[2] += v[e];
@@ -193,9 +194,11 @@ __global__ void __launch_bounds__(kMaxThreads) bwd_kernel(Params p) {
                     for (int k = 0; k < 4; ++k) x[i][k] = pack(v[2 * k], v[2 * k + 1]);
                 }
                 group_sum<GB, kMaxThreads>(q, G, part, half);
-                mean = q[2] * p.inv_n;
-                var = centred_var(q[0] * p.inv_n, mean);
-                cross = fmaf(-mean, mean_d, q[1] * p.inv_n);
+                if (GB || again) {
+                    mean = q[2] * p.inv_n;
+                    var = centred_var(q[0] * p.inv_n, mean);
+                    cross = fmaf(-mean, mean_d, q[1] * p.inv_n);
+                }
             }
         }
         // (0 for rows behind the last one, whose sums then add nothing even with eps = 0)

@@ -125,3 +125,24 @@ def test_eps_of_zero_and_infinite_values(n):
     ref = plain64.norm(x[good].double(), None, None, None, False, 0.0)
     assert torch.isnan(y[[1, 4]]).all()
     assert float((y[good] - ref).abs().max()) <= 128 * U * (1 + float(ref.abs().max()) + 30 * U * 60)
+
+
+@pytest.mark.parametrize("n", [8, 40, 64, 100, 127, 128, 250, 256, 300, 511, 512, 1999])
+@pytest.mark.parametrize("t", [F32, BF])
+def test_rows_do_not_depend_on_their_neighbours(n, t):
+    # rows with ordinary means come out bit for bit as they do where no row has a large one
+    gen = torch.Generator().manual_seed(n)
+    x = (torch.randn(64, n, generator=gen) + 0.7).to(t)
+    dy = torch.randn(64, n, generator=gen).to(t).cuda()
+    mixed = x.clone()
+    big = torch.randperm(64, generator=gen)[:20]
+    mixed[big] = (mixed[big].float() * 0.1 + 50.0).to(t)
+    rest = [i for i in range(64) if i not in set(big.tolist())]
+    out = []
+    for a in (x.cuda(), mixed.cuda()):
+        y, dx = torch.empty_like(a), torch.empty_like(a)
+        gdn.gdn_norm_fwd(a, None, None, None, y, eps=EPS, rms=False)
+        gdn.gdn_norm_bwd(a, None, None, None, dy, dx, None, None, None, gdn.alloc_norm_bwd_workspace(64, n), eps=EPS,
+                         rms=False)
+        out.append((y[rest], dx[rest]))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
