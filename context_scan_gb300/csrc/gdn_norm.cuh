@@ -380,8 +380,10 @@ __device__ __forceinline__ float centred_var(float square, float mean) {
 }
 
 // 1 / (1 + exp(-z)) from the hardware's approximations of 2^x and 1 / x (2 and 1 ulp, subnormals as zero): the
-// rounding of z log2(e) adds |z| / 2 ulp of the exponential. 2^x may overflow to infinity: the quotient is
-// then 0.
+// roundings of z log2(e) and of that constant add 0.6 |z| ulp of the exponential, which shows for negative z: 60 times half an ulp
+// of sigmoid(-80) = 2e-35, never more than half an ulp of 1. With expf, good to 2 ulp whatever z, gated rows take up to
+// 10 % longer forward and 17 % backward (29200 rows of 1999 in bf16 75 -> 83 and 136 -> 156 us). 2^x may overflow to
+// infinity: the quotient is then 0.
 __device__ __forceinline__ float sigmoid(float z) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * z));

@@ -488,7 +488,8 @@ GDN_API gdn_status gdn_cache_compact(void* pages, int layers, int num_pages, siz
  * or term out. With rms == 1, w = 1/sqrt(N) and eps / N for eps it is the L2 normalisation of q and k.
  * x [rows, N] in x_dtype (the rule's out_dtype); z, y [rows, N] in y_dtype; w, b [N] fp32; contiguous.
  * 1 <= N <= 8192, rows >= 0, rows * N < 2^40, eps >= 0 and finite; pointers 16-byte aligned.
- * Sums and statistics are fp32 (a row whose squares leave fp32's range overflows as they do). */
+ * Sums and statistics are fp32 (a row whose squares leave fp32's range overflows as they do), dw and db too;
+ * sigmoid(z) is good to 4 + 0.7 |z| ulp, and 0 where it is no normal number. */
 GDN_API gdn_status gdn_norm_fwd(long long rows, int N, int x_dtype, int y_dtype, int rms, float eps,
                                 const void* x, const float* w, const float* b, const void* z,
                                 void* y, void* stream);
