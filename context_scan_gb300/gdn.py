@@ -141,8 +141,10 @@ def _ptr(t):
 
 def _stream(stream):
     import torch
-    if stream is None:   # the current stream's handle, without a stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        # the current stream's handle; without a stream object around it where this torch has a way to that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 

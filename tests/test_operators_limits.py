@@ -1,5 +1,8 @@
 """Counts near 2^31, which the operators over the state cache step through in 31 bits, are refused on the host
-(no GPU: nothing here gets as far as a launch)."""
+(no GPU: nothing here gets as far as a launch); so are sizes past a C int by the binding. And how that finds
+the current stream."""
+import types
+
 import pytest
 import torch
 
@@ -46,3 +49,15 @@ def test_recurrent_tokens_near_31_bits(L, prob, nseq, cu, per_token):  # noqa: F
     assert recurrent(L, prob=prob, nseq=nseq, cu=cu, per_token=per_token, Hqk=1, n=ROOM) == 2
     if cu is not None:   # (one fewer than the limit is looked at further: here, the missing workspace)
         assert recurrent(L, prob=P(B=1, T=TOP - 4096), nseq=nseq, cu=cu, per_token=per_token, ws=None) == 5
+
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_binding_finds_the_current_stream(monkeypatch, raw):
+    # with torch's short way to the handle and, in a torch that lacks it, by the stream object
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=1234))
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    if raw:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1000 + device, raising=False)
+    assert gdn._stream(None) == (1003 if raw else 1234)
+    assert gdn._stream(77) == 77 and gdn._stream(types.SimpleNamespace(cuda_stream=5)) == 5
