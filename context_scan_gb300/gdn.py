@@ -449,7 +449,7 @@ def _indexes(**arrays):
 
 
 def _room(workspace):
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def gdn_cache_copy(pages, src, dst, workspace, stream=None):

@@ -61,3 +61,10 @@ def test_binding_finds_the_current_stream(monkeypatch, raw):
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1000 + device, raising=False)
     assert gdn._stream(None) == (1003 if raw else 1234)
     assert gdn._stream(77) == 77 and gdn._stream(types.SimpleNamespace(cuda_stream=5)) == 5
+
+
+def test_binding_hands_on_a_missing_workspace():
+    # (the library refuses it with GDN_ERR_WORKSPACE, as for the calls that were there before)
+    assert gdn._room(None) == (None, 0)
+    w = torch.empty(8, dtype=torch.int32)
+    assert gdn._room(w) == (w.data_ptr(), 32)
