@@ -386,8 +386,13 @@ GDN_API gdn_status gdn_varlen_fwd_timed(const gdn_problem* p, int nseq, const in
  * A state cache is an array state [num_slots, H, K, V] fp32: slot (page) i holds one sequence's
  * state. The rule of RFC section 2.1 runs token by token from the state in one slot, in fp32
  * throughout, for any number of tokens from none on -- one new token of every sequence of a decode
- * batch, a few draft tokens, a prompt's last tokens. (Long prompts: gdn_varlen_fwd, whose h_final
- * rows are pages, is faster from about a chunk of tokens on when the shapes allow it.) */
+ * batch, a few draft tokens, a prompt's last tokens.
+ * Whole prompts also go through gdn_varlen_fwd, whose h_final rows are pages. Where that runs on the tensor cores -- bf16
+ * inputs, 64 packed tokens or more, K = V = 128 or per-channel gates; its outputs are off by some 5e-3 of their RMS -- it is the faster
+ * one on one GB300 from about so many tokens a sequence on: scalar gates, 30 to 40 where sequences x heads are 128 or more,
+ * 64 to 128 where they are fewer; per-channel gates, 70 to 250 where sequences x heads are at most 148, and at
+ * no length measured (up to 1024) where they are 256 or more. Elsewhere -- fp32 inputs, K = V = 64 with scalar gates,
+ * packed batches of fewer than 64 tokens -- gdn_recurrent_fwd is the faster one at every length measured. */
 
 /* Workspace bytes for gdn_recurrent_fwd on a cache of num_slots slots: the header and one int per
  * slot. Returns 0 for num_slots < 0. */
