@@ -36,7 +36,8 @@
  *   1 <= nseg (and nseg <= T/64 when T > 0); B*T*H*max(K,V) < 2^40.
  *   in_dtype  in {GDN_DTYPE_F32, GDN_DTYPE_BF16}; out_dtype in {GDN_DTYPE_F32, GDN_DTYPE_BF16}.
  *   bf16 inputs with K == V == 128 run the tcgen05 tensor-core kernels (fp32 accumulation);
- *   fp32 inputs, and bf16 inputs with K == V == 64, run the fp32 CUDA-core kernels.
+ *   fp32 inputs, and bf16 inputs with K == V == 64, run the fp32 CUDA-core kernels (bf16 inputs
+ *   with per-channel gates: see gate_k).
  *   Every device pointer must be 16-byte aligned (GDN_ERR_MISALIGNED otherwise).
  *
  * Ownership: the caller allocates every buffer (device memory) and keeps it alive until the
@@ -102,7 +103,8 @@ typedef struct {
     /* 0: one gate per token and head, g is [B, T, H] (Gated DeltaNet).
      * 1: one gate per key channel, g is [B, T, H, K], and the state decays row by row,
      *    diag(exp(g_t)) H ("KDA Chunk Backward -- TPU/Pallas Kernel Design", section 1.2;
-     *    with either reading above). Runs the fp32 CUDA-core kernels for every dtype. */
+     *    with either reading above). bf16 inputs run their products on the tensor cores with tf32
+     *    operands (fp32 accumulation), fp32 inputs the fp32 CUDA-core kernels. */
     int gate_k;
 } gdn_problem;
 
@@ -338,8 +340,8 @@ GDN_API gdn_status gdn_chunk_bwd_timed(const gdn_problem* p, int nseg, const voi
  * Supporting varlen" (cu_seqlens; every sequence aligned to the chunk size). The tokens stay
  * packed in memory: the alignment is in the chunk numbering, not a padded copy.
  * Supported set: p->B == 1, T >= 0 (any length), nseq >= 1, the K/V/dtype set above;
- * bf16 inputs with K == V == 128 and T >= 64 run the tcgen05 kernels, the rest the CUDA-core
- * kernels. On the tcgen05 path, when every sequence's chains fit the SMs at once, a plan made
+ * bf16 inputs with K == V == 128 and T >= 64 run the tcgen05 kernels, with per-channel gates those
+ * named at gate_k, the rest the CUDA-core kernels. On the tcgen05 path, when every sequence's chains fit the SMs at once, a plan made
  * on the device may cut long sequences into pieces as gdn_segmented_fwd cuts its sequences
  * (RFC section 2.2): piece 0's forward beside the summaries of the middle pieces, their scan,
  * then the forwards of the other pieces, so that a long sequence no longer sets the time
@@ -387,12 +389,14 @@ GDN_API gdn_status gdn_varlen_fwd_timed(const gdn_problem* p, int nseq, const in
  * state. The rule of RFC section 2.1 runs token by token from the state in one slot, in fp32
  * throughout, for any number of tokens from none on -- one new token of every sequence of a decode
  * batch, a few draft tokens, a prompt's last tokens.
- * Whole prompts also go through gdn_varlen_fwd, whose h_final rows are pages. Where that runs on the tensor cores -- bf16
- * inputs, 64 packed tokens or more, K = V = 128 or per-channel gates; its outputs are off by some 5e-3 of their RMS -- it is the faster
- * one on one GB300 from about so many tokens a sequence on: scalar gates, 30 to 40 where sequences x heads are 128 or more,
- * 64 to 128 where they are fewer; per-channel gates, 70 to 250 where sequences x heads are at most 148, and at
- * no length measured (up to 1024) where they are 256 or more. Elsewhere -- fp32 inputs, K = V = 64 with scalar gates,
- * packed batches of fewer than 64 tokens -- gdn_recurrent_fwd is the faster one at every length measured. */
+ * Whole prompts also go through gdn_varlen_fwd, whose h_final rows are pages. Where that runs
+ * on the tensor cores -- bf16 inputs, with per-channel gates or with K = V = 128 and 64 packed
+ * tokens or more; its outputs are off by some 5e-3 of their RMS -- it is the faster one on one
+ * GB300 from about so many tokens a sequence on: scalar gates, 30 to 40 where sequences x heads
+ * are 128 or more, 64 to 128 where they are fewer; per-channel gates, 70 to 250 where sequences
+ * x heads are at most 148, and at no length measured (up to 1024) where they are 256 or more.
+ * Elsewhere -- fp32 inputs, scalar gates with K = V = 64 or fewer than 64 packed tokens --
+ * gdn_recurrent_fwd is the faster one at every length measured. */
 
 /* Workspace bytes for gdn_recurrent_fwd on a cache of num_slots slots: the header and one int per
  * slot. Returns 0 for num_slots < 0. */
@@ -449,8 +453,8 @@ GDN_API size_t gdn_cache_workspace_bytes(int num_pages, int n);
 
 /* Page dst[i] := page src[i] in every layer, i < n; src[i] < 0: page dst[i] := zeros; dst[i] < 0: the
  * pair is skipped, and its src is not read (lists padded to a fixed length). The result is that of
- * reading every page before writing any: a pair whose dst is another pair's dst or (where that pair is not
- * skipped) src is left out and refused, as is one with a number >= num_pages. */
+ * reading every page before writing any: a pair whose dst is another pair's dst or (where that pair
+ * is not skipped) src is left out and refused, as is one with a number >= num_pages. */
 GDN_API gdn_status gdn_cache_copy(void* pages, int layers, int num_pages, size_t page_bytes, int n,
                                   const int* src, const int* dst, void* workspace,
                                   size_t workspace_bytes, void* stream);
@@ -493,8 +497,8 @@ GDN_API gdn_status gdn_cache_compact(void* pages, int layers, int num_pages, siz
  * or term out. With rms == 1, w = 1/sqrt(N) and eps / N for eps it is the L2 normalisation of q and k.
  * x [rows, N] in x_dtype (the rule's out_dtype); z, y [rows, N] in y_dtype; w, b [N] fp32; contiguous.
  * 1 <= N <= 8192, rows >= 0, rows * N < 2^40, eps >= 0 and finite; pointers 16-byte aligned.
- * Sums and statistics are fp32 (a row whose squares leave fp32's range overflows as they do), dw and db too;
- * sigmoid(z) is good to 4 + 0.7 |z| ulp, and 0 where it is no normal number. */
+ * Sums and statistics are fp32 (a row whose squares leave fp32's range overflows as they do), dw and
+ * db too; sigmoid(z) is good to 4 + 0.7 |z| ulp, and 0 where it is no normal number. */
 GDN_API gdn_status gdn_norm_fwd(long long rows, int N, int x_dtype, int y_dtype, int rms, float eps,
                                 const void* x, const float* w, const float* b, const void* z,
                                 void* y, void* stream);
