@@ -341,11 +341,12 @@ GDN_API gdn_status gdn_chunk_bwd_timed(const gdn_problem* p, int nseg, const voi
  * packed in memory: the alignment is in the chunk numbering, not a padded copy.
  * Supported set: p->B == 1, T >= 0 (any length), nseq >= 1, the K/V/dtype set above;
  * bf16 inputs with K == V == 128 and T >= 64 run the tcgen05 kernels, with per-channel gates those
- * named at gate_k, the rest the CUDA-core kernels. On the tcgen05 path, when every sequence's chains fit the SMs at once, a plan made
- * on the device may cut long sequences into pieces as gdn_segmented_fwd cuts its sequences
- * (RFC section 2.2): piece 0's forward beside the summaries of the middle pieces, their scan,
- * then the forwards of the other pieces, so that a long sequence no longer sets the time
- * alone. The results are those of the uncut recurrence within the bf16 tolerance. */
+ * named at gate_k, the rest the CUDA-core kernels. On the tcgen05 path, when every sequence's
+ * chains fit the SMs at once, a plan made on the device may cut long sequences into pieces as
+ * gdn_segmented_fwd cuts its sequences (RFC section 2.2): piece 0's forward beside the summaries
+ * of the middle pieces, their scan, then the forwards of the other pieces, so that a long
+ * sequence no longer sets the time alone. The results are those of the uncut recurrence within
+ * the bf16 tolerance. */
 
 /* Workspace bytes for gdn_varlen_fwd: the error word, the WY tiles of at most T/64 + nseq
  * chunks per head (tensor-core shapes), two int arrays of nseq + 1 and (tensor-core shapes)
