@@ -28,6 +28,8 @@ EXPORTED = ("gdn_workspace_bytes", "gdn_segmented_pieces", "gdn_segmented_plan",
             "gdn_recurrent_workspace_bytes", "gdn_recurrent_fwd",
             "gdn_cache_workspace_bytes", "gdn_cache_copy", "gdn_cache_fork", "gdn_cache_free",
             "gdn_cache_compact", "gdn_norm_fwd", "gdn_norm_bwd_workspace_bytes", "gdn_norm_bwd",
+            "gdn_linear_workspace_bytes", "gdn_linear_fwd", "gdn_linear_bwd", "gdn_linear_recurrent_fwd",
+            "gdn_qk_norm_fwd", "gdn_qk_norm_bwd_workspace_bytes", "gdn_qk_norm_bwd",
             "gdn_status_string", "gdn_check_device_error", "gdn_selftest_wait_timeout")
 
 
@@ -43,6 +45,13 @@ class Problem(ctypes.Structure):
                 ("K", ctypes.c_int), ("V", ctypes.c_int), ("chunk", ctypes.c_int),
                 ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
                 ("decay_first", ctypes.c_int), ("gate_k", ctypes.c_int)]
+
+
+class QkProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("K", ctypes.c_int), ("R", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("x_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong)]
 
 
 _lib = None
@@ -100,6 +109,17 @@ def lib():
         L.gdn_norm_bwd_workspace_bytes.argtypes = [ctypes.c_longlong, ctypes.c_int]
         L.gdn_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_norm_bwd.argtypes = rows + [_P] * 9 + ws
+        L.gdn_linear_workspace_bytes.argtypes = [pp, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+        L.gdn_linear_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_linear_fwd.argtypes = [pp, ctypes.c_int, ctypes.c_int] + [_P] * 8 + ws
+        L.gdn_linear_bwd.argtypes = [pp, ctypes.c_int, ctypes.c_int] + [_P] * 12 + ws
+        L.gdn_linear_recurrent_fwd.argtypes = ([pp, ctypes.c_int, ctypes.c_int] + [_P] * 6 + [ctypes.c_int] +
+                                               [_P] * 2 + [ctypes.c_int, _P] + ws)
+        qk = ctypes.POINTER(QkProblem)
+        L.gdn_qk_norm_fwd.argtypes = [qk] + [_P] * 9
+        L.gdn_qk_norm_bwd_workspace_bytes.argtypes = [ctypes.c_int]
+        L.gdn_qk_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_qk_norm_bwd.argtypes = [qk] + [_P] * 12 + ws
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_check_device_error.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_uint)]
@@ -110,7 +130,8 @@ def lib():
                    "gdn_selftest_wait_timeout", "gdn_state_grad_summary", "gdn_state_grad_scan",
                    "gdn_chunk_bwd", "gdn_chunk_bwd_timed", "gdn_recurrent_fwd", "gdn_cache_copy",
                    "gdn_cache_fork", "gdn_cache_free", "gdn_cache_compact", "gdn_norm_fwd",
-                   "gdn_norm_bwd"):
+                   "gdn_norm_bwd", "gdn_linear_fwd", "gdn_linear_bwd", "gdn_linear_recurrent_fwd",
+                   "gdn_qk_norm_fwd", "gdn_qk_norm_bwd"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -537,6 +558,159 @@ def gdn_norm_bwd(x, w, b, z, dy, dx, dz, dw, db, workspace, eps=1e-6, rms=True, 
     _check(lib().gdn_norm_bwd(rows, N, _dtype_code(x), _dtype_code(dy), int(rms), eps, _ptr(x), _ptr(w),
                               _ptr(b), _ptr(z), _ptr(dy), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(db),
                               *_room(workspace), _stream(stream)), "gdn_norm_bwd")
+
+
+def _linear(q, k, v, decay, o, cu_seqlens, states, **more):
+    """(problem, Hqk, nseq) of a linear-attention call, its tensors' shapes and types checked: q, k [B, T, Hqk, K], v
+    and what is like it [B, T, H, V], states [nseq, H, K, V] fp32, o (or its gradient) of a type of its own."""
+    import torch
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"k is {tuple(k.shape)}, v {tuple(v.shape)}, not [B, T, heads, channels]")
+    B, T, H, V = v.shape
+    Hqk, K = k.shape[2:]
+    nseq = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    if k.shape[:2] != (B, T):
+        raise ValueError(f"k is {tuple(k.shape)}, v {tuple(v.shape)}")
+    for name, n in (("B", B), ("T", T), ("H", H), ("the number of sequences", nseq)):
+        _int(name, n)
+    _is("q", q, k.dtype, k.shape)
+    _is("v", v, k.dtype, v.shape)
+    _is("o", o, None if o is None else o.dtype, v.shape)
+    _is("decay", decay, torch.float32, (H,))
+    _is("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,))
+    for name, t in states.items():
+        _is(name, t, torch.float32, (nseq, H, K, V))
+    for name, (t, like) in more.items():
+        _is(name, t, like.dtype, like.shape)
+    return Problem(B, T, H, K, V, 64, _dtype_code(k), _dtype_code(v if o is None else o), 0, 0), Hqk, nseq
+
+
+def alloc_linear_workspace(k, v, cu_seqlens=None, backward=False):
+    """A zeroed workspace tensor for gdn_linear_fwd (or gdn_linear_bwd) on tensors of these shapes, on their device."""
+    import torch
+    prob, Hqk, nseq = _linear(k, k, v, None, None, cu_seqlens, {})
+    n = int(lib().gdn_linear_workspace_bytes(ctypes.byref(prob), Hqk, nseq, int(backward)))
+    if n == 0:
+        raise GdnError(2, "gdn_linear_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=k.device)
+
+
+def gdn_linear_fwd(q, k, v, decay, h0, o, h_final, workspace, cu_seqlens=None, stream=None):
+    """Linear attention with a decay for each head, H_t = exp(decay[h]) H_{t-1} + k_t v_t^T, o_t = q_t^T H_t, in chunks: q, k
+    [B, T, Hqk, K], v, o [B, T, H, V], decay [H] fp32, h0, h_final [nseq, H, K, V] fp32 (or None). Without cu_seqlens B
+    sequences of T tokens; with it (int32, on the GPU) B == 1 and len(cu_seqlens) - 1 packed sequences."""
+    _on_device(q, k, v, decay, h0, o, h_final, workspace, cu_seqlens)
+    prob, Hqk, nseq = _linear(q, k, v, decay, o, cu_seqlens, dict(h0=h0, h_final=h_final))
+    _check(lib().gdn_linear_fwd(ctypes.byref(prob), Hqk, nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                _ptr(decay), _ptr(h0), o.data_ptr(), _ptr(h_final), *_room(workspace),
+                                _stream(stream)), "gdn_linear_fwd")
+
+
+def gdn_linear_bwd(q, k, v, decay, h0, dO, dht, dq, dk, dv, dh0, workspace, cu_seqlens=None, stream=None):
+    """Gradients of gdn_linear_fwd for dO (o's type) and dht (or None): dq, dk, dv (q's, k's and v's shape and type) and
+    dh0 (or None). workspace: alloc_linear_workspace(..., backward=True)."""
+    _on_device(q, k, v, decay, h0, dO, dht, dq, dk, dv, dh0, workspace, cu_seqlens)
+    prob, Hqk, nseq = _linear(q, k, v, decay, dO, cu_seqlens, dict(h0=h0, dht=dht, dh0=dh0), dq=(dq, q), dk=(dk, k),
+                              dv=(dv, v))
+    _check(lib().gdn_linear_bwd(ctypes.byref(prob), Hqk, nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                _ptr(decay), _ptr(h0), dO.data_ptr(), _ptr(dht), dq.data_ptr(), dk.data_ptr(),
+                                dv.data_ptr(), _ptr(dh0), *_room(workspace), _stream(stream)), "gdn_linear_bwd")
+
+
+def gdn_linear_recurrent_fwd(q, k, v, decay, state, slots_in, slots_out, o, workspace, cu_seqlens=None,
+                             per_token=False, stream=None):
+    """The same rule token by token over a state cache [num_slots, H, K, V] fp32, as gdn_recurrent_fwd takes it;
+    workspace: alloc_recurrent_workspace(num_slots)."""
+    import torch
+    _on_device(q, k, v, decay, state, slots_in, slots_out, o, workspace, cu_seqlens)
+    prob, Hqk, nseq = _linear(q, k, v, decay, o, cu_seqlens, {})
+    B, T, H, V = v.shape
+    slots = 0 if state is None else _int("the number of slots", state.shape[0])
+    _is("state", state, torch.float32, (slots, H, k.shape[-1], V))
+    _is("slots_in", slots_in, torch.int32, (nseq,))
+    _is("slots_out", slots_out, torch.int32, (B * T if per_token else nseq,))
+    _check(lib().gdn_linear_recurrent_fwd(ctypes.byref(prob), Hqk, nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(),
+                                          v.data_ptr(), _ptr(decay), _ptr(state), slots, _ptr(slots_in), _ptr(slots_out),
+                                          int(per_token), o.data_ptr(), *_room(workspace), _stream(stream)),
+           "gdn_linear_recurrent_fwd")
+
+
+def _head_stride(name, t, like=None):
+    """Values from one token of t [B, T, heads, K] to the next; within a token the heads lie side by side."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} is {tuple(t.shape)}, not [B, T, heads, K]")
+    B, T, H, K = t.shape
+    if like is not None:
+        _is(name, t, like.dtype, like.shape)
+    b, n, h, c = t.stride()
+    n = n if T > 1 else b if B > 1 else H * K    # (the strides of axes of one entry say nothing)
+    if (c != 1 and K > 1) or (h != K and H > 1) or (B > 1 and T > 1 and b != T * n) or n < H * K:
+        raise ValueError(f"{name} has strides {t.stride()}: wanted are heads side by side, tokens evenly apart")
+    return n
+
+
+def _qk(q, k, wq, wk, freq, y_dtype, positions, eps, interleaved):
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    for name, t in (("q", q), ("k", k)):
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    _on_device(wq, wk, freq, positions)
+    qs, ks = _head_stride("q", q), _head_stride("k", k)
+    B, T, Hq, K = q.shape
+    for name, n in (("B", B), ("T", T), ("Hq", Hq), ("Hk", k.shape[2]), ("K", K)):
+        _int(name, n)
+    _is("k", k, q.dtype, (B, T, k.shape[2], K))
+    R = 0 if freq is None else 2 * freq.numel()
+    _is("wq", wq, torch.float32, (K,))
+    _is("wk", wk, torch.float32, (K,))
+    _is("freq", freq, torch.float32, (R // 2,))
+    if positions is not None and (positions.dtype != torch.int32 or positions.numel() != B * T):
+        raise ValueError("positions holds one int32 a token")
+    return QkProblem(B, T, Hq, k.shape[2], K, R, int(interleaved), _dtype_code(q), y_dtype, eps, qs, ks)
+
+
+def gdn_qk_norm_fwd(q, k, wq, wk, freq, yq, yk, positions=None, eps=1e-6, interleaved=False, stream=None):
+    """Every head of q [B, T, Hq, K] and k [B, T, Hk, K] (tokens evenly apart: parts of one projection's rows, say)
+    normalised by its root mean square, scaled by wq, wk [K] fp32 (or None) and rotated by its position: freq [R / 2]
+    fp32 (or None: not rotated), positions int32 (or None: 0 .. T - 1). yq, yk: contiguous, of one type."""
+    prob = _qk(q, k, wq, wk, freq, _dtype_code(yq), positions, eps, interleaved)
+    _on_device(yq, yk)
+    _is("yq", yq, yq.dtype, q.shape)
+    _is("yk", yk, yq.dtype, k.shape)
+    _check(lib().gdn_qk_norm_fwd(ctypes.byref(prob), q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freq),
+                                 _ptr(positions), yq.data_ptr(), yk.data_ptr(), _stream(stream)), "gdn_qk_norm_fwd")
+
+
+def alloc_qk_norm_bwd_workspace(q, k=None):
+    """A workspace tensor for gdn_qk_norm_bwd on heads like q's, on its device."""
+    import torch
+    n = int(lib().gdn_qk_norm_bwd_workspace_bytes(_int("K", q.shape[-1])))
+    if n == 0:
+        raise GdnError(2, "gdn_qk_norm_bwd_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def gdn_qk_norm_bwd(q, k, wq, wk, freq, dyq, dyk, dq, dk, dwq, dwk, workspace, positions=None, eps=1e-6,
+                    interleaved=False, stream=None):
+    """Gradients of gdn_qk_norm_fwd for dyq, dyk (contiguous): dq, dk (q's and k's type, shape and token stride), dwq, dwk [K]
+    fp32 (None skips either)."""
+    import torch
+    prob = _qk(q, k, wq, wk, freq, _dtype_code(dyq), positions, eps, interleaved)
+    _on_device(dyq, dyk, dwq, dwk, workspace)
+    _is("dyq", dyq, dyq.dtype, q.shape)
+    _is("dyk", dyk, dyq.dtype, k.shape)
+    for name, t, like, stride in (("dq", dq, q, prob.q_stride), ("dk", dk, k, prob.k_stride)):
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+        if _head_stride(name, t, like) != stride and t.shape[0] * t.shape[1] > 1:
+            raise ValueError(f"{name} has another token stride than its input")
+    K = q.shape[-1]
+    _is("dwq", dwq, torch.float32, (K,))
+    _is("dwk", dwk, torch.float32, (K,))
+    _check(lib().gdn_qk_norm_bwd(ctypes.byref(prob), q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freq),
+                                 _ptr(positions), dyq.data_ptr(), dyk.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                 _ptr(dwq), _ptr(dwk), *_room(workspace), _stream(stream)), "gdn_qk_norm_bwd")
 
 
 def gdn_selftest_wait_timeout(workspace, limit_cycles, stream=None):

@@ -518,6 +518,101 @@ GDN_API gdn_status gdn_norm_bwd(long long rows, int N, int x_dtype, int y_dtype,
                                 const void* dy, void* dx, void* dz, float* dw, float* db,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Linear attention with a decay for each head
+ * ---------------------------------------------------------------------------------------
+ * The rule without the delta term and with a constant gate:
+ *   H_t = exp(decay[h]) H_{t-1} + k_t v_t^T,   o_t = q_t^T H_t
+ * (no query scale), for layers whose heads each forget at a rate of their own. decay [H] fp32, DEVICE, a natural
+ * logarithm (<= 0; -inf and anything below -200 forget at once). It is a constant of the layer: it gets no gradient.
+ * q, k [B,T,Hqk,K] and v, o [B,T,H,V] with p->H % Hqk == 0 (head h reads q/k head h / (H / Hqk)); states [H,K,V]
+ * fp32, as everywhere here, so that state caches and their pages serve both rules. K and V in {64, 128}, each;
+ * p->decay_first and p->gate_k must be 0; p->chunk is not read. B*T < 2^31 - 4096, nseq*H < 2^28.
+ * Any T. With cu_seqlens NULL, p->B == nseq sequences of p->T tokens; else p->B == 1 and sequence s holds tokens
+ * cu_seqlens[s] .. cu_seqlens[s+1]-1 ([nseq + 1] int32 DEVICE array: 0 first, non-decreasing, p->T at most; rows
+ * behind the last sequence are neither read into any result nor written). A bad cu_seqlens writes nothing and is recorded in
+ * the error word (GDN_ERR_INVALID_ARG from gdn_check_device_error). Nothing is read back to the host: every call can
+ * be captured in a CUDA graph. decay and cu_seqlens need 4-byte alignment, every other pointer 16. Calls that share
+ * a workspace must not overlap; its first 256 bytes must be zero before the first call.
+ * bf16 inputs and outputs run on the tensor cores: products of bf16 values summed in fp32, where the weighted
+ * attention inside a chunk of 128 tokens and the state that a chunk's outputs read are rounded to bf16 once, and the state
+ * itself is fp32, its updates good to 2^-17 of each term. A NaN or infinity in one token may then reach the
+ * outputs of the tokens of its chunk that lie before it (never those of another sequence). Other types run in fp32
+ * throughout. */
+
+/* Workspace bytes for gdn_linear_fwd (backward == 0) or gdn_linear_bwd (1), with or without cu_seqlens. Depends
+ * on the sizes and the current device's SM count, not on the lengths. Returns 0 for an invalid problem. */
+GDN_API size_t gdn_linear_workspace_bytes(const gdn_problem* p, int Hqk, int nseq, int backward);
+
+/* The chunked form, for prompts and training.
+ *   h0       [nseq,H,K,V] fp32, or NULL for zero states
+ *   o        [B,T,H,V] out_dtype, written
+ *   h_final  [nseq,H,K,V] fp32, the state after each sequence's last token (after none: h0); NULL skips it */
+GDN_API gdn_status gdn_linear_fwd(const gdn_problem* p, int Hqk, int nseq, const int* cu_seqlens, const void* q,
+                                  const void* k, const void* v, const float* decay, const float* h0,
+                                  void* o, float* h_final, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Its gradients: of L = sum_t dO_t . o_t + <dht, h_final>, from the inputs alone (nothing is kept from the forward).
+ *   dO       [B,T,H,V] out_dtype; dht [nseq,H,K,V] fp32, or NULL (zero)
+ *   dq, dk   [B,T,Hqk,K] in_dtype, written: of shared heads, the sums over the heads that read them, in a fixed order
+ *   dv       [B,T,H,V] in_dtype, written
+ *   dh0      [nseq,H,K,V] fp32 (of an empty sequence: dht); NULL skips it
+ * Outputs overlap nothing. */
+GDN_API gdn_status gdn_linear_bwd(const gdn_problem* p, int Hqk, int nseq, const int* cu_seqlens, const void* q,
+                                  const void* k, const void* v, const float* decay, const float* h0,
+                                  const void* dO, const float* dht, void* dq, void* dk, void* dv,
+                                  float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The recurrent form over a state cache, for decode, draft tokens and the ends of prompts: gdn_recurrent_fwd with the rule
+ * above. Slots, per_token, refusals and workspace (gdn_recurrent_workspace_bytes) are those of that call; cu_seqlens may
+ * end before p->T (then slots_out with per_token is not read for the tokens behind). fp32 throughout. */
+GDN_API gdn_status gdn_linear_recurrent_fwd(const gdn_problem* p, int Hqk, int nseq, const int* cu_seqlens,
+                                            const void* q, const void* k, const void* v,
+                                            const float* decay, float* state, int num_slots,
+                                            const int* slots_in, const int* slots_out, int per_token,
+                                            void* o, void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Norm of the query and key heads with the position rotation, and its gradients
+ * ---------------------------------------------------------------------------------------
+ * What precedes a rule in a layer: every head of every token is normalised, scaled and turned by the token's position n,
+ *   u = x s w,  s = 1 / sqrt(mean(x^2) + eps),
+ *   (y_a, y_b) = (u_a cos t - u_b sin t, u_b cos t + u_a sin t),  t = n freq_i,  for the R / 2 pairs (a, b),
+ *   y = u for the K - R channels behind the first R.
+ * Pair i is (i, i + R / 2), or with interleaved == 1 (2 i, 2 i + 1). With w = 1/sqrt(K) and eps / K for eps this is
+ * the L2 normalisation that the delta rule takes its q and k in. t is formed modulo a turn in 64 bits: any position is
+ * as exact as the first. */
+typedef struct {
+    int B, T;                      /* sequences and tokens; packed ones: B = 1 and positions given */
+    int Hq, Hk, K;                 /* heads of q and of k, channels of a head: even, 2 .. 256 */
+    int R;                         /* rotated channels: even, 0 (the norm alone) .. K */
+    int interleaved;
+    int x_dtype, y_dtype;          /* of q, k and their gradients; of the results and their gradients */
+    float eps;                     /* >= 0 and finite */
+    long long q_stride, k_stride;  /* values from one token of q (k) to the next, Hq*K (Hk*K) at least: q and k, and dq
+                                      and dk, may be parts of the rows of one projection; below 2^31 */
+} gdn_qk_problem;
+
+/* q [B,T,Hq,K], k [B,T,Hk,K] at their strides; wq, wk [K] fp32 or NULL (ones); freq [R / 2] fp32, finite (NULL with
+ * R == 0); positions [B*T] int32, or NULL: 0 .. T - 1 in every sequence; yq, yk [B,T,H*,K] contiguous, which overlap no
+ * input. Every pointer needs its type's alignment; all of 16 bytes (and strides of as much) run fastest.
+ * B*T < 2^31, Hq and Hk at most 4096. */
+GDN_API gdn_status gdn_qk_norm_fwd(const gdn_qk_problem* p, const void* q, const void* k, const float* wq,
+                                   const float* wk, const float* freq, const int* positions, void* yq,
+                                   void* yk, void* stream);
+
+/* Workspace bytes for gdn_qk_norm_bwd (at most 3 MiB). It needs no initial value. Returns 0 for a K outside the set. */
+GDN_API size_t gdn_qk_norm_bwd_workspace_bytes(int K);
+
+/* The gradients for dyq, dyk (contiguous, in y_dtype): dq, dk in x_dtype at q's and k's strides (what lies between the
+ * rows is left as it was); dwq, dwk [K] fp32, summed in a fixed order (NULL skips either). Outputs overlap nothing. */
+GDN_API gdn_status gdn_qk_norm_bwd(const gdn_qk_problem* p, const void* q, const void* k, const float* wq,
+                                   const float* wk, const float* freq, const int* positions,
+                                   const void* dyq, const void* dyk, void* dq, void* dk, float* dwq,
+                                   float* dwk, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Self-test of the failure path every kernel wait takes: one CTA waits on a barrier that
  * nothing arrives at, with a limit of limit_cycles SM clock cycles (1 .. 2^32), then records
  * GDN_ERR_TIMEOUT (detail word 0x5E) in the workspace's device error word and returns, as a
@@ -531,7 +626,7 @@ GDN_API const char* gdn_status_string(gdn_status s);
 
 /* Synchronises `stream`, reads the workspace's device error word, clears it, and returns
  * GDN_OK, GDN_ERR_TIMEOUT (a bounded wait ran out; the results of the affected calls are
- * invalid), GDN_ERR_INVALID_ARG (gdn_varlen_fwd or gdn_recurrent_fwd got a bad cu_seqlens, or an
+ * invalid), GDN_ERR_INVALID_ARG (a call got a bad cu_seqlens, or an
  * entry of an index array was refused), GDN_ERR_NO_PAGE (gdn_cache_fork) or GDN_ERR_CUDA. If `detail` is non-NULL it receives the
  * recorded detail word (which wait gave up, which check failed), or 0. */
 GDN_API gdn_status gdn_check_device_error(void* workspace, void* stream, unsigned* detail);
