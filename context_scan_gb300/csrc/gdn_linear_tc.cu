@@ -1,5 +1,595 @@
+// gdn_linear_tc.cu -- linear attention with a decay for each head on the 5th-generation tensor cores: bf16 inputs and outputs
+// (the forward and, with the roles changed, the three gradients: gdn_linear.cuh).
+//
+// A CTA owns one piece of one sequence and one head, and walks over its chunks of 128 tokens. Per chunk, with weights w^..
+// of the head's constant decay:
+//   S = A B^T                              128 x 128 x dA
+//   P = S with the weights of the gaps, masked, rounded to bf16 (tensor memory, over S)
+//   O = A X                                128 x dC x dA, X the state entering the chunk, rounded to bf16 (shared memory)
+//   O = w^(i + 1 - s) O, row by row        (through registers: the row's weight is not rounded)
+//   O += P C                               128 x dC x 128
+//   U^T = Cw^T B                           dC x dA x 128, Cw = C with the weights of the update, as an unevaluated sum of
+//                                          two bf16 values (tensor memory), so that the state gets products good to 2^-17
+//   X' = w^L X + U                         fp32, in registers
+// The state never passes through bf16 on its own way. U is formed transposed, with the scaled operand in tensor memory:
+// its 128 rows (channels of C) are then the lanes, each of which scales its own channel; the chunk's tiles fill shared
+// memory (two stages of A, B, C: 192 KB, and 32 KB of X), which would not hold scaled copies as well.
+//
+// Warps: 0-3 P, the scaling of O, the outputs; 4-11 the state: Cw (each half of them 64 tokens) and X (each half 64 rows);
+// 12 loads (TMA, 128-byte swizzle), 13 issues the MMAs. Every wait on an mbarrier is bounded: on expiry the kernel records
+// GDN_ERR_TIMEOUT, lets what it issued retire, frees tensor memory and returns.
+//
+// A sequence's last chunk may hold fewer than 128 tokens: the rows of B and C behind it (the next sequence's) are
+// overwritten by zeros in shared memory, so that nothing of another sequence enters a sum, not as 0 times NaN either.
+#include <cstring>
+
 #include "gdn_linear.cuh"
-namespace gdn { namespace linear {
-bool tc_supported(const Params& p) { return false; }
-cudaError_t launch_tc(const Params& p, cudaStream_t s) { return cudaErrorInvalidValue; }
-} }
+#include "gdn_pair.cuh"
+#include "gdn_tc_common.cuh"
+
+namespace gdn {
+namespace linear {
+namespace {
+
+constexpr int kThreads = 448;
+constexpr int kStateThreads = 256;
+constexpr int kLoadWarp = 12, kMmaWarp = 13;
+constexpr long long kWaitLimit = 4000000000LL;   // SM cycles, some two seconds
+
+constexpr uint32_t kHalf = 16384;                // 128 tokens x 64 features
+constexpr uint32_t kTileBytes = 2 * kHalf;
+constexpr uint32_t kStage = 3 * kTileBytes;      // A, B, C
+constexpr uint32_t kX = 2 * kStage;              // [dA / 64][dC rows of 128 bytes]
+constexpr uint32_t kTab = kX + kTileBytes;       // w^0 .. w^128
+constexpr uint32_t kKey = kTab + 132 * 4;        // weights of the update (see below): 256
+constexpr uint32_t kBar = kKey + 256 * 4;
+constexpr uint32_t kSmem = kBar + 256 + 1024;    // (with the slack of a 1024-byte alignment)
+static_assert(kSmem <= 232448, "shared memory");
+static_assert(kTab % 16 == 0 && kKey % 16 == 0 && kBar % 16 == 0, "alignment");
+
+// tensor memory, columns
+constexpr uint32_t kTmS = 0, kTmU = 128, kTmHi = 256, kTmLo = 320, kTmO = 384;
+
+// mbarriers, 8 bytes each from kBar on
+enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_DRAIN, B_N };
+constexpr unsigned kTag = 0x60;   // + the barrier's number
+
+struct TcParams {
+    Params p;
+    CUtensorMap a[kMaxRoles], b[kMaxRoles], c[kMaxRoles];
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
+        "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
+        "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]),
+        "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ float lds(uint32_t at) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
+    return x;
+}
+__device__ __forceinline__ float4 lds4(uint32_t at) {
+    float4 x;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at));
+    return x;
+}
+// a bf16 value as fp32
+__device__ __forceinline__ float lds_bf16(uint32_t at) {
+    unsigned short x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at));
+    return __uint_as_float((unsigned)x << 16);
+}
+__device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// What every warp of the CTA knows of its work.
+struct Work {
+    const Params* p;
+    const Role* r;
+    Item it;
+    int h, chunks, n;      // chunks of the piece, of the sequence
+    bool sums;             // phase 1's middle pieces: U alone
+    uint32_t base, tmem;
+    volatile int* abort_flag;
+    float lg;
+    __device__ __forceinline__ int phys(int m) const { return r->rev ? n - 1 - (it.m0 + m) : it.m0 + m; }
+    __device__ __forceinline__ int length(int m) const { return min(kChunk, it.len - kChunk * phys(m)); }
+    __device__ __forceinline__ uint32_t bar(int i) const { return base + kBar + 8 * i; }
+    // the whole warp waits; every lane gets the same verdict
+    __device__ __forceinline__ bool wait(int i, int parity) const {
+        const bool ok = mbar_wait(bar(i), parity & 1, abort_flag, kWaitLimit, p->err, kTag + i);
+        return __all_sync(0xffffffffu, ok);
+    }
+    __device__ __forceinline__ bool wait1(int i, int parity) const {   // one lane
+        return mbar_wait(bar(i), parity & 1, abort_flag, kWaitLimit, p->err, kTag + i);
+    }
+};
+
+template <int DA, int DC>
+__device__ __forceinline__ void load_warp(const Work& w, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* mc) {
+    const int rep = w.p->H;
+    const int ah = w.h / (rep / w.r->a_heads), bh = w.h / (rep / w.r->b_heads), ch = w.h / (rep / w.r->c_heads);
+    const uint32_t bytes = (DA / 64) * kHalf * (w.sums ? 1 : 2) + (DC / 64) * kHalf;
+    int issued = 0;
+    for (int m = 0; m < w.chunks; ++m) {
+        const int s = m & 1;
+        if (m >= 2 && !w.wait1(B_EMPTY0 + s, (m >> 1) - 1)) break;
+        const uint32_t to = w.base + s * kStage, full = w.bar(B_FULL0 + s);
+        const int row = w.it.lo + kChunk * w.phys(m);
+        mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+        for (int f = 0; f < DA / 64; ++f) {
+            if (!w.sums) tma_load_3d(to + f * kHalf, ma, full, 64 * f, ah, row);
+            tma_load_3d(to + kTileBytes + f * kHalf, mb, full, 64 * f, bh, row);
+        }
+#pragma unroll
+        for (int f = 0; f < DC / 64; ++f) tma_load_3d(to + 2 * kTileBytes + f * kHalf, mc, full, 64 * f, ch, row);
+        issued = m + 1;
+    }
+    if (*w.abort_flag)   // (what is in flight lands before shared memory is given back)
+        for (int m = max(0, issued - 2); m < issued; ++m) mbar_drain(w.bar(B_FULL0 + (m & 1)), (m >> 1) & 1, kWaitLimit);
+}
+
+template <int DA, int DC>
+__device__ __forceinline__ void mma_warp(const Work& w) {
+    constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_OI = idesc_bf16(128, DC, false, false),
+                       ID_OP = idesc_bf16(128, DC, false, true), ID_U = idesc_bf16(128, DA, false, true);
+    bool zero_seen = false;
+    auto ready = [&](int m) {   // the chunk's tiles have landed, and end in zeros where they should
+        if (!w.wait1(B_FULL0 + (m & 1), m >> 1)) return false;
+        if (w.length(m) < kChunk && !zero_seen) {
+            if (!w.wait1(B_ZERO, 0)) return false;
+            zero_seen = true;
+        }
+        return true;
+    };
+    auto s_mma = [&](int m) {
+        const uint32_t A = w.base + (m & 1) * kStage, B = A + kTileBytes;
+#pragma unroll
+        for (int k = 0; k < DA / 16; ++k) {
+            const uint32_t at = (k / 4) * kHalf + (k % 4) * 32;
+            mma_ss<ID_S>(w.tmem + kTmS, desc_k(A + at), desc_k(B + at), k > 0);
+        }
+        mma_commit(w.bar(B_S));
+    };
+    int m = 0;
+    for (; m < w.chunks; ++m) {
+        const uint32_t A = w.base + (m & 1) * kStage, B = A + kTileBytes, C = B + kTileBytes;
+        if (w.sums) {
+            if (!ready(m)) break;
+        } else {
+            if (m == 0) {
+                if (!ready(0)) break;
+                tc_fence_after();
+                s_mma(0);
+            }
+            if (!w.wait1(B_X, m) || (m > 0 && !w.wait1(B_OFREE, m - 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < DA / 16; ++k)
+                mma_ss<ID_OI>(w.tmem + kTmO, desc_k(A + (k / 4) * kHalf + (k % 4) * 32),
+                              desc_k(w.base + kX + (k / 4) * (DC * 128) + (k % 4) * 32), k > 0);
+            mma_commit(w.bar(B_OI));
+        }
+        if (!w.wait1(B_VD, m)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mma_ts_bf16<ID_U>(w.tmem + kTmU, w.tmem + (part ? kTmLo : kTmHi) + 8 * k, desc_mn(B + 2048 * k, kHalf),
+                                  part + k > 0);
+        mma_commit(w.bar(B_U));
+        if (w.sums) {
+            mma_commit(w.bar(B_EMPTY0 + (m & 1)));
+            continue;
+        }
+        if (!w.wait1(B_P, m) || !w.wait1(B_OSCALED, m)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            mma_ts_bf16<ID_OP>(w.tmem + kTmO, w.tmem + kTmS + 8 * k, desc_mn(C + 2048 * k, kHalf), 1u);
+        mma_commit(w.bar(B_O));
+        mma_commit(w.bar(B_EMPTY0 + (m & 1)));
+        if (m + 1 < w.chunks) {
+            if (!ready(m + 1) || !w.wait1(B_O, m)) break;
+            tc_fence_after();
+            s_mma(m + 1);
+        }
+    }
+    if (m < w.chunks) {
+        mma_commit(w.bar(B_DRAIN));
+        mbar_drain(w.bar(B_DRAIN), 0, kWaitLimit);
+    }
+}
+
+// P, the scaling of O, the outputs: thread = row (token) of the chunk = lane of tensor memory
+template <int DA, int DC>
+__device__ __forceinline__ void out_warps(const Work& w, int warp, int lane) {
+    const Role& r = *w.r;
+    const int row = 32 * warp + lane;
+    const uint32_t lanes = w.tmem + ((uint32_t)(32 * warp) << 16);
+    const uint32_t tab = w.base + kTab;
+    // w^(31 - c) (or, backward in time, w^c) for the 32 columns of a block: what is left of a gap to another block's column
+    pair_t col[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+        col[c] = r.rev ? pack(lds(tab + 4 * (2 * c)), lds(tab + 4 * (2 * c + 1)))
+                       : pack(lds(tab + 4 * (31 - 2 * c)), lds(tab + 4 * (30 - 2 * c)));
+    for (int m = 0; m < w.chunks; ++m) {
+        const int L = w.length(m);
+        if (!w.wait(B_S, m)) return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+            uint32_t q[16];
+            const int away = r.rev ? b - warp : warp - b;
+            if (away < 0) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) q[c] = 0;
+            } else {
+                float x[32];
+                tmem_ld32(lanes + kTmS + 32 * b, x);
+                tmem_wait_ld();
+                if (away == 0) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const int gap = r.rev ? c - lane : lane - c;
+                        x[c] = gap >= 0 ? x[c] * lds(tab + 4 * max(gap, 0)) : 0.f;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) q[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
+                } else {
+                    const float f = lds(tab + 4 * (r.rev ? 32 * away - lane : 32 * away + lane - 31));
+                    const pair_t f2 = pack(f, f);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        float lo, hi;
+                        unpack(mul2(pack(x[2 * c], x[2 * c + 1]), mul2(f2, col[c])), lo, hi);
+                        q[c] = pack_bf16(lo, hi);
+                    }
+                }
+            }
+            tmem_st16(lanes + kTmS + 16 * b, q);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(w.bar(B_P));
+        if (!w.wait(B_OI, m)) return;
+        tc_fence_after();
+        const float keep = exp2f(w.lg * (r.rev ? max(L - 1 - row, 0) : row + 1));
+#pragma unroll 1
+        for (int b = 0; b < DC / 32; ++b) {
+            float x[32];
+            tmem_ld32(lanes + kTmO + 32 * b, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] *= keep;
+            tmem_st32(lanes + kTmO + 32 * b, x);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(w.bar(B_OSCALED));
+        if (!w.wait(B_O, m)) return;
+        tc_fence_after();
+        const long long at = ((long long)(w.it.lo + kChunk * w.phys(m) + row) * w.p->H + w.h) * DC;
+#pragma unroll 1
+        for (int b = 0; b < DC / 32; ++b) {
+            float x[32];
+            tmem_ld32(lanes + kTmO + 32 * b, x);
+            tmem_wait_ld();
+            if (b == DC / 32 - 1) {
+                tc_fence_before();
+                mbar_arrive(w.bar(B_OFREE));
+            }
+            if (row < L) {
+                if (r.out_bf16) {
+                    uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(r.out) + at + 32 * b);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        to[c] = make_uint4(pack_bf16(x[8 * c], x[8 * c + 1]), pack_bf16(x[8 * c + 2], x[8 * c + 3]),
+                                           pack_bf16(x[8 * c + 4], x[8 * c + 5]), pack_bf16(x[8 * c + 6], x[8 * c + 7]));
+                } else {
+                    float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(r.out) + at + 32 * b);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) to[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+                }
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// Cw and the state: thread = channel of C = lane of tensor memory; the two halves of the warps take 64 tokens of Cw and 64
+// rows of the state each
+template <int DA, int DC>
+__device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
+    const Role& r = *w.r;
+    const int half = warp >> 2, quarter = warp & 3;
+    const int chan = 32 * quarter + lane, c = chan & (DC - 1);   // (with DC = 64, lanes 64 .. repeat channels 0 ..)
+    const bool mine = chan < DC && 64 * half < DA;               // holds rows of the state
+    const uint32_t lanes = w.tmem + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t key = w.base + kKey;
+    constexpr long long kState = (long long)DA * DC;
+    float X[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) X[i] = 0.f;
+    auto slot = [&](int q) {
+        return r.slots + ((long long)(w.it.slot0 + q - 1) * w.p->H + w.h) * kState + (long long)64 * half * DC + c;
+    };
+    auto given = [&](auto base) {   // of a state as the caller stores it: this thread's row 0
+        const auto at = base + ((long long)w.it.seq * w.p->H + w.h) * kState;
+        return r.state_t ? at + (long long)c * DA + 64 * half : at + (long long)64 * half * DC + c;
+    };
+    if (mine) {
+        if (w.it.piece == 0) {
+            if (r.start) {
+                const float* from = given(r.start);
+                const int step = r.state_t ? 1 : DC;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) X[i] = __ldg(from + i * step);
+            }
+        } else if (!w.sums) {
+            for (int q = 1; q <= w.it.piece; ++q) {
+                // entering piece q: from the state entering piece q - 1 and that piece's sum
+                const float keep = q == 1 ? 0.f
+                    : exp2f(w.lg * tokens_of(w.p->first + (q - 2) * w.p->rest, w.p->first + (q - 1) * w.p->rest, w.it.len, r.rev));
+                const float* from = slot(q);
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    const float u = __ldcg(from + i * DC);
+                    X[i] = q == 1 ? u : fmaf(keep, X[i], u);
+                }
+            }
+        }
+    }
+    auto put_x = [&]() {   // the state as the next chunk's outputs read it
+        if (mine) {
+            const uint32_t to = w.base + kX + half * (DC * 128);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                sts4(to + sw128(c, k), pack_bf16(X[8 * k], X[8 * k + 1]), pack_bf16(X[8 * k + 2], X[8 * k + 3]),
+                     pack_bf16(X[8 * k + 4], X[8 * k + 5]), pack_bf16(X[8 * k + 6], X[8 * k + 7]));
+        }
+        fence_proxy_async();
+        mbar_arrive(w.bar(B_X));
+    };
+    if (!w.sums && w.chunks > 0) put_x();
+    // this thread's channel in a row of a tile: rows 0 .. 7 of an 8-row group
+    uint32_t off[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) off[i] = (c >> 6) * kHalf + i * 128 + ((((c & 63) >> 3) ^ i) << 4) + (c & 7) * 2;
+    bool zeroed = false;
+    for (int m = 0; m < w.chunks; ++m) {
+        const int L = w.length(m);
+        const uint32_t B = w.base + (m & 1) * kStage + kTileBytes, C = B + kTileBytes;
+        if (!w.wait(B_FULL0 + (m & 1), m >> 1)) return;
+        if (L < kChunk && !zeroed) {
+            zeroed = true;
+            const int t = 128 * half + chan;   // two threads a row, one a tile
+            const int row = t >> 1;
+            if (row >= L) {
+                const uint32_t tile = t & 1 ? C : B;
+                const int halves = t & 1 ? DC / 64 : DA / 64;
+                for (int f = 0; f < halves; ++f)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) sts4(tile + f * kHalf + row * 128 + 16 * k, 0, 0, 0, 0);
+            }
+            fence_proxy_async();
+            mbar_arrive(w.bar(B_ZERO));
+        }
+        // Cw: hi + lo of 64 tokens' values, packed by token pairs
+        const uint32_t from = C + half * 8192;
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {   // 16 tokens
+            float x[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = lds_bf16(from + g * 2048 + (j >> 3) * 1024 + off[j & 7]);
+            const int j0 = 64 * half + 16 * g;
+            if (L == kChunk) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 k4 = lds4(key + 4 * (j0 + j));
+                    x[j] *= k4.x, x[j + 1] *= k4.y, x[j + 2] *= k4.z, x[j + 3] *= k4.w;
+                }
+            } else {
+                const int shift = r.rev ? 0 : kChunk - L;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = j0 + j < L ? x[j] * lds(key + 4 * (j0 + j + shift)) : 0.f;
+            }
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                hi[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                const float a = x[2 * j] - __uint_as_float(hi[j] << 16);
+                const float b = x[2 * j + 1] - __uint_as_float(hi[j] & 0xffff0000u);
+                lo[j] = pack_bf16(a, b);
+            }
+            tmem_st8(lanes + kTmHi + j0 / 2, hi);
+            tmem_st8(lanes + kTmLo + j0 / 2, lo);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(w.bar(B_VD));
+        if (!w.wait(B_U, m)) return;
+        tc_fence_after();
+        const float keep = exp2f(w.lg * L);
+        if (64 * half < DA) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float u[32];
+                tmem_ld32(lanes + kTmU + 64 * half + 32 * b, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) X[32 * b + i] = fmaf(keep, X[32 * b + i], u[i]);
+            }
+        }
+        if (!w.sums && m + 1 < w.chunks) {
+            tc_fence_before();
+            put_x();
+        }
+    }
+    // where the state goes: behind the last piece to the caller, behind the others' first phase to the next piece's slot
+    if (!mine) return;
+    if (w.it.piece == w.it.pieces - 1) {
+        if (r.last) {
+            float* to = given(r.last);
+            const int step = r.state_t ? 1 : DC;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) to[i * step] = X[i];
+        }
+    } else if (w.p->phase == 1) {
+        float* to = slot(w.it.piece + 1);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) to[i * DC] = X[i];
+    }
+}
+
+template <int DA, int DC>
+__device__ __forceinline__ void walk(const Work& w, const TcParams& q, int role, int warp, int lane) {
+    if (warp < 4) {
+        if (!w.sums) out_warps<DA, DC>(w, warp, lane);
+    } else if (warp < kLoadWarp) {
+        state_warps<DA, DC>(w, warp - 4, lane);
+    } else if (lane == 0) {
+        if (warp == kLoadWarp)
+            load_warp<DA, DC>(w, &q.a[role], &q.b[role], &q.c[role]);
+        else
+            mma_warp<DA, DC>(w);
+    }
+}
+
+template <int K, int V>
+__global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ TcParams q) {
+    extern __shared__ uint8_t smem_raw[];
+    const Params& p = q.p;
+    const int role = blockIdx.y;
+    if (p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
+    Work w;
+    w.p = &p;
+    w.r = &p.role[role];
+    w.h = blockIdx.x % p.H;
+    if (!item_of(p, blockIdx.x / p.H, w.it)) return;
+    w.sums = p.phase == 1 && w.it.piece > 0;
+    w.chunks = w.it.m1 - w.it.m0;
+    w.n = (w.it.len + kChunk - 1) / kChunk;
+    w.lg = log2_weight(p.decay, w.h);
+    w.base = (smem_u32(smem_raw) + 1023) & ~1023u;
+    uint8_t* sm = smem_raw + (w.base - smem_u32(smem_raw));
+    w.abort_flag = reinterpret_cast<volatile int*>(sm + kBar + 8 * B_N);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBar + 8 * B_N + 8);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < B_N; ++i)
+            mbar_init(w.bar(i), i == B_P || i == B_OSCALED || i == B_OFREE ? 128 : i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
+        *w.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    float* tab = reinterpret_cast<float*>(sm + kTab);
+    float* key = reinterpret_cast<float*>(sm + kKey);
+    if (tid <= 128) tab[tid] = exp2f(w.lg * tid);
+    // the update's weights: forward w^(127 - j), read from place 128 - L on in a shorter chunk; backward w^(j + 1)
+    if (tid < 256) key[tid] = tid < 128 ? exp2f(w.lg * (w.r->rev ? tid + 1 : 127 - tid)) : 0.f;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    w.tmem = *tmem_slot;
+    if (K == V || !w.r->state_t)
+        walk<K, V>(w, q, role, warp, lane);
+    else
+        walk<V, K>(w, q, role, warp, lane);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(w.tmem), "r"(512u) : "memory");
+}
+
+// [tokens, heads, D] bf16; box = 64 features x 1 head x 128 tokens
+bool tile_map(CUtensorMap* m, const void* ptr, int D, int heads, long long tokens) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
+    cuuint32_t box[3] = {64, 1, kChunk};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int K, int V>
+cudaError_t launch(const TcParams& q, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(tc_kernel<K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((long long)q.p.entries * q.p.H), (unsigned)q.p.nroles);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = q.p.dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, tc_kernel<K, V>, q);
+}
+
+}  // namespace
+
+bool tc_supported(const Params& p) {
+    if (p.T == 0 || !encode_fn()) return false;
+    for (int i = 0; i < p.nroles; ++i)
+        if (!p.role[i].a_bf16 || !p.role[i].b_bf16 || !p.role[i].c_bf16) return false;
+    return p.nroles == kMaxRoles || p.role[0].out_bf16;   // (gradients of shared heads leave as fp32, to be summed)
+}
+
+cudaError_t launch_tc(const Params& p, cudaStream_t s) {
+    TcParams q;
+    memset(&q, 0, sizeof q);
+    q.p = p;
+    const long long tokens = p.cu ? p.T : (long long)p.nseq * p.T;
+    for (int i = 0; i < p.nroles; ++i) {
+        const Role& r = p.role[i];
+        if (!tile_map(&q.a[i], r.a, r.dA, r.a_heads, tokens) || !tile_map(&q.b[i], r.b, r.dA, r.b_heads, tokens) ||
+            !tile_map(&q.c[i], r.c, r.dC, r.c_heads, tokens))
+            return cudaErrorInvalidValue;
+    }
+    // (K, V: of the roles whose state is stored as it is)
+    const bool t = p.role[0].state_t;
+    const int K = t ? p.role[0].dC : p.role[0].dA, V = t ? p.role[0].dA : p.role[0].dC;
+    if (K == 64) return V == 64 ? launch<64, 64>(q, s) : launch<64, 128>(q, s);
+    return V == 64 ? launch<128, 64>(q, s) : launch<128, 128>(q, s);
+}
+
+}  // namespace linear
+}  // namespace gdn
