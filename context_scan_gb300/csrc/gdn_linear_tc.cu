@@ -31,8 +31,10 @@ namespace gdn {
 namespace linear {
 namespace {
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 512;   // (four warpgroups; warps 14 and 15 have no work)
 constexpr int kStateThreads = 256;
+constexpr int kRegsOut = 120, kRegsState = 152, kRegsRest = 88;
+static_assert(128 * kRegsOut + 256 * kRegsState + 128 * kRegsRest == 128 * kThreads, "the registers of the launch");
 constexpr int kLoadWarp = 12, kMmaWarp = 13;
 constexpr long long kWaitLimit = 4000000000LL;   // SM cycles, some two seconds
 
@@ -51,12 +53,12 @@ static_assert(kTab % 16 == 0 && kKey % 16 == 0 && kBar % 16 == 0, "alignment");
 constexpr uint32_t kTmS = 0, kTmU = 128, kTmHi = 256, kTmLo = 320, kTmO = 384;
 
 // mbarriers, 8 bytes each from kBar on
-enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_DRAIN, B_N };
+enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_AFULL0, B_AFULL1, B_AFREE0, B_AFREE1, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_DRAIN, B_N };
 constexpr unsigned kTag = 0x60;   // + the barrier's number
 
 struct TcParams {
     Params p;
-    CUtensorMap a[kMaxRoles], b[kMaxRoles], c[kMaxRoles];
+    CUtensorMap a[kMaxRoles], b[kMaxRoles], c[kMaxRoles], out[kMaxRoles];
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -84,6 +86,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
         : "memory");
 }
 
+// a box from shared memory to global, in the thread's open group; its commit; the wait until the groups' boxes have been read
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t from, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(from), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 __device__ __forceinline__ float lds(uint32_t at) {
     float x;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
@@ -104,6 +116,29 @@ __device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+// The bounded wait of gdn_tc_common.cuh with its loop in place: a call would put the caller's registers on the stack, and
+// with all of the SM's memory shared, the stack is in L2.
+__device__ __forceinline__ bool wait_in_place(uint32_t bar, uint32_t parity, volatile int* abort_flag, DeviceError* err, unsigned tag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait_suspend(bar, parity, 20000u)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitLimit) {
+            record_error(err, GDN_ERR_TIMEOUT, tag);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// while shutting down after a wait that ran out: lets what the CTA issued retire
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, long long limit) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > limit) return;
+}
+
 // What every warp of the CTA knows of its work.
 struct Work {
     const Params* p;
@@ -119,11 +154,10 @@ struct Work {
     __device__ __forceinline__ uint32_t bar(int i) const { return base + kBar + 8 * i; }
     // the whole warp waits; every lane gets the same verdict
     __device__ __forceinline__ bool wait(int i, int parity) const {
-        const bool ok = mbar_wait(bar(i), parity & 1, abort_flag, kWaitLimit, p->err, kTag + i);
-        return __all_sync(0xffffffffu, ok);
+        return __all_sync(0xffffffffu, wait1(i, parity));
     }
     __device__ __forceinline__ bool wait1(int i, int parity) const {   // one lane
-        return mbar_wait(bar(i), parity & 1, abort_flag, kWaitLimit, p->err, kTag + i);
+        return wait_in_place(bar(i), parity & 1, abort_flag, p->err, kTag + i);
     }
 };
 
@@ -131,25 +165,30 @@ template <int DA, int DC>
 __device__ __forceinline__ void load_warp(const Work& w, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* mc) {
     const int rep = w.p->H;
     const int ah = w.h / (rep / w.r->a_heads), bh = w.h / (rep / w.r->b_heads), ch = w.h / (rep / w.r->c_heads);
-    const uint32_t bytes = (DA / 64) * kHalf * (w.sums ? 1 : 2) + (DC / 64) * kHalf;
-    int issued = 0;
+    int issued = 0, issued_a = 0;
     for (int m = 0; m < w.chunks; ++m) {
         const int s = m & 1;
         if (m >= 2 && !w.wait1(B_EMPTY0 + s, (m >> 1) - 1)) break;
-        const uint32_t to = w.base + s * kStage, full = w.bar(B_FULL0 + s);
+        const uint32_t to = w.base + s * kStage;
         const int row = w.it.lo + kChunk * w.phys(m);
-        mbar_arrive_expect_tx(full, bytes);
+        mbar_arrive_expect_tx(w.bar(B_FULL0 + s), (DA / 64 + DC / 64) * kHalf);
 #pragma unroll
-        for (int f = 0; f < DA / 64; ++f) {
-            if (!w.sums) tma_load_3d(to + f * kHalf, ma, full, 64 * f, ah, row);
-            tma_load_3d(to + kTileBytes + f * kHalf, mb, full, 64 * f, bh, row);
-        }
+        for (int f = 0; f < DC / 64; ++f) tma_load_3d(to + 2 * kTileBytes + f * kHalf, mc, w.bar(B_FULL0 + s), 64 * f, ch, row);
 #pragma unroll
-        for (int f = 0; f < DC / 64; ++f) tma_load_3d(to + 2 * kTileBytes + f * kHalf, mc, full, 64 * f, ch, row);
+        for (int f = 0; f < DA / 64; ++f) tma_load_3d(to + kTileBytes + f * kHalf, mb, w.bar(B_FULL0 + s), 64 * f, bh, row);
         issued = m + 1;
+        if (w.sums) continue;
+        // (A's tile holds the outputs of chunk m - 2 until they have left)
+        if (m >= 2 && !w.wait1(B_AFREE0 + s, (m >> 1) - 1)) break;
+        mbar_arrive_expect_tx(w.bar(B_AFULL0 + s), (DA / 64) * kHalf);
+#pragma unroll
+        for (int f = 0; f < DA / 64; ++f) tma_load_3d(to + f * kHalf, ma, w.bar(B_AFULL0 + s), 64 * f, ah, row);
+        issued_a = m + 1;
     }
-    if (*w.abort_flag)   // (what is in flight lands before shared memory is given back)
-        for (int m = max(0, issued - 2); m < issued; ++m) mbar_drain(w.bar(B_FULL0 + (m & 1)), (m >> 1) & 1, kWaitLimit);
+    if (*w.abort_flag) {   // (what is in flight lands before shared memory is given back)
+        for (int m = max(0, issued - 2); m < issued; ++m) drain(w.bar(B_FULL0 + (m & 1)), (m >> 1) & 1, kWaitLimit);
+        for (int m = max(0, issued_a - 2); m < issued_a; ++m) drain(w.bar(B_AFULL0 + (m & 1)), (m >> 1) & 1, kWaitLimit);
+    }
 }
 
 template <int DA, int DC>
@@ -158,7 +197,7 @@ __device__ __forceinline__ void mma_warp(const Work& w) {
                        ID_OP = idesc_bf16(128, DC, false, true), ID_U = idesc_bf16(128, DA, false, true);
     bool zero_seen = false;
     auto ready = [&](int m) {   // the chunk's tiles have landed, and end in zeros where they should
-        if (!w.wait1(B_FULL0 + (m & 1), m >> 1)) return false;
+        if (!w.wait1(B_FULL0 + (m & 1), m >> 1) || (!w.sums && !w.wait1(B_AFULL0 + (m & 1), m >> 1))) return false;
         if (w.length(m) < kChunk && !zero_seen) {
             if (!w.wait1(B_ZERO, 0)) return false;
             zero_seen = true;
@@ -221,13 +260,13 @@ __device__ __forceinline__ void mma_warp(const Work& w) {
     }
     if (m < w.chunks) {
         mma_commit(w.bar(B_DRAIN));
-        mbar_drain(w.bar(B_DRAIN), 0, kWaitLimit);
+        drain(w.bar(B_DRAIN), 0, kWaitLimit);
     }
 }
 
 // P, the scaling of O, the outputs: thread = row (token) of the chunk = lane of tensor memory
-template <int DA, int DC>
-__device__ __forceinline__ void out_warps(const Work& w, int warp, int lane) {
+template <int DA, int DC, bool OUT_BF16>
+__device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map, int warp, int lane) {
     const Role& r = *w.r;
     const int row = 32 * warp + lane;
     const uint32_t lanes = w.tmem + ((uint32_t)(32 * warp) << 16);
@@ -240,7 +279,7 @@ __device__ __forceinline__ void out_warps(const Work& w, int warp, int lane) {
                        : pack(lds(tab + 4 * (31 - 2 * c)), lds(tab + 4 * (30 - 2 * c)));
     for (int m = 0; m < w.chunks; ++m) {
         const int L = w.length(m);
-        if (!w.wait(B_S, m)) return;
+        if (!w.wait(B_S, m)) return store_wait();
         tc_fence_after();
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
@@ -277,7 +316,12 @@ __device__ __forceinline__ void out_warps(const Work& w, int warp, int lane) {
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(w.bar(B_P));
-        if (!w.wait(B_OI, m)) return;
+        if (m > 0) {   // the last chunk's outputs have left A's tile by now
+            store_wait();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(w.bar(B_AFREE0 + ((m - 1) & 1)));
+        }
+        if (!w.wait(B_OI, m)) return store_wait();
         tc_fence_after();
         const float keep = exp2f(w.lg * (r.rev ? max(L - 1 - row, 0) : row + 1));
 #pragma unroll 1
@@ -292,34 +336,56 @@ __device__ __forceinline__ void out_warps(const Work& w, int warp, int lane) {
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(w.bar(B_OSCALED));
-        if (!w.wait(B_O, m)) return;
+        if (!w.wait(B_O, m)) return store_wait();
         tc_fence_after();
-        const long long at = ((long long)(w.it.lo + kChunk * w.phys(m) + row) * w.p->H + w.h) * DC;
-#pragma unroll 1
-        for (int b = 0; b < DC / 32; ++b) {
-            float x[32];
-            tmem_ld32(lanes + kTmO + 32 * b, x);
-            tmem_wait_ld();
-            if (b == DC / 32 - 1) {
-                tc_fence_before();
-                mbar_arrive(w.bar(B_OFREE));
+        // out through A's tile, which is done with: each warp its own 8 KB of it, boxes of 32 rows of 128 bytes
+        const uint32_t mine = w.base + (m & 1) * kStage + warp * 8192;
+        const int row0 = w.it.lo + kChunk * w.phys(m) + 32 * warp, rows = min(32, L - 32 * warp);
+        constexpr int kPer = OUT_BF16 ? 64 : 32, kBoxes = DC / kPer;   // features of a box
+#pragma unroll
+        for (int b = 0; b < kBoxes; ++b) {
+            if (b == 2) {   // (fp32: the first two boxes have to leave before the next two)
+                store_wait();
+                __syncwarp();
             }
-            if (row < L) {
-                if (r.out_bf16) {
-                    uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(r.out) + at + 32 * b);
+            const uint32_t box = mine + (b & 1) * 4096;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        to[c] = make_uint4(pack_bf16(x[8 * c], x[8 * c + 1]), pack_bf16(x[8 * c + 2], x[8 * c + 3]),
-                                           pack_bf16(x[8 * c + 4], x[8 * c + 5]), pack_bf16(x[8 * c + 6], x[8 * c + 7]));
+            for (int x = 0; x < kPer / 32; ++x) {
+                float f[32];
+                tmem_ld32(lanes + kTmO + kPer * b + 32 * x, f);
+                tmem_wait_ld();
+                if (b == kBoxes - 1 && x == kPer / 32 - 1) {
+                    tc_fence_before();
+                    mbar_arrive(w.bar(B_OFREE));
+                }
+                if constexpr (OUT_BF16) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sts4(box + sw128(lane, 4 * x + k), pack_bf16(f[8 * k], f[8 * k + 1]), pack_bf16(f[8 * k + 2], f[8 * k + 3]),
+                             pack_bf16(f[8 * k + 4], f[8 * k + 5]), pack_bf16(f[8 * k + 6], f[8 * k + 7]));
                 } else {
-                    float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(r.out) + at + 32 * b);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) to[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+                    for (int k = 0; k < 8; ++k)
+                        sts4(box + sw128(lane, k), __float_as_uint(f[4 * k]), __float_as_uint(f[4 * k + 1]),
+                             __float_as_uint(f[4 * k + 2]), __float_as_uint(f[4 * k + 3]));
                 }
             }
+            fence_proxy_async();
             __syncwarp();
+            if (rows == 32) {
+                if (lane == 0) tma_store_3d(map, box, kPer * b, w.h, row0);
+            } else {   // the sequence ends here: row by row, eight lanes each
+                constexpr int kSize = OUT_BF16 ? 2 : 4;
+                for (int i = lane >> 3; i < rows; i += 4) {
+                    const float4 x = lds4(box + sw128(i, lane & 7));
+                    char* to = (char*)r.out + (((long long)(row0 + i) * w.p->H + w.h) * DC + kPer * b) * kSize + 16 * (lane & 7);
+                    *reinterpret_cast<float4*>(to) = x;
+                }
+                __syncwarp();
+            }
         }
     }
+    store_wait();
 }
 
 // Cw and the state: thread = channel of C = lane of tensor memory; the two halves of the warps take 64 tokens of Cw and 64
@@ -467,20 +533,6 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
     }
 }
 
-template <int DA, int DC>
-__device__ __forceinline__ void walk(const Work& w, const TcParams& q, int role, int warp, int lane) {
-    if (warp < 4) {
-        if (!w.sums) out_warps<DA, DC>(w, warp, lane);
-    } else if (warp < kLoadWarp) {
-        state_warps<DA, DC>(w, warp - 4, lane);
-    } else if (lane == 0) {
-        if (warp == kLoadWarp)
-            load_warp<DA, DC>(w, &q.a[role], &q.b[role], &q.c[role]);
-        else
-            mma_warp<DA, DC>(w);
-    }
-}
-
 template <int K, int V>
 __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ TcParams q) {
     extern __shared__ uint8_t smem_raw[];
@@ -503,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < B_N; ++i)
-            mbar_init(w.bar(i), i == B_P || i == B_OSCALED || i == B_OFREE ? 128 : i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
+            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? 4 : i == B_P || i == B_OSCALED || i == B_OFREE ? 128 : i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
         *w.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
@@ -522,10 +574,28 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     __syncthreads();
     tc_fence_after();
     w.tmem = *tmem_slot;
-    if (K == V || !w.r->state_t)
-        walk<K, V>(w, q, role, warp, lane);
-    else
-        walk<V, K>(w, q, role, warp, lane);
+    const bool turned = K != V && w.r->state_t;   // dA = V, dC = K
+    // The launch's 128 registers a thread, dealt anew: 128 x 120 + 256 x 152 + 128 x 88 = 512 x 128. (At 128 the
+    // state's warps spill, and the stack is in L2.)
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+        const bool bf16 = w.r->out_bf16;
+        const CUtensorMap* map = &q.out[role];
+        if (w.sums) {
+        } else if (turned) {
+            bf16 ? out_warps<V, K, true>(w, map, warp, lane) : out_warps<V, K, false>(w, map, warp, lane);
+        } else {
+            bf16 ? out_warps<K, V, true>(w, map, warp, lane) : out_warps<K, V, false>(w, map, warp, lane);
+        }
+    } else if (warp < kLoadWarp) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
+        turned ? state_warps<V, K>(w, warp - 4, lane) : state_warps<K, V>(w, warp - 4, lane);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (lane == 0 && warp == kLoadWarp)
+            turned ? load_warp<V, K>(w, &q.a[role], &q.b[role], &q.c[role]) : load_warp<K, V>(w, &q.a[role], &q.b[role], &q.c[role]);
+        if (lane == 0 && warp == kMmaWarp) turned ? mma_warp<V, K>(w) : mma_warp<K, V>(w);
+    }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -534,16 +604,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(w.tmem), "r"(512u) : "memory");
 }
 
-// [tokens, heads, D] bf16; box = 64 features x 1 head x 128 tokens
-bool tile_map(CUtensorMap* m, const void* ptr, int D, int heads, long long tokens) {
+// [tokens, heads, D]; box = 128 bytes of features x 1 head x `rows` tokens
+bool tile_map(CUtensorMap* m, const void* ptr, bool bf16, int D, int heads, long long tokens, int rows) {
     auto fn = encode_fn();
     if (!fn) return false;
+    const cuuint64_t size = bf16 ? 2 : 4;
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
-    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
-    cuuint32_t box[3] = {64, 1, kChunk};
+    cuuint64_t strides[2] = {(cuuint64_t)D * size, (cuuint64_t)heads * D * size};
+    cuuint32_t box[3] = {(cuuint32_t)(128 / size), 1, (cuuint32_t)rows};
     cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(ptr), dims,
+              strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -580,8 +651,9 @@ cudaError_t launch_tc(const Params& p, cudaStream_t s) {
     const long long tokens = p.cu ? p.T : (long long)p.nseq * p.T;
     for (int i = 0; i < p.nroles; ++i) {
         const Role& r = p.role[i];
-        if (!tile_map(&q.a[i], r.a, r.dA, r.a_heads, tokens) || !tile_map(&q.b[i], r.b, r.dA, r.b_heads, tokens) ||
-            !tile_map(&q.c[i], r.c, r.dC, r.c_heads, tokens))
+        if (!tile_map(&q.a[i], r.a, true, r.dA, r.a_heads, tokens, kChunk) || !tile_map(&q.b[i], r.b, true, r.dA, r.b_heads, tokens, kChunk) ||
+            !tile_map(&q.c[i], r.c, true, r.dC, r.c_heads, tokens, kChunk) ||
+            !tile_map(&q.out[i], r.out, r.out_bf16, r.dC, p.H, tokens, 32))
             return cudaErrorInvalidValue;
     }
     // (K, V: of the roles whose state is stored as it is)
