@@ -16,12 +16,13 @@
 // memory (two stages of A, B, C: 192 KB, and 32 KB of X), which would not hold scaled copies as well.
 //
 // Warps: 0-3 P, the scaling of O, the outputs; 4-11 the state: Cw (each half of them 64 tokens) and X (each half 64 rows);
-// 12 loads (TMA, 128-byte swizzle), 13 issues the MMAs. Every wait on an mbarrier is bounded: on expiry the kernel records
+// 12 loads (TMA, 128-byte swizzle), 13 issues the MMAs, 14 stores bf16 outputs (TMA). Every wait on an mbarrier is bounded: on expiry the kernel records
 // GDN_ERR_TIMEOUT, lets what it issued retire, frees tensor memory and returns.
 //
 // A sequence's last chunk may hold fewer than 128 tokens: the rows of B and C behind it (the next sequence's) are
 // overwritten by zeros in shared memory, so that nothing of another sequence enters a sum, not as 0 times NaN either.
 #include <cstring>
+#include <type_traits>
 
 #include "gdn_linear.cuh"
 #include "gdn_pair.cuh"
@@ -31,11 +32,11 @@ namespace gdn {
 namespace linear {
 namespace {
 
-constexpr int kThreads = 512;   // (four warpgroups; warps 14 and 15 have no work)
+constexpr int kThreads = 512;   // (four warpgroups; warp 15 has no work)
 constexpr int kStateThreads = 256;
 constexpr int kRegsOut = 120, kRegsState = 152, kRegsRest = 88;
 static_assert(128 * kRegsOut + 256 * kRegsState + 128 * kRegsRest == 128 * kThreads, "the registers of the launch");
-constexpr int kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kLoadWarp = 12, kMmaWarp = 13, kStoreWarp = 14;
 constexpr long long kWaitLimit = 4000000000LL;   // SM cycles, some two seconds
 
 constexpr uint32_t kHalf = 16384;                // 128 tokens x 64 features
@@ -53,7 +54,7 @@ static_assert(kTab % 16 == 0 && kKey % 16 == 0 && kBar % 16 == 0, "alignment");
 constexpr uint32_t kTmS = 0, kTmU = 128, kTmHi = 256, kTmLo = 320, kTmO = 384;
 
 // mbarriers, 8 bytes each from kBar on
-enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_AFULL0, B_AFULL1, B_AFREE0, B_AFREE1, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_DRAIN, B_N };
+enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_AFULL0, B_AFULL1, B_AFREE0, B_AFREE1, B_OUT, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_DRAIN, B_N };
 constexpr unsigned kTag = 0x60;   // + the barrier's number
 
 struct TcParams {
@@ -86,6 +87,35 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
         : "memory");
 }
 
+// one MMA by the lane with `first`; and the arrival of the barrier once that lane's MMAs have retired
+template <uint32_t ID>
+__device__ __forceinline__ void mma_one_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate, uint32_t first) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "n"(ID), "r"(accumulate), "r"(first)
+        : "memory");
+}
+template <uint32_t ID>
+__device__ __forceinline__ void mma_one_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate, uint32_t first) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(b), "n"(ID), "r"(accumulate), "r"(first)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar, uint32_t first) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(first)
+        : "memory");
+}
+
 // a box from shared memory to global, in the thread's open group; its commit; the wait until the groups' boxes have been read
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t from, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -96,6 +126,19 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t fr
 }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
+__device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t (&v)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+}
+// 16 lanes x 32 columns: register 2 g + h holds lane 8 h + T / 4, column 4 g + T % 4
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
 __device__ __forceinline__ float lds(uint32_t at) {
     float x;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
@@ -105,12 +148,6 @@ __device__ __forceinline__ float4 lds4(uint32_t at) {
     float4 x;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at));
     return x;
-}
-// a bf16 value as fp32
-__device__ __forceinline__ float lds_bf16(uint32_t at) {
-    unsigned short x;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at));
-    return __uint_as_float((unsigned)x << 16);
 }
 __device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -192,26 +229,38 @@ __device__ __forceinline__ void load_warp(const Work& w, const CUtensorMap* ma, 
 }
 
 template <int DA, int DC>
-__device__ __forceinline__ void mma_warp(const Work& w) {
+__device__ __forceinline__ void mma_warp(const Work& w, int lane) {
     constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_OI = idesc_bf16(128, DC, false, false),
                        ID_OP = idesc_bf16(128, DC, false, true), ID_U = idesc_bf16(128, DA, false, true);
     bool zero_seen = false;
     auto ready = [&](int m) {   // the chunk's tiles have landed, and end in zeros where they should
-        if (!w.wait1(B_FULL0 + (m & 1), m >> 1) || (!w.sums && !w.wait1(B_AFULL0 + (m & 1), m >> 1))) return false;
+        if (!w.wait(B_FULL0 + (m & 1), m >> 1) || (!w.sums && !w.wait(B_AFULL0 + (m & 1), m >> 1))) return false;
         if (w.length(m) < kChunk && !zero_seen) {
-            if (!w.wait1(B_ZERO, 0)) return false;
+            if (!w.wait(B_ZERO, 0)) return false;
             zero_seen = true;
         }
         return true;
     };
-    auto s_mma = [&](int m) {
-        const uint32_t A = w.base + (m & 1) * kStage, B = A + kTileBytes;
+    // The whole warp walks through this, with values that are the same in every lane, and the first lane issues: descriptors
+    // then stay in uniform registers (under a branch on the lane each MMA took some 140 cycles to issue). The start
+    // addresses of operands whose rows hold the contraction (K-major) advance by 32 bytes a step within a half, the others
+    // by 16 rows of 128 bytes; in descriptors, in units of 16 bytes.
+    const uint32_t first = lane == 0;
+    auto by_rows = [&](auto id, uint32_t d, uint32_t a, uint32_t b, uint32_t b_half) {
 #pragma unroll
-        for (int k = 0; k < DA / 16; ++k) {
-            const uint32_t at = (k / 4) * kHalf + (k % 4) * 32;
-            mma_ss<ID_S>(w.tmem + kTmS, desc_k(A + at), desc_k(B + at), k > 0);
-        }
-        mma_commit(w.bar(B_S));
+        for (int k = 0; k < DA / 16; ++k)
+            mma_one_ss<decltype(id)::value>(d, desc_k(a + (k / 4) * kHalf) + 2 * (k % 4), desc_k(b + (k / 4) * b_half) + 2 * (k % 4), k > 0, first);
+    };
+    auto by_tokens = [&](auto id, uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
+        const uint64_t db = desc_mn(b, kHalf);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_one_ts<decltype(id)::value>(d, a + 8 * k, db + 128 * k, k ? 1u : accumulate, first);
+    };
+    auto commit = [&](int i) { commit_one(w.bar(i), first); };
+    auto s_mma = [&](int m) {
+        const uint32_t A = w.base + (m & 1) * kStage;
+        by_rows(std::integral_constant<uint32_t, ID_S>(), w.tmem + kTmS, A, A + kTileBytes, kHalf);
+        commit(B_S);
     };
     int m = 0;
     for (; m < w.chunks; ++m) {
@@ -224,42 +273,34 @@ __device__ __forceinline__ void mma_warp(const Work& w) {
                 tc_fence_after();
                 s_mma(0);
             }
-            if (!w.wait1(B_X, m) || (m > 0 && !w.wait1(B_OFREE, m - 1))) break;
+            if (!w.wait(B_X, m) || (m > 0 && !w.wait(B_OFREE, m - 1))) break;
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < DA / 16; ++k)
-                mma_ss<ID_OI>(w.tmem + kTmO, desc_k(A + (k / 4) * kHalf + (k % 4) * 32),
-                              desc_k(w.base + kX + (k / 4) * (DC * 128) + (k % 4) * 32), k > 0);
-            mma_commit(w.bar(B_OI));
+            by_rows(std::integral_constant<uint32_t, ID_OI>(), w.tmem + kTmO, A, w.base + kX, DC * 128);
+            commit(B_OI);
         }
-        if (!w.wait1(B_VD, m)) break;
+        if (!w.wait(B_VD, m)) break;
         tc_fence_after();
 #pragma unroll
         for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                mma_ts_bf16<ID_U>(w.tmem + kTmU, w.tmem + (part ? kTmLo : kTmHi) + 8 * k, desc_mn(B + 2048 * k, kHalf),
-                                  part + k > 0);
-        mma_commit(w.bar(B_U));
+            by_tokens(std::integral_constant<uint32_t, ID_U>(), w.tmem + kTmU, w.tmem + kTmHi + (kTmLo - kTmHi) * part, B, part);
+        commit(B_U);
         if (w.sums) {
-            mma_commit(w.bar(B_EMPTY0 + (m & 1)));
+            commit(B_EMPTY0 + (m & 1));
             continue;
         }
-        if (!w.wait1(B_P, m) || !w.wait1(B_OSCALED, m)) break;
+        if (!w.wait(B_P, m) || !w.wait(B_OSCALED, m)) break;
         tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            mma_ts_bf16<ID_OP>(w.tmem + kTmO, w.tmem + kTmS + 8 * k, desc_mn(C + 2048 * k, kHalf), 1u);
-        mma_commit(w.bar(B_O));
-        mma_commit(w.bar(B_EMPTY0 + (m & 1)));
+        by_tokens(std::integral_constant<uint32_t, ID_OP>(), w.tmem + kTmO, w.tmem + kTmS, C, 1);
+        commit(B_O);
+        commit(B_EMPTY0 + (m & 1));
         if (m + 1 < w.chunks) {
-            if (!ready(m + 1) || !w.wait1(B_O, m)) break;
+            if (!ready(m + 1) || !w.wait(B_O, m)) break;
             tc_fence_after();
             s_mma(m + 1);
         }
     }
     if (m < w.chunks) {
-        mma_commit(w.bar(B_DRAIN));
+        commit(B_DRAIN);
         drain(w.bar(B_DRAIN), 0, kWaitLimit);
     }
 }
@@ -271,12 +312,15 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
     const int row = 32 * warp + lane;
     const uint32_t lanes = w.tmem + ((uint32_t)(32 * warp) << 16);
     const uint32_t tab = w.base + kTab;
-    // w^(31 - c) (or, backward in time, w^c) for the 32 columns of a block: what is left of a gap to another block's column
-    pair_t col[16];
+    // The weight of row i and column j is w^|i - j|. Columns in blocks of 32: w^(31 - c) (or, backward in time, w^c) for the column
+    // of a block, times what is left of the gap, one value a row and block. In the diagonal block that is w^(lane - 31) (or
+    // w^-lane), which fp32 holds unless the head decays by some 17 e-folds or more in a block; `steep` ones look every
+    // weight up.
+    float col[32];
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-        col[c] = r.rev ? pack(lds(tab + 4 * (2 * c)), lds(tab + 4 * (2 * c + 1)))
-                       : pack(lds(tab + 4 * (31 - 2 * c)), lds(tab + 4 * (30 - 2 * c)));
+    for (int c = 0; c < 32; ++c) col[c] = lds(tab + 4 * (r.rev ? c : 31 - c));
+    const bool steep = !(w.lg * 31.f > -80.f);
+    const float diag = exp2f(w.lg * (r.rev ? -lane : lane - 31));
     for (int m = 0; m < w.chunks; ++m) {
         const int L = w.length(m);
         if (!w.wait(B_S, m)) return store_wait();
@@ -291,24 +335,22 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
             } else {
                 float x[32];
                 tmem_ld32(lanes + kTmS + 32 * b, x);
+                const float f = away ? lds(tab + 4 * (r.rev ? 32 * away - lane : 32 * away + lane - 31)) : diag;
                 tmem_wait_ld();
-                if (away == 0) {
+                if (away == 0 && steep) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const int gap = r.rev ? c - lane : lane - c;
-                        x[c] = gap >= 0 ? x[c] * lds(tab + 4 * max(gap, 0)) : 0.f;
-                    }
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) q[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
+                    for (int c = 0; c < 32; ++c) x[c] *= lds(tab + 4 * abs(lane - c));
                 } else {
-                    const float f = lds(tab + 4 * (r.rev ? 32 * away - lane : 32 * away + lane - 31));
-                    const pair_t f2 = pack(f, f);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        float lo, hi;
-                        unpack(mul2(pack(x[2 * c], x[2 * c + 1]), mul2(f2, col[c])), lo, hi);
-                        q[c] = pack_bf16(lo, hi);
-                    }
+                    for (int c = 0; c < 32; ++c) x[c] *= f * col[c];
+                }
+#pragma unroll
+                for (int c = 0; c < 16; ++c) q[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
+                if (away == 0) {   // the columns behind the row (by time)
+                    const uint32_t seen = r.rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        q[c] &= (seen >> (2 * c) & 1 ? 0xffffu : 0u) | (seen >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
                 }
             }
             tmem_st16(lanes + kTmS + 16 * b, q);
@@ -316,11 +358,6 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(w.bar(B_P));
-        if (m > 0) {   // the last chunk's outputs have left A's tile by now
-            store_wait();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(w.bar(B_AFREE0 + ((m - 1) & 1)));
-        }
         if (!w.wait(B_OI, m)) return store_wait();
         tc_fence_after();
         const float keep = exp2f(w.lg * (r.rev ? max(L - 1 - row, 0) : row + 1));
@@ -373,7 +410,7 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
             fence_proxy_async();
             __syncwarp();
             if (rows == 32) {
-                if (lane == 0) tma_store_3d(map, box, kPer * b, w.h, row0);
+                if (!OUT_BF16 && lane == 0) tma_store_3d(map, box, kPer * b, w.h, row0);
             } else {   // the sequence ends here: row by row, eight lanes each
                 constexpr int kSize = OUT_BF16 ? 2 : 4;
                 for (int i = lane >> 3; i < rows; i += 4) {
@@ -384,6 +421,30 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
                 __syncwarp();
             }
         }
+        if constexpr (OUT_BF16) {
+            mbar_arrive(w.bar(B_OUT));   // (to store_warp)
+        } else {
+            store_wait();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(w.bar(B_AFREE0 + (m & 1)));
+        }
+    }
+    store_wait();
+}
+
+// Sends the bf16 outputs from A's tile and gives it back to the loads: lane i for the rows of warp i.
+template <int DC>
+__device__ __forceinline__ void store_warp(const Work& w, const CUtensorMap* map, int lane) {
+    for (int m = 0; m < w.chunks; ++m) {
+        if (!w.wait1(B_OUT, m)) break;
+        if (w.length(m) >= 32 * lane + 32) {   // (the last rows of a sequence have gone by other ways)
+            const uint32_t from = w.base + (m & 1) * kStage + lane * 8192;
+            const int row0 = w.it.lo + kChunk * w.phys(m) + 32 * lane;
+#pragma unroll
+            for (int b = 0; b < DC / 64; ++b) tma_store_3d(map, from + 4096 * b, 64 * b, w.h, row0);
+            store_wait();
+        }
+        mbar_arrive(w.bar(B_AFREE0 + (m & 1)));
     }
     store_wait();
 }
@@ -443,10 +504,16 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
         mbar_arrive(w.bar(B_X));
     };
     if (!w.sums && w.chunks > 0) put_x();
-    // this thread's channel in a row of a tile: rows 0 .. 7 of an 8-row group
-    uint32_t off[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) off[i] = (c >> 6) * kHalf + i * 128 + ((((c & 63) >> 3) ^ i) << 4) + (c & 7) * 2;
+    // Cw's fragments: an 8 x 8 matrix of tokens x channels, loaded with transposition, leaves a lane channel lane / 4 of
+    // tokens 2 (lane % 4) and the next one; two of them (channels 0 .. 7 and 8 .. 15) are what a 16 x 128-bit store to
+    // tensor memory takes for 16 channels (its lanes) and four token pairs (its columns). A lane's row address:
+    const int chan0 = (32 * quarter) & (DC - 1);
+    // (lanes 0 .. 15: tokens of group g, 16 .. 31: of group g + 1; 16 channels further on, bit 5 of the address flips)
+    const uint32_t ldm = (chan0 >> 6) * kHalf + half * 8192 + (lane >> 4) * 1024 + (lane & 7) * 128 +
+                         (((((chan0 & 63) >> 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+    const int tok = 64 * half + 2 * (lane & 3);   // of its pairs in 8-token group 0
+    float2 weight[8];
+    int weight_len = 0;
     bool zeroed = false;
     for (int m = 0; m < w.chunks; ++m) {
         const int L = w.length(m);
@@ -465,36 +532,39 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
             }
             fence_proxy_async();
             mbar_arrive(w.bar(B_ZERO));
+            if (!w.wait(B_ZERO, 0)) return;
         }
-        // Cw: hi + lo of 64 tokens' values, packed by token pairs
-        const uint32_t from = C + half * 8192;
+        if (L != weight_len) {
+            weight_len = L;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const int j = tok + 8 * g, at = j + (r.rev ? 0 : kChunk - L);
+                weight[g] = make_float2(lds(key + 4 * at), lds(key + 4 * at + 4));
+            }
+        }
+        // Cw = hi + lo of 64 tokens' values of 32 channels, 16 channels at a time: hi is the value cut off to bf16 and lo the
+        // rest of it, rounded
+        uint32_t from = C + ldm;
 #pragma unroll 1
-        for (int g = 0; g < 4; ++g) {   // 16 tokens
-            float x[16];
+        for (int x = 0; x < 2; ++x, from ^= 32) {
+            uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = lds_bf16(from + g * 2048 + (j >> 3) * 1024 + off[j & 7]);
-            const int j0 = 64 * half + 16 * g;
-            if (L == kChunk) {
+            for (int g = 0; g < 8; g += 2) {
+                uint32_t v[4];   // two 8-token groups x 16 channels
+                ldmatrix_trans(from + g * 1024, v);
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 k4 = lds4(key + 4 * (j0 + j));
-                    x[j] *= k4.x, x[j + 1] *= k4.y, x[j + 2] *= k4.z, x[j + 3] *= k4.w;
+                for (int i = 0; i < 4; ++i) {   // (group g + i / 2, channels 8 (i % 2) ..)
+                    const float a = __uint_as_float(v[i] << 16) * weight[g + i / 2].x;
+                    const float b = __uint_as_float(v[i] & 0xffff0000u) * weight[g + i / 2].y;
+                    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+                    const int at = 2 * (g + i / 2) + (i & 1);
+                    hi[at] = __byte_perm(ua, ub, 0x7632);
+                    lo[at] = pack_bf16(a - __uint_as_float(ua & 0xffff0000u), b - __uint_as_float(ub & 0xffff0000u));
                 }
-            } else {
-                const int shift = r.rev ? 0 : kChunk - L;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = j0 + j < L ? x[j] * lds(key + 4 * (j0 + j + shift)) : 0.f;
             }
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                hi[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-                const float a = x[2 * j] - __uint_as_float(hi[j] << 16);
-                const float b = x[2 * j + 1] - __uint_as_float(hi[j] & 0xffff0000u);
-                lo[j] = pack_bf16(a, b);
-            }
-            tmem_st8(lanes + kTmHi + j0 / 2, hi);
-            tmem_st8(lanes + kTmLo + j0 / 2, lo);
+            const uint32_t to = lanes + ((uint32_t)(16 * x) << 16) + 32 * half;
+            tmem_st_16x128b_x8(to + kTmHi, hi);
+            tmem_st_16x128b_x8(to + kTmLo, lo);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -552,10 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     uint8_t* sm = smem_raw + (w.base - smem_u32(smem_raw));
     w.abort_flag = reinterpret_cast<volatile int*>(sm + kBar + 8 * B_N);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBar + 8 * B_N + 8);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < B_N; ++i)
-            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? 4 : i == B_P || i == B_OSCALED || i == B_OFREE ? 128 : i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
+            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? 4 : i == B_P || i == B_OUT || i == B_OSCALED || i == B_OFREE ? 128 : i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
         *w.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
@@ -573,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    w.tmem = *tmem_slot;
+    w.tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const bool turned = K != V && w.r->state_t;   // dA = V, dC = K
     // The launch's 128 registers a thread, dealt anew: 128 x 120 + 256 x 152 + 128 x 88 = 512 x 128. (At 128 the
     // state's warps spill, and the stack is in L2.)
@@ -594,7 +664,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
         if (lane == 0 && warp == kLoadWarp)
             turned ? load_warp<V, K>(w, &q.a[role], &q.b[role], &q.c[role]) : load_warp<K, V>(w, &q.a[role], &q.b[role], &q.c[role]);
-        if (lane == 0 && warp == kMmaWarp) turned ? mma_warp<V, K>(w) : mma_warp<K, V>(w);
+        if (lane < 4 && warp == kStoreWarp && !w.sums && w.r->out_bf16) {
+            const CUtensorMap* map = &q.out[role];
+            turned ? store_warp<K>(w, map, lane) : store_warp<V>(w, map, lane);
+        }
+        if (warp == kMmaWarp) turned ? mma_warp<V, K>(w, lane) : mma_warp<K, V>(w, lane);
     }
     __syncwarp();
     tc_fence_before();
