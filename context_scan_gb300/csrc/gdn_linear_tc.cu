@@ -16,7 +16,7 @@
 // memory (two stages of A, B, C: 192 KB, and 32 KB of X), which would not hold scaled copies as well.
 //
 // Warps: 0-3 P, the scaling of O, the outputs; 4-11 the state: Cw (each half of them 64 tokens) and X (each half 64 rows);
-// 12 loads (TMA, 128-byte swizzle), 13 issues the MMAs, 14 stores bf16 outputs (TMA). Every wait on an mbarrier is bounded: on expiry the kernel records
+// 12 loads (TMA, 128-byte swizzle), 13 and 15 issue the MMAs, 14 stores bf16 outputs (TMA). Every wait on an mbarrier is bounded: on expiry the kernel records
 // GDN_ERR_TIMEOUT, lets what it issued retire, frees tensor memory and returns.
 //
 // A sequence's last chunk may hold fewer than 128 tokens: the rows of B and C behind it (the next sequence's) are
@@ -32,12 +32,13 @@ namespace gdn {
 namespace linear {
 namespace {
 
-constexpr int kThreads = 512;   // (four warpgroups; warp 15 has no work)
+constexpr int kThreads = 512;   // (four warpgroups)
 constexpr int kStateThreads = 256;
 constexpr int kRegsOut = 120, kRegsState = 152, kRegsRest = 88;
 static_assert(128 * kRegsOut + 256 * kRegsState + 128 * kRegsRest == 128 * kThreads, "the registers of the launch");
-constexpr int kLoadWarp = 12, kMmaWarp = 13, kStoreWarp = 14;
-constexpr long long kWaitLimit = 4000000000LL;   // SM cycles, some two seconds
+constexpr int kLoadWarp = 12, kMmaWarp = 13, kStoreWarp = 14, kStateMmaWarp = 15;
+constexpr long long kWaitLimit = 4000000000LL;   // SM cycles, some two seconds (for the waits while shutting down)
+constexpr int kWaitTries = 1 << 20;              // of a wait: a second or so at least, 20 at most
 
 constexpr uint32_t kHalf = 16384;                // 128 tokens x 64 features
 constexpr uint32_t kTileBytes = 2 * kHalf;
@@ -54,7 +55,7 @@ static_assert(kTab % 16 == 0 && kKey % 16 == 0 && kBar % 16 == 0, "alignment");
 constexpr uint32_t kTmS = 0, kTmU = 128, kTmHi = 256, kTmLo = 320, kTmO = 384;
 
 // mbarriers, 8 bytes each from kBar on
-enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_AFULL0, B_AFULL1, B_AFREE0, B_AFREE1, B_OUT, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_DRAIN, B_N };
+enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_AFULL0, B_AFULL1, B_AFREE0, B_AFREE1, B_OUT, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_DRAIN0, B_DRAIN1, B_N };
 constexpr unsigned kTag = 0x60;   // + the barrier's number
 
 struct TcParams {
@@ -153,22 +154,6 @@ __device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// The bounded wait of gdn_tc_common.cuh with its loop in place: a call would put the caller's registers on the stack, and
-// with all of the SM's memory shared, the stack is in L2.
-__device__ __forceinline__ bool wait_in_place(uint32_t bar, uint32_t parity, volatile int* abort_flag, DeviceError* err, unsigned tag) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try_wait_suspend(bar, parity, 20000u)) {
-        if (*abort_flag) return false;
-        if (clock64() - t0 > kWaitLimit) {
-            record_error(err, GDN_ERR_TIMEOUT, tag);
-            *abort_flag = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
 // while shutting down after a wait that ran out: lets what the CTA issued retire
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, long long limit) {
     const long long t0 = clock64();
@@ -176,7 +161,9 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, long long l
         if (clock64() - t0 > limit) return;
 }
 
-// What every warp of the CTA knows of its work.
+// What every warp of the CTA knows of its work. Its waits are those of gdn_tc_common.cuh with the loop in place and
+// the limit counted in tries (each of at most 20 us): a call would put the caller's registers on the stack, which, with
+// all of the SM's memory shared, is in L2; and every warp walks through its waits once a chunk, so their code is short.
 struct Work {
     const Params* p;
     const Role* r;
@@ -191,10 +178,28 @@ struct Work {
     __device__ __forceinline__ uint32_t bar(int i) const { return base + kBar + 8 * i; }
     // the whole warp waits; every lane gets the same verdict
     __device__ __forceinline__ bool wait(int i, int parity) const {
-        return __all_sync(0xffffffffu, wait1(i, parity));
+        for (int left = kWaitTries; !__all_sync(0xffffffffu, mbar_try_wait_suspend(bar(i), parity & 1, 20000u)); --left) {
+            if (__any_sync(0xffffffffu, *abort_flag)) return false;
+            if (left == 0) {
+                give_up(i);
+                return false;
+            }
+        }
+        return true;
+    }
+    __device__ __forceinline__ void give_up(int i) const {
+        record_error(p->err, GDN_ERR_TIMEOUT, kTag + i);
+        *abort_flag = 1;
     }
     __device__ __forceinline__ bool wait1(int i, int parity) const {   // one lane
-        return wait_in_place(bar(i), parity & 1, abort_flag, p->err, kTag + i);
+        for (int left = kWaitTries; !mbar_try_wait_suspend(bar(i), parity & 1, 20000u); --left) {
+            if (*abort_flag) return false;
+            if (left == 0) {
+                give_up(i);
+                return false;
+            }
+        }
+        return true;
     }
 };
 
@@ -228,80 +233,76 @@ __device__ __forceinline__ void load_warp(const Work& w, const CUtensorMap* ma, 
     }
 }
 
+// The MMAs: one warp issues S and O += P C, another one O = A X and U, so that what a step costs besides its MMAs (some
+// hundred cycles of waits and commits) passes while the other's are at work. The whole warp walks through the code, with
+// values that are the same in every lane, and the first lane issues: descriptors then stay in uniform registers (under a
+// branch on the lane each MMA took some 140 cycles to issue). Operands whose rows hold the contraction advance by 32 bytes a
+// step within a half, the others by 16 rows of 128 bytes; in descriptors, in units of 16 bytes.
+template <uint32_t ID, int STEPS>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t b_half, uint32_t first) {
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+        mma_one_ss<ID>(d, desc_k(a + (k / 4) * kHalf) + 2 * (k % 4), desc_k(b + (k / 4) * b_half) + 2 * (k % 4), k > 0, first);
+}
+template <uint32_t ID, int PARTS>
+__device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate, uint32_t first) {
+    const uint64_t db = desc_mn(b, kHalf);
+#pragma unroll
+    for (int k = 0; k < 8 * PARTS; ++k) mma_one_ts<ID>(d, a + 8 * k, db + 128 * (k % 8), k ? 1u : accumulate, first);
+}
+
 template <int DA, int DC>
-__device__ __forceinline__ void mma_warp(const Work& w, int lane) {
-    constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_OI = idesc_bf16(128, DC, false, false),
-                       ID_OP = idesc_bf16(128, DC, false, true), ID_U = idesc_bf16(128, DA, false, true);
-    bool zero_seen = false;
-    auto ready = [&](int m) {   // the chunk's tiles have landed, and end in zeros where they should
-        if (!w.wait(B_FULL0 + (m & 1), m >> 1) || (!w.sums && !w.wait(B_AFULL0 + (m & 1), m >> 1))) return false;
-        if (w.length(m) < kChunk && !zero_seen) {
-            if (!w.wait(B_ZERO, 0)) return false;
-            zero_seen = true;
-        }
-        return true;
-    };
-    // The whole warp walks through this, with values that are the same in every lane, and the first lane issues: descriptors
-    // then stay in uniform registers (under a branch on the lane each MMA took some 140 cycles to issue). The start
-    // addresses of operands whose rows hold the contraction (K-major) advance by 32 bytes a step within a half, the others
-    // by 16 rows of 128 bytes; in descriptors, in units of 16 bytes.
+__device__ __forceinline__ void intra_warp(const Work& w, int lane) {
+    constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_OP = idesc_bf16(128, DC, false, true);
     const uint32_t first = lane == 0;
-    auto by_rows = [&](auto id, uint32_t d, uint32_t a, uint32_t b, uint32_t b_half) {
-#pragma unroll
-        for (int k = 0; k < DA / 16; ++k)
-            mma_one_ss<decltype(id)::value>(d, desc_k(a + (k / 4) * kHalf) + 2 * (k % 4), desc_k(b + (k / 4) * b_half) + 2 * (k % 4), k > 0, first);
-    };
-    auto by_tokens = [&](auto id, uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
-        const uint64_t db = desc_mn(b, kHalf);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mma_one_ts<decltype(id)::value>(d, a + 8 * k, db + 128 * k, k ? 1u : accumulate, first);
-    };
-    auto commit = [&](int i) { commit_one(w.bar(i), first); };
-    auto s_mma = [&](int m) {
-        const uint32_t A = w.base + (m & 1) * kStage;
-        by_rows(std::integral_constant<uint32_t, ID_S>(), w.tmem + kTmS, A, A + kTileBytes, kHalf);
-        commit(B_S);
-    };
     int m = 0;
     for (; m < w.chunks; ++m) {
-        const uint32_t A = w.base + (m & 1) * kStage, B = A + kTileBytes, C = B + kTileBytes;
-        if (w.sums) {
-            if (!ready(m)) break;
-        } else {
-            if (m == 0) {
-                if (!ready(0)) break;
-                tc_fence_after();
-                s_mma(0);
-            }
-            if (!w.wait(B_X, m) || (m > 0 && !w.wait(B_OFREE, m - 1))) break;
+        const int st = m & 1;
+        const uint32_t A = w.base + st * kStage, B = A + kTileBytes, C = B + kTileBytes;
+        if (!w.wait(B_FULL0 + st, m >> 1) || !w.wait(B_AFULL0 + st, m >> 1)) break;
+        if (w.length(m) < kChunk && !w.wait(B_ZERO, 0)) break;
+        if (m > 0 && !w.wait(B_O, m - 1)) break;   // (P has been read)
+        tc_fence_after();
+        mma_rows<ID_S, DA / 16>(w.tmem + kTmS, A, B, kHalf, first);
+        commit_one(w.bar(B_S), first);
+        if (!w.wait(B_P, m) || !w.wait(B_OSCALED, m)) break;
+        tc_fence_after();
+        mma_tokens<ID_OP, 1>(w.tmem + kTmO, w.tmem + kTmS, C, 1, first);
+        commit_one(w.bar(B_O), first);
+        commit_one(w.bar(B_EMPTY0 + st), first);
+    }
+    if (m < w.chunks) {
+        commit_one(w.bar(B_DRAIN0), first);
+        drain(w.bar(B_DRAIN0), 0, kWaitLimit);
+    }
+}
+
+template <int DA, int DC>
+__device__ __forceinline__ void state_mma_warp(const Work& w, int lane) {
+    constexpr uint32_t ID_OI = idesc_bf16(128, DC, false, false), ID_U = idesc_bf16(128, DA, false, true);
+    static_assert(kTmLo == kTmHi + 64, "one part behind the other");
+    const uint32_t first = lane == 0;
+    int m = 0;
+    for (; m < w.chunks; ++m) {
+        const int st = m & 1;
+        const uint32_t A = w.base + st * kStage, B = A + kTileBytes;
+        if (!w.wait(B_FULL0 + st, m >> 1)) break;
+        if (w.length(m) < kChunk && !w.wait(B_ZERO, 0)) break;
+        if (!w.sums) {
+            if (!w.wait(B_AFULL0 + st, m >> 1) || !w.wait(B_X, m) || (m > 0 && !w.wait(B_OFREE, m - 1))) break;
             tc_fence_after();
-            by_rows(std::integral_constant<uint32_t, ID_OI>(), w.tmem + kTmO, A, w.base + kX, DC * 128);
-            commit(B_OI);
+            mma_rows<ID_OI, DA / 16>(w.tmem + kTmO, A, w.base + kX, DC * 128, first);
+            commit_one(w.bar(B_OI), first);
         }
         if (!w.wait(B_VD, m)) break;
         tc_fence_after();
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-            by_tokens(std::integral_constant<uint32_t, ID_U>(), w.tmem + kTmU, w.tmem + kTmHi + (kTmLo - kTmHi) * part, B, part);
-        commit(B_U);
-        if (w.sums) {
-            commit(B_EMPTY0 + (m & 1));
-            continue;
-        }
-        if (!w.wait(B_P, m) || !w.wait(B_OSCALED, m)) break;
-        tc_fence_after();
-        by_tokens(std::integral_constant<uint32_t, ID_OP>(), w.tmem + kTmO, w.tmem + kTmS, C, 1);
-        commit(B_O);
-        commit(B_EMPTY0 + (m & 1));
-        if (m + 1 < w.chunks) {
-            if (!ready(m + 1) || !w.wait(B_O, m)) break;
-            tc_fence_after();
-            s_mma(m + 1);
-        }
+        mma_tokens<ID_U, 2>(w.tmem + kTmU, w.tmem + kTmHi, B, 0, first);
+        commit_one(w.bar(B_U), first);
+        commit_one(w.bar(B_EMPTY0 + st), first);
     }
     if (m < w.chunks) {
-        commit(B_DRAIN);
-        drain(w.bar(B_DRAIN), 0, kWaitLimit);
+        commit_one(w.bar(B_DRAIN1), first);
+        drain(w.bar(B_DRAIN1), 0, kWaitLimit);
     }
 }
 
@@ -313,14 +314,16 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
     const uint32_t lanes = w.tmem + ((uint32_t)(32 * warp) << 16);
     const uint32_t tab = w.base + kTab;
     // The weight of row i and column j is w^|i - j|. Columns in blocks of 32: w^(31 - c) (or, backward in time, w^c) for the column
-    // of a block, times what is left of the gap, one value a row and block. In the diagonal block that is w^(lane - 31) (or
-    // w^-lane), which fp32 holds unless the head decays by some 17 e-folds or more in a block; `steep` ones look every
-    // weight up.
-    float col[32];
+    // of a block, times what is left of the gap, one value a row and block; in the diagonal block 2^(log2 w gap) as it is.
+    // (Only the bits of columns that the row sees stay there: what lies behind it, infinities too, becomes zero.)
+    pair_t col[16];
+    uint32_t seen[16];
 #pragma unroll
-    for (int c = 0; c < 32; ++c) col[c] = lds(tab + 4 * (r.rev ? c : 31 - c));
-    const bool steep = !(w.lg * 31.f > -80.f);
-    const float diag = exp2f(w.lg * (r.rev ? -lane : lane - 31));
+    for (int c = 0; c < 16; ++c) {
+        col[c] = pack(lds(tab + 4 * (r.rev ? 2 * c : 31 - 2 * c)), lds(tab + 4 * (r.rev ? 2 * c + 1 : 30 - 2 * c)));
+        seen[c] = ((r.rev ? 2 * c >= lane : 2 * c <= lane) ? 0xffffu : 0u) | ((r.rev ? 2 * c + 1 >= lane : 2 * c + 1 <= lane) ? 0xffff0000u : 0u);
+    }
+    const float slope = r.rev ? w.lg : -w.lg, level = slope * lane;   // log2 of the diagonal block's weights: slope c - level
     for (int m = 0; m < w.chunks; ++m) {
         const int L = w.length(m);
         if (!w.wait(B_S, m)) return store_wait();
@@ -335,22 +338,20 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
             } else {
                 float x[32];
                 tmem_ld32(lanes + kTmS + 32 * b, x);
-                const float f = away ? lds(tab + 4 * (r.rev ? 32 * away - lane : 32 * away + lane - 31)) : diag;
+                const float f = lds(tab + 4 * (away == 0 ? 0 : r.rev ? 32 * away - lane : 32 * away + lane - 31));
                 tmem_wait_ld();
-                if (away == 0 && steep) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) x[c] *= lds(tab + 4 * abs(lane - c));
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) x[c] *= f * col[c];
-                }
-#pragma unroll
-                for (int c = 0; c < 16; ++c) q[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
-                if (away == 0) {   // the columns behind the row (by time)
-                    const uint32_t seen = r.rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+                if (away == 0) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
-                        q[c] &= (seen >> (2 * c) & 1 ? 0xffffu : 0u) | (seen >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
+                        q[c] = pack_bf16(x[2 * c] * ex2(fmaf(slope, 2 * c, -level)), x[2 * c + 1] * ex2(fmaf(slope, 2 * c + 1, -level))) & seen[c];
+                } else {
+                    const pair_t f2 = pack(f, f);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        float lo, hi;
+                        unpack(mul2(pack(x[2 * c], x[2 * c + 1]), mul2(f2, col[c])), lo, hi);
+                        q[c] = pack_bf16(lo, hi);
+                    }
                 }
             }
             tmem_st16(lanes + kTmS + 16 * b, q);
@@ -367,7 +368,7 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
             tmem_ld32(lanes + kTmO + 32 * b, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] *= keep;
+            for (int c = 0; c < 32; c += 2) unpack(mul2(pack(x[c], x[c + 1]), pack(keep, keep)), x[c], x[c + 1]);
             tmem_st32(lanes + kTmO + 32 * b, x);
         }
         tmem_wait_st();
@@ -379,14 +380,14 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
         const uint32_t mine = w.base + (m & 1) * kStage + warp * 8192;
         const int row0 = w.it.lo + kChunk * w.phys(m) + 32 * warp, rows = min(32, L - 32 * warp);
         constexpr int kPer = OUT_BF16 ? 64 : 32, kBoxes = DC / kPer;   // features of a box
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < kBoxes; ++b) {
-            if (b == 2) {   // (fp32: the first two boxes have to leave before the next two)
+            if (!OUT_BF16 && b == 2) {   // (fp32: the first two boxes have to leave before the next two)
                 store_wait();
                 __syncwarp();
             }
             const uint32_t box = mine + (b & 1) * 4096;
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < kPer / 32; ++x) {
                 float f[32];
                 tmem_ld32(lanes + kTmO + kPer * b + 32 * x, f);
@@ -512,7 +513,7 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
     const uint32_t ldm = (chan0 >> 6) * kHalf + half * 8192 + (lane >> 4) * 1024 + (lane & 7) * 128 +
                          (((((chan0 & 63) >> 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
     const int tok = 64 * half + 2 * (lane & 3);   // of its pairs in 8-token group 0
-    float2 weight[8];
+    pair_t weight[8];
     int weight_len = 0;
     bool zeroed = false;
     for (int m = 0; m < w.chunks; ++m) {
@@ -539,7 +540,7 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
                 const int j = tok + 8 * g, at = j + (r.rev ? 0 : kChunk - L);
-                weight[g] = make_float2(lds(key + 4 * at), lds(key + 4 * at + 4));
+                weight[g] = pack(lds(key + 4 * at), lds(key + 4 * at + 4));
             }
         }
         // Cw = hi + lo of 64 tokens' values of 32 channels, 16 channels at a time: hi is the value cut off to bf16 and lo the
@@ -554,12 +555,14 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
                 ldmatrix_trans(from + g * 1024, v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {   // (group g + i / 2, channels 8 (i % 2) ..)
-                    const float a = __uint_as_float(v[i] << 16) * weight[g + i / 2].x;
-                    const float b = __uint_as_float(v[i] & 0xffff0000u) * weight[g + i / 2].y;
+                    const pair_t y = mul2(pack(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u)), weight[g + i / 2]);
+                    float a, b;
+                    unpack(y, a, b);
                     const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
                     const int at = 2 * (g + i / 2) + (i & 1);
                     hi[at] = __byte_perm(ua, ub, 0x7632);
-                    lo[at] = pack_bf16(a - __uint_as_float(ua & 0xffff0000u), b - __uint_as_float(ub & 0xffff0000u));
+                    unpack(fma2(pack(__uint_as_float(ua & 0xffff0000u), __uint_as_float(ub & 0xffff0000u)), pack(-1.f, -1.f), y), a, b);
+                    lo[at] = pack_bf16(a, b);
                 }
             }
             const uint32_t to = lanes + ((uint32_t)(16 * x) << 16) + 32 * half;
@@ -579,7 +582,9 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
                 tmem_ld32(lanes + kTmU + 64 * half + 32 * b, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) X[32 * b + i] = fmaf(keep, X[32 * b + i], u[i]);
+                for (int i = 0; i < 32; i += 2)
+                    unpack(fma2(pack(keep, keep), pack(X[32 * b + i], X[32 * b + i + 1]), pack(u[i], u[i + 1])), X[32 * b + i],
+                           X[32 * b + i + 1]);
             }
         }
         if (!w.sums && m + 1 < w.chunks) {
@@ -625,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < B_N; ++i)
-            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? 4 : i == B_P || i == B_OUT || i == B_OSCALED || i == B_OFREE ? 128 : i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
+            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? 4 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT || i == B_OSCALED || i == B_OFREE ? 128 : i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
         *w.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
@@ -668,7 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             const CUtensorMap* map = &q.out[role];
             turned ? store_warp<K>(w, map, lane) : store_warp<V>(w, map, lane);
         }
-        if (warp == kMmaWarp) turned ? mma_warp<V, K>(w, lane) : mma_warp<K, V>(w, lane);
+        if (warp == kMmaWarp && !w.sums) turned ? intra_warp<V, K>(w, lane) : intra_warp<K, V>(w, lane);
+        if (warp == kStateMmaWarp) turned ? state_mma_warp<V, K>(w, lane) : state_mma_warp<K, V>(w, lane);
     }
     __syncwarp();
     tc_fence_before();
