@@ -15,7 +15,7 @@
 // its 128 rows (channels of C) are then the lanes, each of which scales its own channel; the chunk's tiles fill shared
 // memory (two stages of A, B, C: 192 KB, and 32 KB of X), which would not hold scaled copies as well.
 //
-// Warps: 0-3 P, the scaling of O, the outputs; 4-11 the state: Cw (each half of them 64 tokens) and X (each half 64 rows);
+// Warps: 0-3 P and the outputs; 4-11 the state: Cw (each half of them 64 tokens), X (each half 64 rows) and the scaling of O;
 // 12 loads (TMA, 128-byte swizzle), 13 and 15 issue the MMAs, 14 stores bf16 outputs (TMA). Every wait on an mbarrier is bounded: on expiry the kernel records
 // GDN_ERR_TIMEOUT, lets what it issued retire, frees tensor memory and returns.
 //
@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 512;   // (four warpgroups)
 constexpr int kStateThreads = 256;
-constexpr int kRegsOut = 120, kRegsState = 152, kRegsRest = 88;
+constexpr int kRegsOut = 144, kRegsState = 152, kRegsRest = 64;
 static_assert(128 * kRegsOut + 256 * kRegsState + 128 * kRegsRest == 128 * kThreads, "the registers of the launch");
 constexpr int kLoadWarp = 12, kMmaWarp = 13, kStoreWarp = 14, kStateMmaWarp = 15;
 constexpr long long kWaitLimit = 4000000000LL;   // SM cycles, some two seconds (for the waits while shutting down)
@@ -131,13 +131,11 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t (&v)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
 }
-// 16 lanes x 32 columns: register 2 g + h holds lane 8 h + T / 4, column 4 g + T % 4
-__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+// 16 lanes x 8 columns: register 2 g + h holds lane 8 h + T / 4, column 4 g + T % 4
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3])
+                 : "memory");
 }
 
 __device__ __forceinline__ float lds(uint32_t at) {
@@ -240,15 +238,19 @@ __device__ __forceinline__ void load_warp(const Work& w, const CUtensorMap* ma, 
 // step within a half, the others by 16 rows of 128 bytes; in descriptors, in units of 16 bytes.
 template <uint32_t ID, int STEPS>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t b_half, uint32_t first) {
+    uint64_t da = desc_k(a), db = desc_k(b);
+#pragma unroll 1
+    for (int f = 0; f < STEPS / 4; ++f, da += kHalf / 16, db += b_half / 16)
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k)
-        mma_one_ss<ID>(d, desc_k(a + (k / 4) * kHalf) + 2 * (k % 4), desc_k(b + (k / 4) * b_half) + 2 * (k % 4), k > 0, first);
+        for (int k = 0; k < 4; ++k) mma_one_ss<ID>(d, da + 2 * k, db + 2 * k, f + k > 0, first);
 }
 template <uint32_t ID, int PARTS>
 __device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate, uint32_t first) {
     const uint64_t db = desc_mn(b, kHalf);
+#pragma unroll 1
+    for (int k = 0; k < 8 * PARTS; k += 4, accumulate = 1)
 #pragma unroll
-    for (int k = 0; k < 8 * PARTS; ++k) mma_one_ts<ID>(d, a + 8 * k, db + 128 * (k % 8), k ? 1u : accumulate, first);
+        for (int i = 0; i < 4; ++i) mma_one_ts<ID>(d, a + 8 * (k + i), db + 128 * (k % 8 + i), i ? 1u : accumulate, first);
 }
 
 template <int DA, int DC>
@@ -306,7 +308,8 @@ __device__ __forceinline__ void state_mma_warp(const Work& w, int lane) {
     }
 }
 
-// P, the scaling of O, the outputs: thread = row (token) of the chunk = lane of tensor memory
+// P and the outputs: thread = row (token) of the chunk = lane of tensor memory. Sixteen columns at a time, the next ones on
+// their way from tensor memory meanwhile.
 template <int DA, int DC, bool OUT_BF16>
 __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map, int warp, int lane) {
     const Role& r = *w.r;
@@ -314,8 +317,10 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
     const uint32_t lanes = w.tmem + ((uint32_t)(32 * warp) << 16);
     const uint32_t tab = w.base + kTab;
     // The weight of row i and column j is w^|i - j|. Columns in blocks of 32: w^(31 - c) (or, backward in time, w^c) for the column
-    // of a block, times what is left of the gap, one value a row and block; in the diagonal block 2^(log2 w gap) as it is.
-    // (Only the bits of columns that the row sees stay there: what lies behind it, infinities too, becomes zero.)
+    // of a block, times what is left of the gap, one value a row and block. In the diagonal block that is w^(lane - 31) (or
+    // w^-lane), which fp32 holds for heads that lose fewer than 2^100 over a block; `steep` ones take 2^(log2 w gap) as it is.
+    // (Of the diagonal block only the bits of columns that the row sees stay: what lies behind it, infinities too, becomes
+    // zero.)
     pair_t col[16];
     uint32_t seen[16];
 #pragma unroll
@@ -323,101 +328,110 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
         col[c] = pack(lds(tab + 4 * (r.rev ? 2 * c : 31 - 2 * c)), lds(tab + 4 * (r.rev ? 2 * c + 1 : 30 - 2 * c)));
         seen[c] = ((r.rev ? 2 * c >= lane : 2 * c <= lane) ? 0xffffu : 0u) | ((r.rev ? 2 * c + 1 >= lane : 2 * c + 1 <= lane) ? 0xffff0000u : 0u);
     }
-    const float slope = r.rev ? w.lg : -w.lg, level = slope * lane;   // log2 of the diagonal block's weights: slope c - level
+    const bool steep = !(w.lg * 31.f > -100.f);
+    const float diag = exp2f(r.rev ? -w.lg * lane : w.lg * (lane - 31));
     for (int m = 0; m < w.chunks; ++m) {
         const int L = w.length(m);
         if (!w.wait(B_S, m)) return store_wait();
         tc_fence_after();
+        float x[2][16];
+        const int b0 = r.rev ? warp : 0, b1 = r.rev ? 4 : warp + 1;   // the blocks that the row sees anything of
+        tmem_ld16(lanes + kTmS + 32 * b0, x[0]);
+        if (!steep) {
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-            uint32_t q[16];
-            const int away = r.rev ? b - warp : warp - b;
-            if (away < 0) {
+            for (int b = b0; b < b1; ++b) {
+                const uint32_t all = b == warp ? 0u : 0xffffffffu;
+                const float f = b == warp ? diag : lds(tab + 4 * (r.rev ? 32 * (b - warp) - lane : 32 * (warp - b) + lane - 31));
+                const pair_t f2 = pack(f, f);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) q[c] = 0;
-            } else {
-                float x[32];
-                tmem_ld32(lanes + kTmS + 32 * b, x);
-                const float f = lds(tab + 4 * (away == 0 ? 0 : r.rev ? 32 * away - lane : 32 * away + lane - 31));
-                tmem_wait_ld();
-                if (away == 0) {
+                for (int y = 0; y < 2; ++y) {
+                    tmem_wait_ld();
+                    if (y == 0 || b + 1 < b1) tmem_ld16(lanes + kTmS + 32 * b + 16 * (y + 1), x[1 - y]);
+                    uint32_t q[8];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        q[c] = pack_bf16(x[2 * c] * ex2(fmaf(slope, 2 * c, -level)), x[2 * c + 1] * ex2(fmaf(slope, 2 * c + 1, -level))) & seen[c];
-                } else {
-                    const pair_t f2 = pack(f, f);
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
+                    for (int c = 0; c < 8; ++c) {
                         float lo, hi;
-                        unpack(mul2(pack(x[2 * c], x[2 * c + 1]), mul2(f2, col[c])), lo, hi);
-                        q[c] = pack_bf16(lo, hi);
+                        unpack(mul2(pack(x[y][2 * c], x[y][2 * c + 1]), mul2(f2, col[8 * y + c])), lo, hi);
+                        q[c] = pack_bf16(lo, hi) & (seen[8 * y + c] | all);
                     }
+                    tmem_st8(lanes + kTmS + 16 * b + 8 * y, q);
                 }
             }
-            tmem_st16(lanes + kTmS + 16 * b, q);
+        } else {
+#pragma unroll 1
+            for (int j = 32 * b0; j < 32 * b1; j += 16) {
+                uint32_t q[8];
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 16; c += 2) {
+                    const int gap = r.rev ? j + c - row : row - j - c, gap1 = r.rev ? gap + 1 : gap - 1;
+                    q[c / 2] = pack_bf16(gap >= 0 ? x[0][c] * ex2(w.lg * gap) : 0.f, gap1 >= 0 ? x[0][c + 1] * ex2(w.lg * gap1) : 0.f);
+                }
+                if (j + 16 < 32 * b1) tmem_ld16(lanes + kTmS + j + 16, x[0]);
+                tmem_st8(lanes + kTmS + j / 2, q);
+            }
         }
+        // (P's other blocks are zeros; where S lay under them it has been read, and P's own columns 16 b .. lie in S's
+        // first half, of which blocks 32 b .. are read before)
+        uint32_t none[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) none[c] = 0;
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b)
+            if (b < b0 || b >= b1) tmem_st16(lanes + kTmS + 16 * b, none);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(w.bar(B_P));
-        if (!w.wait(B_OI, m)) return store_wait();
-        tc_fence_after();
-        const float keep = exp2f(w.lg * (r.rev ? max(L - 1 - row, 0) : row + 1));
-#pragma unroll 1
-        for (int b = 0; b < DC / 32; ++b) {
-            float x[32];
-            tmem_ld32(lanes + kTmO + 32 * b, x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) unpack(mul2(pack(x[c], x[c + 1]), pack(keep, keep)), x[c], x[c + 1]);
-            tmem_st32(lanes + kTmO + 32 * b, x);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(w.bar(B_OSCALED));
         if (!w.wait(B_O, m)) return store_wait();
         tc_fence_after();
-        // out through A's tile, which is done with: each warp its own 8 KB of it, boxes of 32 rows of 128 bytes
-        const uint32_t mine = w.base + (m & 1) * kStage + warp * 8192;
+        // out through A's tile, which is done with: halves of 128 bytes by 128 rows
+        const uint32_t mine = w.base + (m & 1) * kStage + warp * 4096;
         const int row0 = w.it.lo + kChunk * w.phys(m) + 32 * warp, rows = min(32, L - 32 * warp);
-        constexpr int kPer = OUT_BF16 ? 64 : 32, kBoxes = DC / kPer;   // features of a box
+        constexpr int kPer = OUT_BF16 ? 64 : 32, kBoxes = DC / kPer;   // features of a half
+        tmem_ld16(lanes + kTmO, x[0]);
 #pragma unroll 1
         for (int b = 0; b < kBoxes; ++b) {
-            if (!OUT_BF16 && b == 2) {   // (fp32: the first two boxes have to leave before the next two)
+            if (!OUT_BF16 && b == 2) {   // (fp32: the first two halves have to leave before the next two)
                 store_wait();
                 __syncwarp();
             }
-            const uint32_t box = mine + (b & 1) * 4096;
+            const uint32_t box = mine + (b & 1) * kHalf;
 #pragma unroll 1
-            for (int x = 0; x < kPer / 32; ++x) {
-                float f[32];
-                tmem_ld32(lanes + kTmO + kPer * b + 32 * x, f);
-                tmem_wait_ld();
-                if (b == kBoxes - 1 && x == kPer / 32 - 1) {
-                    tc_fence_before();
-                    mbar_arrive(w.bar(B_OFREE));
-                }
-                if constexpr (OUT_BF16) {
+            for (int z = 0; z < kPer / 32; ++z) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        sts4(box + sw128(lane, 4 * x + k), pack_bf16(f[8 * k], f[8 * k + 1]), pack_bf16(f[8 * k + 2], f[8 * k + 3]),
-                             pack_bf16(f[8 * k + 4], f[8 * k + 5]), pack_bf16(f[8 * k + 6], f[8 * k + 7]));
-                } else {
+                for (int y = 0; y < 2; ++y) {
+                    tmem_wait_ld();
+                    const int next = kPer * b + 32 * z + 16 * (y + 1);
+                    if (next < DC) {
+                        tmem_ld16(lanes + kTmO + next, x[1 - y]);
+                    } else {
+                        tc_fence_before();
+                        mbar_arrive(w.bar(B_OFREE));
+                    }
+                    const float (&f)[16] = x[y];
+                    if constexpr (OUT_BF16) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        sts4(box + sw128(lane, k), __float_as_uint(f[4 * k]), __float_as_uint(f[4 * k + 1]),
-                             __float_as_uint(f[4 * k + 2]), __float_as_uint(f[4 * k + 3]));
+                        for (int k = 0; k < 2; ++k)
+                            sts4(box + sw128(lane, 4 * z + 2 * y + k), pack_bf16(f[8 * k], f[8 * k + 1]), pack_bf16(f[8 * k + 2], f[8 * k + 3]),
+                                 pack_bf16(f[8 * k + 4], f[8 * k + 5]), pack_bf16(f[8 * k + 6], f[8 * k + 7]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            sts4(box + sw128(lane, 4 * y + k), __float_as_uint(f[4 * k]), __float_as_uint(f[4 * k + 1]),
+                                 __float_as_uint(f[4 * k + 2]), __float_as_uint(f[4 * k + 3]));
+                    }
                 }
             }
             fence_proxy_async();
             __syncwarp();
-            if (rows == 32) {
-                if (!OUT_BF16 && lane == 0) tma_store_3d(map, box, kPer * b, w.h, row0);
-            } else {   // the sequence ends here: row by row, eight lanes each
+            if (!OUT_BF16 && rows == 32) {
+                if (lane == 0) tma_store_3d(map, box, kPer * b, w.h, row0);
+            } else if (OUT_BF16 ? L < kChunk : rows < 32) {   // the sequence ends in this chunk: row by row, eight lanes each
                 constexpr int kSize = OUT_BF16 ? 2 : 4;
                 for (int i = lane >> 3; i < rows; i += 4) {
-                    const float4 x = lds4(box + sw128(i, lane & 7));
+                    const float4 v = lds4(box + sw128(i, lane & 7));
                     char* to = (char*)r.out + (((long long)(row0 + i) * w.p->H + w.h) * DC + kPer * b) * kSize + 16 * (lane & 7);
-                    *reinterpret_cast<float4*>(to) = x;
+                    *reinterpret_cast<float4*>(to) = v;
                 }
                 __syncwarp();
             }
@@ -433,19 +447,18 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
     store_wait();
 }
 
-// Sends the bf16 outputs from A's tile and gives it back to the loads: lane i for the rows of warp i.
+// Sends the bf16 outputs from A's tile and gives it back to the loads (one lane).
 template <int DC>
-__device__ __forceinline__ void store_warp(const Work& w, const CUtensorMap* map, int lane) {
+__device__ __forceinline__ void store_warp(const Work& w, const CUtensorMap* map) {
     for (int m = 0; m < w.chunks; ++m) {
         if (!w.wait1(B_OUT, m)) break;
-        if (w.length(m) >= 32 * lane + 32) {   // (the last rows of a sequence have gone by other ways)
-            const uint32_t from = w.base + (m & 1) * kStage + lane * 8192;
-            const int row0 = w.it.lo + kChunk * w.phys(m) + 32 * lane;
+        if (w.length(m) == kChunk) {   // (a sequence's last rows have gone by other ways)
 #pragma unroll
-            for (int b = 0; b < DC / 64; ++b) tma_store_3d(map, from + 4096 * b, 64 * b, w.h, row0);
+            for (int b = 0; b < DC / 64; ++b)
+                tma_store_3d(map, w.base + (m & 1) * kStage + b * kHalf, 64 * b, w.h, w.it.lo + kChunk * w.phys(m));
             store_wait();
         }
-        mbar_arrive(w.bar(B_AFREE0 + (m & 1)));
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 4;" ::"r"(w.bar(B_AFREE0 + (m & 1))) : "memory");
     }
     store_wait();
 }
@@ -513,8 +526,6 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
     const uint32_t ldm = (chan0 >> 6) * kHalf + half * 8192 + (lane >> 4) * 1024 + (lane & 7) * 128 +
                          (((((chan0 & 63) >> 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
     const int tok = 64 * half + 2 * (lane & 3);   // of its pairs in 8-token group 0
-    pair_t weight[8];
-    int weight_len = 0;
     bool zeroed = false;
     for (int m = 0; m < w.chunks; ++m) {
         const int L = w.length(m);
@@ -535,43 +546,55 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
             mbar_arrive(w.bar(B_ZERO));
             if (!w.wait(B_ZERO, 0)) return;
         }
-        if (L != weight_len) {
-            weight_len = L;
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const int j = tok + 8 * g, at = j + (r.rev ? 0 : kChunk - L);
-                weight[g] = pack(lds(key + 4 * at), lds(key + 4 * at + 4));
-            }
-        }
-        // Cw = hi + lo of 64 tokens' values of 32 channels, 16 channels at a time: hi is the value cut off to bf16 and lo the
-        // rest of it, rounded
-        uint32_t from = C + ldm;
+        // Cw = hi + lo of 64 tokens' values of 32 channels, 16 tokens and 16 channels at a time: hi is the value cut off to bf16
+        // and lo the rest of it, rounded
+        const uint32_t weights = key + 4 * (tok + (r.rev ? 0 : kChunk - L));
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x, from ^= 32) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint32_t to = lanes + ((uint32_t)(16 * x) << 16) + 32 * half;
+            const uint32_t from = C + (ldm ^ 32 * x);
+#pragma unroll 1
             for (int g = 0; g < 8; g += 2) {
-                uint32_t v[4];   // two 8-token groups x 16 channels
+                uint32_t v[4], hi[4], lo[4];   // two 8-token groups x 16 channels
                 ldmatrix_trans(from + g * 1024, v);
+                const pair_t weight[2] = {pack(lds(weights + 32 * g), lds(weights + 32 * g + 4)),
+                                          pack(lds(weights + 32 * g + 32), lds(weights + 32 * g + 36))};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {   // (group g + i / 2, channels 8 (i % 2) ..)
-                    const pair_t y = mul2(pack(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u)), weight[g + i / 2]);
+                    const pair_t y = mul2(pack(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u)), weight[i / 2]);
                     float a, b;
                     unpack(y, a, b);
                     const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-                    const int at = 2 * (g + i / 2) + (i & 1);
-                    hi[at] = __byte_perm(ua, ub, 0x7632);
+                    hi[i] = __byte_perm(ua, ub, 0x7632);
                     unpack(fma2(pack(__uint_as_float(ua & 0xffff0000u), __uint_as_float(ub & 0xffff0000u)), pack(-1.f, -1.f), y), a, b);
-                    lo[at] = pack_bf16(a, b);
+                    lo[i] = pack_bf16(a, b);
                 }
+                tmem_st_16x128b_x2(to + kTmHi + 4 * g, hi);
+                tmem_st_16x128b_x2(to + kTmLo + 4 * g, lo);
             }
-            const uint32_t to = lanes + ((uint32_t)(16 * x) << 16) + 32 * half;
-            tmem_st_16x128b_x8(to + kTmHi, hi);
-            tmem_st_16x128b_x8(to + kTmLo, lo);
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(w.bar(B_VD));
+        if (!w.sums) {   // the rows' weights on O = A X, while U is formed: half of the columns each; here lane = row
+            if (!w.wait(B_OI, m)) return;
+            tc_fence_after();
+            const int row = chan;
+            const float keep = exp2f(w.lg * (r.rev ? max(L - 1 - row, 0) : row + 1));
+            const pair_t keep2 = pack(keep, keep);
+#pragma unroll 1
+            for (int b = 0; b < DC / 64; ++b) {
+                float x[32];
+                tmem_ld32(lanes + kTmO + DC / 2 * half + 32 * b, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) unpack(mul2(pack(x[i], x[i + 1]), keep2), x[i], x[i + 1]);
+                tmem_st32(lanes + kTmO + DC / 2 * half + 32 * b, x);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(w.bar(B_OSCALED));
+        }
         if (!w.wait(B_U, m)) return;
         tc_fence_after();
         const float keep = exp2f(w.lg * L);
@@ -630,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < B_N; ++i)
-            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? 4 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT || i == B_OSCALED || i == B_OFREE ? 128 : i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
+            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? 4 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT || i == B_OFREE ? 128 : i == B_OSCALED || i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
         *w.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
@@ -650,10 +673,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     tc_fence_after();
     w.tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const bool turned = K != V && w.r->state_t;   // dA = V, dC = K
-    // The launch's 128 registers a thread, dealt anew: 128 x 120 + 256 x 152 + 128 x 88 = 512 x 128. (At 128 the
+    // The launch's 128 registers a thread, dealt anew: 128 x 144 + 256 x 152 + 128 x 64 = 512 x 128. (At 128 the
     // state's warps spill, and the stack is in L2.)
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
         const bool bf16 = w.r->out_bf16;
         const CUtensorMap* map = &q.out[role];
         if (w.sums) {
@@ -669,9 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
         if (lane == 0 && warp == kLoadWarp)
             turned ? load_warp<V, K>(w, &q.a[role], &q.b[role], &q.c[role]) : load_warp<K, V>(w, &q.a[role], &q.b[role], &q.c[role]);
-        if (lane < 4 && warp == kStoreWarp && !w.sums && w.r->out_bf16) {
+        if (lane == 0 && warp == kStoreWarp && !w.sums && w.r->out_bf16) {
             const CUtensorMap* map = &q.out[role];
-            turned ? store_warp<K>(w, map, lane) : store_warp<V>(w, map, lane);
+            turned ? store_warp<K>(w, map) : store_warp<V>(w, map);
         }
         if (warp == kMmaWarp && !w.sums) turned ? intra_warp<V, K>(w, lane) : intra_warp<K, V>(w, lane);
         if (warp == kStateMmaWarp) turned ? state_mma_warp<V, K>(w, lane) : state_mma_warp<K, V>(w, lane);
@@ -733,7 +756,7 @@ cudaError_t launch_tc(const Params& p, cudaStream_t s) {
         const Role& r = p.role[i];
         if (!tile_map(&q.a[i], r.a, true, r.dA, r.a_heads, tokens, kChunk) || !tile_map(&q.b[i], r.b, true, r.dA, r.b_heads, tokens, kChunk) ||
             !tile_map(&q.c[i], r.c, true, r.dC, r.c_heads, tokens, kChunk) ||
-            !tile_map(&q.out[i], r.out, r.out_bf16, r.dC, p.H, tokens, 32))
+            !tile_map(&q.out[i], r.out, r.out_bf16, r.dC, p.H, tokens, r.out_bf16 ? kChunk : 32))
             return cudaErrorInvalidValue;
     }
     // (K, V: of the roles whose state is stored as it is)
