@@ -11,63 +11,58 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr unsigned kTagLengths = 0x51;
-// words of the workspace's header, from kWsVerdict on: entries of the two phases, tokens of all sequences
-enum { kCount1 = 0, kCount2, kTokens };
-
+// How chains are cut into pieces. `room`: pieces that the GPU runs at once. A chain of n chunks cut into piece 0 of `first` and
+// others of `rest` takes first + rest chunks' time instead of n (a sum over a piece takes about 0.4 of a forward's time,
+// so that first = 0.4 rest ends with the sums), and a second launch, which is worth kSaved chunks.
+constexpr int kSaved = 3;
 struct Cut {
-    int first = 0, rest = 0;     // chunks of piece 0 and of the others; rest 0: no sequence is cut
-    int pieces = 1;              // of every sequence, where all have T tokens
-    long long entries2 = 0;      // bound on the entries of phase 2, which bounds the middle pieces' sums too
+    int whole = INT_MAX;         // chains that are not cut come first
+    int first = 0, rest = 0, pieces = 1;
+    long long blocks2 = 0;       // of phase 2, which has as many pieces as phase 1 has piece 0s and sums of cut chains
 };
+__host__ __device__ inline int first_of(int rest) { return (2 * rest + 4) / 5; }
 
-// How sequences are cut. `room`: kernel blocks that the GPU holds at once, `per`: blocks that one piece takes. A sequence cut
-// into piece 0 of `first` chunks and others of `rest` takes first + rest chunks' time instead of all of them (a sum over a
-// piece takes about half of a forward's time, so first = rest / 2 ends with the sums), and a second launch, which is
-// worth kSaved chunks.
-constexpr int kSaved = 4;
-Cut cut(long long T, int nseq, bool packed, long long room, long long per) {
+// Chains of n chunks each: as many as fill the GPU whole rounds run in one piece, the others are cut so that they fill it too.
+Cut cut_even(long long T, long long chains, long long room) {
     Cut c;
-    const long long at_once = room / per;
-    if (at_once < 2) return c;
-    if (!packed) {
-        const long long n = (T + kChunk - 1) / kChunk;
-        const long long more = std::min(at_once / nseq, n);   // pieces behind the first one
-        if (more < 2) return c;
-        const long long rest = (2 * n + 2 * more) / (2 * more + 1);   // n / (more + 1/2), rounded up
-        long long first = n - more * rest;
-        if (first < 1) first = std::max(1LL, rest / 2);
-        if (first + rest + kSaved > n) return c;
-        c.first = (int)first;
-        c.rest = (int)rest;
-        c.pieces = 1 + (int)((n - first + rest - 1) / rest);
-        c.entries2 = (long long)nseq * (c.pieces - 1);
-        return c;
-    }
-    const long long most = T / kChunk + nseq;   // chunks of any lengths
-    const long long n = T / kChunk + nseq / 2;  // and as a rule
-    const long long rest = std::max(1LL, (n + at_once - 1) / at_once), first = (rest + 1) / 2;
-    if (first + rest + kSaved > T / kChunk + 1) return c;
+    const long long n = (T + kChunk - 1) / kChunk, left = room > 0 ? chains % room : 0;
+    if (left == 0) return c;
+    const long long more = std::min(room / left, n);       // pieces behind the first one
+    if (more < 2) return c;
+    const long long rest = (5 * n + 5 * more + 1) / (5 * more + 2);   // n / (more + 0.4), rounded up
+    long long first = n - more * rest;
+    if (first < 1) first = first_of((int)rest);
+    if (first + rest + kSaved > n) return c;
+    c.whole = (int)(chains - left);
     c.first = (int)first;
     c.rest = (int)rest;
-    c.entries2 = most / rest + std::min<long long>(nseq, most / (first + rest + kSaved));
+    c.pieces = 1 + (int)((n - first + rest - 1) / rest);
+    c.blocks2 = left * (c.pieces - 1);
     return c;
 }
 
-// whether a sequence of n chunks is cut, and into how many pieces (packed batches)
-__host__ __device__ inline int pieces_of(int n, int first, int rest) {
-    return rest > 0 && n >= first + rest + kSaved ? 1 + (n - first + rest - 1) / rest : 1;
-}
+// Packed sequences: whether the plan may cut any, with room for `room` pieces behind first ones.
+bool cut_possible(long long T, long long room) { return room >= 2 && T / kChunk + 1 >= 2 + kSaved; }
+
+// a sequence of n chunks, in a batch that is cut
+__device__ __forceinline__ int more_pieces(int n, int first, int rest) { return n > first + 1 ? (n - first + rest - 1) / rest : 0; }
 
 // Checks the lengths of a packed batch and makes the phases' entries: every sequence's piece 0, then the middle pieces;
-// the pieces from 1 on. Bad lengths are recorded and leave no entries, so that nothing is written.
+// the pieces from 1 on. Bad lengths are recorded and leave no entries, so that nothing is written. The cut: the
+// shortest `rest` with which at most `room` pieces lie behind first ones, where that takes less time than the longest
+// sequence by itself; every warp tries one.
 __global__ void __launch_bounds__(kPlanThreads)
-    plan_kernel(const int* cu, int nseq, int T, int first, int rest, int bound2, int* words, int4* table1, int4* table2,
-                DeviceError* err) {
+    plan_kernel(const int* cu, int nseq, int T, int room, int* words, int4* table1, int4* table2, DeviceError* err) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ int warp_sum[32];
-    const int t = threadIdx.x;
+    __shared__ int warp_sum[32], warp_max[32];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     bool bad = t == 0 && (cu[0] != 0 || cu[nseq] > T);
-    for (int s = t; s < nseq; s += kPlanThreads) bad |= cu[s + 1] < cu[s];
+    int longest = 0;
+    for (int s = t; s < nseq; s += kPlanThreads) {
+        const int a = cu[s], b = cu[s + 1];
+        bad |= b < a;
+        longest = max(longest, (int)(((long long)b - a + kChunk - 1) / kChunk));
+    }
     if (__syncthreads_or(bad)) {
         if (t == 0) {
             if (atomicCAS(&err->code, 0u, (unsigned)GDN_ERR_INVALID_ARG) == 0u) atomicExch(&err->detail, kTagLengths);
@@ -75,18 +70,45 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         return;
     }
+    auto chunks = [&](int s) { return (cu[s + 1] - cu[s] + kChunk - 1) / kChunk; };
+    int first = 0, rest = 0;
+    if (room > 0) {
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0) warp_max[warp] = longest;
+        __syncthreads();
+        longest = __reduce_max_sync(0xffffffffu, warp_max[lane]);
+        // lengths worth trying: from what an even cut of all chunks would give on, in steps of a sixteenth of it
+        const int even = max(1, (int)(((long long)cu[nseq] / kChunk) / (room + nseq))), step = (even + 15) / 16;
+        for (int r0 = even; r0 + first_of(r0) + kSaved <= longest; r0 += 32 * step) {
+            const int r = r0 + warp * step, f = first_of(r);
+            long long count = 0;
+            for (int s = lane; s < nseq; s += 32) count += more_pieces(chunks(s), f, r);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) count += __shfl_xor_sync(0xffffffffu, count, off);
+            __syncthreads();
+            if (lane == 0) warp_sum[warp] = count <= room;
+            __syncthreads();
+            const unsigned fit = __ballot_sync(0xffffffffu, warp_sum[lane]);
+            if (fit) {
+                rest = r0 + (__ffs(fit) - 1) * step;
+                first = first_of(rest);
+                break;
+            }
+        }
+        if (first + rest + kSaved > longest) rest = 0;
+    }
+    __syncthreads();
     int before = 0;   // pieces behind the first ones of all sequences before this round's
     for (int s0 = 0; s0 < nseq; s0 += kPlanThreads) {
         const int s = s0 + t;
-        const int n = s < nseq ? (int)(((long long)cu[s + 1] - cu[s] + kChunk - 1) / kChunk) : 0;
-        const int pieces = s < nseq ? pieces_of(n, first, rest) : 1;
+        const int pieces = s < nseq && rest > 0 ? 1 + more_pieces(chunks(s), first, rest) : 1;
         int sum = pieces - 1;   // inclusive sums over the warp, then over the warps
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, sum, off);
-            if ((t & 31) >= off) sum += y;
+            if (lane >= off) sum += y;
         }
-        if ((t & 31) == 31) warp_sum[t >> 5] = sum;
+        if (lane == 31) warp_sum[warp] = sum;
         __syncthreads();
         if (t < 32) {
             int x = warp_sum[t];
@@ -98,16 +120,14 @@ __global__ void __launch_bounds__(kPlanThreads)
             warp_sum[t] = x;
         }
         __syncthreads();
-        const int slot0 = before + sum - (pieces - 1) + (t >= 32 ? warp_sum[(t >> 5) - 1] : 0);
-        if (s < nseq && slot0 + pieces - 1 <= bound2) {
+        const int slot0 = before + sum - (pieces - 1) + (warp ? warp_sum[warp - 1] : 0);
+        if (s < nseq) {
             table1[s] = make_int4(s, 0, pieces, slot0);
             for (int q = 1; q < pieces; ++q) {
                 table2[slot0 + q - 1] = make_int4(s, q, pieces, slot0);
-                // (the last piece's place among the sums stays empty: seq -1)
+                // (the last piece's place among the sums stays empty: sequence -1)
                 table1[nseq + slot0 + q - 1] = make_int4(q < pieces - 1 ? s : -1, q, pieces, slot0);
             }
-        } else if (s < nseq) {
-            table1[s] = make_int4(s, 0, 1, 0);   // (the bound holds: not reached)
         }
         before += warp_sum[31];
         __syncthreads();
@@ -116,6 +136,8 @@ __global__ void __launch_bounds__(kPlanThreads)
         words[kCount1] = nseq + before;
         words[kCount2] = before;
         words[kTokens] = cu[nseq];
+        words[kFirst] = first;
+        words[kRest] = rest;
     }
 }
 
@@ -161,18 +183,19 @@ gdn_status check(const gdn_problem* p, int Hqk, int nseq, bool packed) {
     return GDN_OK;
 }
 
-// blocks that one piece takes, and that the GPU holds at once
-long long blocks_of(const gdn_problem& p, bool tc, int roles) {
-    if (tc) return (long long)p.H * roles;
-    return (long long)p.H * (roles == 3 ? 2 * p.K / 64 + p.V / 64 : p.V / 64);
+// Blocks that the GPU runs at once, in pieces of one chain; and of one sequence with all its heads and roles (packed)
+long long room_of(const gdn_problem& p, bool tc, int sms, bool backward) {
+    return tc ? sms : 2LL * sms / (std::max(backward ? p.K : 0, p.V) / 64);
 }
-long long room_of(bool tc, int sms) { return (tc ? 1LL : 2LL) * sms; }
+long long packed_room(const gdn_problem& p, bool tc, int sms, bool backward) {
+    const long long room = room_of(p, tc, sms, backward) / ((long long)p.H * (backward ? 3 : 1));
+    return cut_possible(p.T, room) ? room : 0;
+}
 
 struct Layout {
     size_t table1, table2, slots, part[2], total;
-    size_t slot_bytes;   // of one role
 };
-Layout layout(const gdn_problem& p, int Hqk, int nseq, bool packed, const Cut& c, bool backward) {
+Layout layout(const gdn_problem& p, int Hqk, int nseq, bool packed, bool tc, int sms, bool backward, Cut* even = nullptr) {
     Layout l{};
     size_t at = kWsHeader;
     auto take = [&](size_t bytes) {
@@ -180,12 +203,19 @@ Layout layout(const gdn_problem& p, int Hqk, int nseq, bool packed, const Cut& c
         at += ws_round(bytes);
         return here;
     };
+    const long long width = (long long)p.H * (backward ? 3 : 1);
+    long long states;
     if (packed) {
-        l.table1 = take(sizeof(int4) * (size_t)(nseq + c.entries2));
-        l.table2 = take(sizeof(int4) * (size_t)c.entries2);
+        const long long room = packed_room(p, tc, sms, backward);
+        l.table1 = take(sizeof(int4) * (size_t)(nseq + room));
+        l.table2 = take(sizeof(int4) * (size_t)room);
+        states = room * width;
+    } else {
+        const Cut c = cut_even(p.T, nseq * width, room_of(p, tc, sms, backward));
+        if (even) *even = c;
+        states = c.blocks2;
     }
-    l.slot_bytes = ws_round(sizeof(float) * (size_t)c.entries2 * p.H * p.K * p.V);
-    l.slots = take(l.slot_bytes * (backward ? 3 : 1));
+    l.slots = take(sizeof(float) * (size_t)states * p.K * p.V);
     if (backward && Hqk != p.H)
         for (size_t& x : l.part) x = take(sizeof(float) * (size_t)p.B * p.T * p.H * p.K);
     l.total = at;
@@ -194,37 +224,43 @@ Layout layout(const gdn_problem& p, int Hqk, int nseq, bool packed, const Cut& c
 
 bool misaligned(const void* ptr, unsigned bytes) { return reinterpret_cast<uintptr_t>(ptr) & (bytes - 1); }
 
-// Both directions: the roles' pieces in one or two launches, behind the plan of a packed batch.
+// Both directions: the chains' pieces in one or two launches, behind the plan of a packed batch.
 gdn_status run(Params& c, const gdn_problem& p, int Hqk, bool backward, void* workspace, cudaStream_t s) {
     const bool packed = c.cu != nullptr;
     const bool tc = tc_supported(c);
     const int sms = current_sm_count();
-    const Cut k = cut(p.T, c.nseq, packed, room_of(tc, sms), blocks_of(p, tc, c.nroles));
-    const Layout l = layout(p, Hqk, c.nseq, packed, k, backward);
+    Cut k;
+    const Layout l = layout(p, Hqk, c.nseq, packed, tc, sms, backward, &k);
     char* ws = reinterpret_cast<char*>(workspace);
     c.err = reinterpret_cast<DeviceError*>(ws);
+    c.slots = reinterpret_cast<float*>(ws + l.slots);
+    c.whole = k.whole;
     c.first = k.first;
     c.rest = k.rest;
     c.pieces = k.pieces;
-    for (int i = 0; i < c.nroles; ++i) c.role[i].slots = reinterpret_cast<float*>(ws + l.slots + i * l.slot_bytes);
     int* words = reinterpret_cast<int*>(ws + kWsVerdict);
     int4* table1 = reinterpret_cast<int4*>(ws + l.table1);
     int4* table2 = reinterpret_cast<int4*>(ws + l.table2);
+    const long long width = (long long)c.H * c.nroles, chains = c.nseq * width;
+    long long blocks1 = chains, blocks2 = 0;
     if (packed) {
-        plan_kernel<<<1, kPlanThreads, 0, s>>>(c.cu, c.nseq, p.T, k.first, k.rest, (int)k.entries2, words, table1, table2, c.err);
+        const int room = (int)packed_room(p, tc, sms, backward);
+        plan_kernel<<<1, kPlanThreads, 0, s>>>(c.cu, c.nseq, p.T, room, words, table1, table2, c.err);
         if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+        blocks2 = room * width;
+        blocks1 += blocks2;
+    } else if (k.blocks2 > 0) {
+        blocks2 = k.blocks2;
+        blocks1 += blocks2 / (k.pieces - 1) * (k.pieces - 2);
     }
-    auto phase = [&](int number, long long entries) {
-        c.phase = number;
-        c.entries = (int)entries;
-        c.table = reinterpret_cast<const int*>(number == 1 ? table1 : table2);
-        c.count = words + (number == 1 ? kCount1 : kCount2);
-        c.dependent = packed || number == 2;
-        return tc ? launch_tc(c, s) : launch_simt(c, s);
-    };
-    const long long middle = packed ? k.entries2 : k.rest ? (long long)c.nseq * (k.pieces - 2) : 0;
-    if (phase(1, c.nseq + middle) != cudaSuccess) return GDN_ERR_CUDA;
-    if (k.entries2 > 0 && phase(2, k.entries2) != cudaSuccess) return GDN_ERR_CUDA;
+    c.words = words;
+    for (int phase = 1; phase <= (blocks2 > 0 ? 2 : 1); ++phase) {
+        c.phase = phase;
+        c.blocks = (int)(phase == 1 ? blocks1 : blocks2);
+        c.table = reinterpret_cast<const int*>(phase == 1 ? table1 : table2);
+        c.dependent = packed || phase == 2;
+        if ((tc ? launch_tc(c, s) : launch_simt(c, s)) != cudaSuccess) return GDN_ERR_CUDA;
+    }
     return GDN_OK;
 }
 
@@ -241,10 +277,8 @@ size_t gdn_linear_workspace_bytes(const gdn_problem* p, int Hqk, int nseq, int b
     size_t most = 0;
     for (int packed = 0; packed < 2; ++packed) {
         if (check(p, Hqk, nseq, packed) != GDN_OK) continue;
-        for (int tc = 0; tc < 2; ++tc) {   // (which kernels run depends on the output's type too)
-            const Cut c = cut(p->T, nseq, packed, room_of(tc, current_sm_count()), blocks_of(*p, tc, backward ? 3 : 1));
-            most = std::max(most, layout(*p, Hqk, nseq, packed, c, backward != 0).total);
-        }
+        for (int tc = 0; tc < 2; ++tc)   // (which kernels run depends on the output's type too)
+            most = std::max(most, layout(*p, Hqk, nseq, packed, tc, current_sm_count(), backward != 0).total);
     }
     return most;
 }
@@ -328,9 +362,7 @@ gdn_status gdn_linear_bwd(const gdn_problem* p, int Hqk, int nseq, const int* cu
     }
     // the gradients of shared heads: each head's own in the workspace, then their sums
     char* ws = reinterpret_cast<char*>(workspace);
-    const bool tc = tc_supported(c);
-    const Layout l = layout(*p, Hqk, nseq, cu_seqlens != nullptr,
-                            cut(p->T, nseq, cu_seqlens != nullptr, room_of(tc, current_sm_count()), blocks_of(*p, tc, 3)), true);
+    const Layout l = layout(*p, Hqk, nseq, cu_seqlens != nullptr, tc_supported(c), current_sm_count(), true);
     if (grouped)
         for (int i = 0; i < 2; ++i) {
             c.role[i].out = ws + l.part[i];

@@ -31,8 +31,6 @@ struct Role {
     void* out;             // [tokens][H][dC]
     const float* start;    // [nseq][H] states, or null: zero
     float* last;           // receives the states behind the last token, or null
-    float* slots;          // workspace: [slot][H][dA][dC]; slot of piece p >= 1: the state entering it (p = 1, written by
-                           // piece 0), or the sum over piece p - 1
     int a_heads, b_heads, c_heads;   // head h of the rule reads head h / (H / heads)
     int a_bf16, b_bf16, c_bf16, out_bf16;
     int dA, dC;
@@ -40,65 +38,83 @@ struct Role {
     int state_t;           // start and last are stored [dC][dA]
 };
 
-// One piece of one sequence, for a kernel block.
+// What a kernel block does: one piece of a chain, which is one sequence, head and role.
 struct Item {
-    int seq, lo, len;      // the sequence's first token and length
+    int seq, h, role;
+    int lo, len;           // the sequence's first token and length
     int piece, pieces;
     int m0, m1;            // its chunks, by number in the role's direction
-    int slot0;             // slot of piece 1
+    long long slot;        // state-sized places in the workspace: of piece p >= 1 at slot + (p - 1) slot_step, the state entering
+    int slot_step;         // it (p = 1, written by piece 0), or the sum over piece p - 1
 };
 
-// A packed batch's pieces, made on the device: entries of kFields ints.
-constexpr int kFields = 4;   // sequence, piece, pieces, slot0
 struct Params {
     Role role[kMaxRoles];
     int nroles;
     const float* decay;    // [H], natural log
+    float* slots;
     const int* cu;         // packed batches; null: nseq sequences of T tokens
-    const int* table;      // this phase's entries, and how many of them there are
-    const int* count;
+    const int* table;      // packed: the phase's entries, four ints each (sequence or -1, piece, pieces, slot of piece 1), all of
+    const int* words;      // whose heads and roles are cut alike; and the words of the plan
     int nseq, T, H;
-    int first, rest;       // chunks of piece 0 and of the others
-    int pieces;            // of every sequence, where the batch is not packed
-    int phase;             // 1: piece 0 of every sequence, sums of the middle ones; 2: the other pieces
-    int entries;           // grid: entries x H x tiles, by roles
+    int whole;             // not packed: chains before this number run in one piece, the others in `pieces`
+    int first, rest, pieces;   // chunks of piece 0 and of the others (not packed)
+    int phase;             // 1: piece 0 of every chain, sums of the middle pieces; 2: the other pieces
+    int blocks;            // of the phase, by tiles
     int tiles;             // of the columns, of the role with the most of them
     int dependent;         // launched while the grid before it still runs
     DeviceError* err;
 };
+// words of a packed batch's plan, in the workspace's header from kWsVerdict on: entries of the phases, tokens of all
+// sequences, chunks of piece 0 and of the others
+enum { kCount1 = 0, kCount2, kTokens, kFirst, kRest };
 
-// What entry e of the phase is; false: nothing. Whether it wants sums alone: 1 <= piece in phase 1.
-__device__ __forceinline__ bool item_of(const Params& p, int e, Item& it) {
+// What block number e of the phase does; false: nothing. It wants sums alone where 1 <= piece in phase 1.
+__device__ __forceinline__ bool item_of(const Params& p, int e, Item& it, int& first, int& rest) {
+    const int width = p.H * p.nroles;   // chains of a sequence; roles side by side, which read the same tensors
+    int chain;
     if (p.cu) {
-        if (e >= __ldcg(p.count)) return false;
-        const int4 f = __ldcg(reinterpret_cast<const int4*>(p.table) + e);
+        const int entry = e / width;
+        chain = e - entry * width;
+        if (entry >= __ldcg(p.words + (p.phase == 1 ? kCount1 : kCount2))) return false;
+        const int4 f = __ldcg(reinterpret_cast<const int4*>(p.table) + entry);
         if (f.x < 0) return false;
         it.seq = f.x;
         it.piece = f.y;
         it.pieces = f.z;
-        it.slot0 = f.w;
+        it.slot = (long long)f.w * width + chain;
+        it.slot_step = width;
         it.lo = __ldg(p.cu + it.seq);
         it.len = __ldg(p.cu + it.seq + 1) - it.lo;
+        first = __ldcg(p.words + kFirst);
+        rest = __ldcg(p.words + kRest);
     } else {
-        it.pieces = p.pieces;
-        if (p.phase == 1) {
-            it.seq = e;
-            it.piece = 0;
-            if (e >= p.nseq) {
-                it.seq = (e - p.nseq) / (p.pieces - 2);
-                it.piece = 1 + (e - p.nseq) % (p.pieces - 2);
-            }
-        } else {
-            it.seq = e / (p.pieces - 1);
+        const int chains = p.nseq * width;
+        if (p.phase == 2) {
+            chain = p.whole + e / (p.pieces - 1);
             it.piece = 1 + e % (p.pieces - 1);
+        } else if (e < chains) {
+            chain = e;
+            it.piece = 0;
+        } else {
+            chain = p.whole + (e - chains) / (p.pieces - 2);
+            it.piece = 1 + (e - chains) % (p.pieces - 2);
         }
-        it.slot0 = it.seq * (p.pieces - 1);
+        it.pieces = chain < p.whole ? 1 : p.pieces;
+        it.slot = (long long)(chain - p.whole) * (p.pieces - 1);
+        it.slot_step = 1;
+        it.seq = chain / width;
+        chain -= it.seq * width;
         it.lo = it.seq * p.T;
         it.len = p.T;
+        first = p.first;
+        rest = p.rest;
     }
+    it.h = chain / p.nroles;
+    it.role = chain - it.h * p.nroles;
     const int n = (it.len + kChunk - 1) / kChunk;
-    it.m0 = it.piece == 0 ? 0 : p.first + (it.piece - 1) * p.rest;
-    it.m1 = it.piece == it.pieces - 1 ? n : p.first + it.piece * p.rest;
+    it.m0 = it.piece == 0 ? 0 : first + (it.piece - 1) * rest;
+    it.m1 = it.piece == it.pieces - 1 ? n : first + it.piece * rest;
     return true;
 }
 

@@ -40,8 +40,8 @@ struct Smem {
 };
 
 template <int DA>
-__device__ __forceinline__ void walk(const Params& p, const Role& r, const Item& it, int h, int tile, Smem<DA>& sm) {
-    const int tid = threadIdx.x;
+__device__ __forceinline__ void walk(const Params& p, const Role& r, const Item& it, int first, int rest, int tile, Smem<DA>& sm) {
+    const int tid = threadIdx.x, h = it.h;
     const bool sums = p.phase == 1 && it.piece > 0;
     const float lg = log2_weight(p.decay, h);
     const int col0 = tile * kTile;
@@ -60,7 +60,7 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
         const long long row = RT * tr + i, col = col0 + 4 * tc + c;
         return r.state_t ? col * DA + row : row * r.dC + col;
     };
-    auto slot = [&](int q) { return r.slots + ((long long)(it.slot0 + q - 1) * p.H + h) * state; };
+    auto slot = [&](int q) { return p.slots + (it.slot + (long long)(q - 1) * it.slot_step) * state; };
     auto slot_at = [&](int i) { return (long long)(RT * tr + i) * r.dC + col0 + 4 * tc; };
     if (it.piece == 0) {
         if (r.start) {
@@ -74,7 +74,7 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
         for (int q = 1; q <= it.piece; ++q) {
             // entering piece q: from the state entering piece q - 1 and that piece's sum
             const float keep = q == 1 ? 0.f
-                : exp2f(lg * tokens_of(p.first + (q - 2) * p.rest, p.first + (q - 1) * p.rest, it.len, r.rev));
+                : exp2f(lg * tokens_of(first + (q - 2) * rest, first + (q - 1) * rest, it.len, r.rev));
             const float* from = slot(q);
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
@@ -254,14 +254,16 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
 __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) char raw[];
     if (p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Role& r = p.role[blockIdx.y];
-    const int tile = blockIdx.x % p.tiles, h = blockIdx.x / p.tiles % p.H, e = blockIdx.x / p.tiles / p.H;
+    const int tile = blockIdx.x % p.tiles;
     Item it;
-    if (tile * kTile >= r.dC || !item_of(p, e, it)) return;
+    int first, rest;
+    if (!item_of(p, blockIdx.x / p.tiles, it, first, rest)) return;
+    const Role& r = p.role[it.role];
+    if (tile * kTile >= r.dC) return;
     if (r.dA == 64)
-        walk<64>(p, r, it, h, tile, *reinterpret_cast<Smem<64>*>(raw));
+        walk<64>(p, r, it, first, rest, tile, *reinterpret_cast<Smem<64>*>(raw));
     else
-        walk<128>(p, r, it, h, tile, *reinterpret_cast<Smem<128>*>(raw));
+        walk<128>(p, r, it, first, rest, tile, *reinterpret_cast<Smem<128>*>(raw));
 }
 
 }  // namespace
@@ -275,7 +277,7 @@ cudaError_t launch_simt(const Params& q, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<128>));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((long long)p.entries * p.H * p.tiles), (unsigned)p.nroles);
+    cfg.gridDim = dim3((unsigned)((long long)p.blocks * p.tiles));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;

@@ -15,8 +15,8 @@
 // its 128 rows (channels of C) are then the lanes, each of which scales its own channel; the chunk's tiles fill shared
 // memory (two stages of A, B, C: 192 KB, and 32 KB of X), which would not hold scaled copies as well.
 //
-// Warps: 0-3 P and the outputs; 4-11 the state: Cw (each half of them 64 tokens), X (each half 64 rows) and the scaling of O;
-// 12 loads (TMA, 128-byte swizzle), 13 and 15 issue the MMAs, 14 stores bf16 outputs (TMA). Every wait on an mbarrier is bounded: on expiry the kernel records
+// Warps: 0-7 P and the outputs; 8-15 the state: Cw (each half of them 64 tokens), X (each half 64 rows) and the scaling of O;
+// 16 loads (TMA, 128-byte swizzle), 17 and 19 issue the MMAs, 18 stores bf16 outputs (TMA). Every wait on an mbarrier is bounded: on expiry the kernel records
 // GDN_ERR_TIMEOUT, lets what it issued retire, frees tensor memory and returns.
 //
 // A sequence's last chunk may hold fewer than 128 tokens: the rows of B and C behind it (the next sequence's) are
@@ -32,11 +32,12 @@ namespace gdn {
 namespace linear {
 namespace {
 
-constexpr int kThreads = 512;   // (four warpgroups)
-constexpr int kStateThreads = 256;
-constexpr int kRegsOut = 144, kRegsState = 152, kRegsRest = 64;
-static_assert(128 * kRegsOut + 256 * kRegsState + 128 * kRegsRest == 128 * kThreads, "the registers of the launch");
-constexpr int kLoadWarp = 12, kMmaWarp = 13, kStoreWarp = 14, kStateMmaWarp = 15;
+constexpr int kThreads = 640;   // five warpgroups
+constexpr int kOutThreads = 256, kStateThreads = 256;
+constexpr int kStateWarp0 = 8;
+constexpr int kRegsOut = 64, kRegsState = 144, kRegsRest = 64, kRegsLaunch = 96;
+static_assert(256 * kRegsOut + 256 * kRegsState + 128 * kRegsRest == kRegsLaunch * kThreads, "the registers of the launch");
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kStoreWarp = 18, kStateMmaWarp = 19;
 constexpr long long kWaitLimit = 4000000000LL;   // SM cycles, some two seconds (for the waits while shutting down)
 constexpr int kWaitTries = 1 << 20;              // of a wait: a second or so at least, 20 at most
 
@@ -167,6 +168,7 @@ struct Work {
     const Role* r;
     Item it;
     int h, chunks, n;      // chunks of the piece, of the sequence
+    int first, rest;
     bool sums;             // phase 1's middle pieces: U alone
     uint32_t base, tmem;
     volatile int* abort_flag;
@@ -174,6 +176,9 @@ struct Work {
     __device__ __forceinline__ int phys(int m) const { return r->rev ? n - 1 - (it.m0 + m) : it.m0 + m; }
     __device__ __forceinline__ int length(int m) const { return min(kChunk, it.len - kChunk * phys(m)); }
     __device__ __forceinline__ uint32_t bar(int i) const { return base + kBar + 8 * i; }
+    // tensor memory of Cw and U; sums alone have two of each, in the places of S and O, and form a chunk's Cw during the last one's U
+    __device__ __forceinline__ uint32_t cw(int m) const { return sums && (m & 1) ? kTmS : kTmHi; }
+    __device__ __forceinline__ uint32_t u(int m) const { return sums && (m & 1) ? kTmO : kTmU; }
     // the whole warp waits; every lane gets the same verdict
     __device__ __forceinline__ bool wait(int i, int parity) const {
         for (int left = kWaitTries; !__all_sync(0xffffffffu, mbar_try_wait_suspend(bar(i), parity & 1, 20000u)); --left) {
@@ -244,13 +249,13 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uin
 #pragma unroll
         for (int k = 0; k < 4; ++k) mma_one_ss<ID>(d, da + 2 * k, db + 2 * k, f + k > 0, first);
 }
-template <uint32_t ID, int PARTS>
+template <uint32_t ID, int PARTS, int APART>
 __device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate, uint32_t first) {
     const uint64_t db = desc_mn(b, kHalf);
 #pragma unroll 1
     for (int k = 0; k < 8 * PARTS; k += 4, accumulate = 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma_one_ts<ID>(d, a + 8 * (k + i), db + 128 * (k % 8 + i), i ? 1u : accumulate, first);
+        for (int i = 0; i < 4; ++i) mma_one_ts<ID>(d, a + APART * (k + i), db + 128 * (k % 8 + i), i ? 1u : accumulate, first);
 }
 
 template <int DA, int DC>
@@ -269,7 +274,7 @@ __device__ __forceinline__ void intra_warp(const Work& w, int lane) {
         commit_one(w.bar(B_S), first);
         if (!w.wait(B_P, m) || !w.wait(B_OSCALED, m)) break;
         tc_fence_after();
-        mma_tokens<ID_OP, 1>(w.tmem + kTmO, w.tmem + kTmS, C, 1, first);
+        mma_tokens<ID_OP, 1, 16>(w.tmem + kTmO, w.tmem + kTmS, C, 1, first);
         commit_one(w.bar(B_O), first);
         commit_one(w.bar(B_EMPTY0 + st), first);
     }
@@ -298,7 +303,7 @@ __device__ __forceinline__ void state_mma_warp(const Work& w, int lane) {
         }
         if (!w.wait(B_VD, m)) break;
         tc_fence_after();
-        mma_tokens<ID_U, 2>(w.tmem + kTmU, w.tmem + kTmHi, B, 0, first);
+        mma_tokens<ID_U, 2, 8>(w.tmem + w.u(m), w.tmem + w.cw(m), B, 0, first);
         commit_one(w.bar(B_U), first);
         commit_one(w.bar(B_EMPTY0 + st), first);
     }
@@ -308,129 +313,121 @@ __device__ __forceinline__ void state_mma_warp(const Work& w, int lane) {
     }
 }
 
-// P and the outputs: thread = row (token) of the chunk = lane of tensor memory. Sixteen columns at a time, the next ones on
-// their way from tensor memory meanwhile.
+// P and the outputs: thread = row (token) of the chunk = lane of tensor memory; of every 32 columns of P one half of the warps
+// takes the first 16 and the other the last, of the outputs' columns each takes a half. P's 16 columns (8 of tensor
+// memory, packed) replace the first 8 of the 16 of S that they come from, so that no thread writes where another one still reads.
 template <int DA, int DC, bool OUT_BF16>
 __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map, int warp, int lane) {
     const Role& r = *w.r;
-    const int row = 32 * warp + lane;
-    const uint32_t lanes = w.tmem + ((uint32_t)(32 * warp) << 16);
+    const int half = warp >> 2, quarter = warp & 3;
+    const int row = 32 * quarter + lane;
+    const uint32_t lanes = w.tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t tab = w.base + kTab;
     // The weight of row i and column j is w^|i - j|. Columns in blocks of 32: w^(31 - c) (or, backward in time, w^c) for the column
     // of a block, times what is left of the gap, one value a row and block. In the diagonal block that is w^(lane - 31) (or
     // w^-lane), which fp32 holds for heads that lose fewer than 2^100 over a block; `steep` ones take 2^(log2 w gap) as it is.
     // (Of the diagonal block only the bits of columns that the row sees stay: what lies behind it, infinities too, becomes
     // zero.)
-    pair_t col[16];
-    uint32_t seen[16];
+    pair_t col[8];
+    uint32_t seen[8];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        col[c] = pack(lds(tab + 4 * (r.rev ? 2 * c : 31 - 2 * c)), lds(tab + 4 * (r.rev ? 2 * c + 1 : 30 - 2 * c)));
-        seen[c] = ((r.rev ? 2 * c >= lane : 2 * c <= lane) ? 0xffffu : 0u) | ((r.rev ? 2 * c + 1 >= lane : 2 * c + 1 <= lane) ? 0xffff0000u : 0u);
+    for (int i = 0; i < 8; ++i) {
+        const int c = 16 * half + 2 * i;
+        col[i] = pack(lds(tab + 4 * (r.rev ? c : 31 - c)), lds(tab + 4 * (r.rev ? c + 1 : 30 - c)));
+        seen[i] = ((r.rev ? c >= lane : c <= lane) ? 0xffffu : 0u) | ((r.rev ? c + 1 >= lane : c + 1 <= lane) ? 0xffff0000u : 0u);
     }
     const bool steep = !(w.lg * 31.f > -100.f);
     const float diag = exp2f(r.rev ? -w.lg * lane : w.lg * (lane - 31));
+    const int b0 = r.rev ? quarter : 0, b1 = r.rev ? 4 : quarter + 1;   // the blocks that the row sees anything of
     for (int m = 0; m < w.chunks; ++m) {
         const int L = w.length(m);
         if (!w.wait(B_S, m)) return store_wait();
         tc_fence_after();
-        float x[2][16];
-        const int b0 = r.rev ? warp : 0, b1 = r.rev ? 4 : warp + 1;   // the blocks that the row sees anything of
-        tmem_ld16(lanes + kTmS + 32 * b0, x[0]);
-        if (!steep) {
 #pragma unroll 1
-            for (int b = b0; b < b1; ++b) {
-                const uint32_t all = b == warp ? 0u : 0xffffffffu;
-                const float f = b == warp ? diag : lds(tab + 4 * (r.rev ? 32 * (b - warp) - lane : 32 * (warp - b) + lane - 31));
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t at = lanes + kTmS + 32 * b + 16 * half;
+            uint32_t q[8];
+            if (b < b0 || b >= b1) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[i] = 0;
+            } else {
+                float x[16];
+                tmem_ld16(at, x);
+                const float f = b == quarter ? diag : lds(tab + 4 * (r.rev ? 32 * (b - quarter) - lane : 32 * (quarter - b) + lane - 31));
+                const uint32_t all = b == quarter ? 0u : 0xffffffffu;
                 const pair_t f2 = pack(f, f);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    tmem_wait_ld();
-                    if (y == 0 || b + 1 < b1) tmem_ld16(lanes + kTmS + 32 * b + 16 * (y + 1), x[1 - y]);
-                    uint32_t q[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        float lo, hi;
-                        unpack(mul2(pack(x[y][2 * c], x[y][2 * c + 1]), mul2(f2, col[8 * y + c])), lo, hi);
-                        q[c] = pack_bf16(lo, hi) & (seen[8 * y + c] | all);
-                    }
-                    tmem_st8(lanes + kTmS + 16 * b + 8 * y, q);
-                }
-            }
-        } else {
-#pragma unroll 1
-            for (int j = 32 * b0; j < 32 * b1; j += 16) {
-                uint32_t q[8];
                 tmem_wait_ld();
+                if (!steep) {
 #pragma unroll
-                for (int c = 0; c < 16; c += 2) {
-                    const int gap = r.rev ? j + c - row : row - j - c, gap1 = r.rev ? gap + 1 : gap - 1;
-                    q[c / 2] = pack_bf16(gap >= 0 ? x[0][c] * ex2(w.lg * gap) : 0.f, gap1 >= 0 ? x[0][c + 1] * ex2(w.lg * gap1) : 0.f);
+                    for (int i = 0; i < 8; ++i) {
+                        float lo, hi;
+                        unpack(mul2(pack(x[2 * i], x[2 * i + 1]), mul2(f2, col[i])), lo, hi);
+                        q[i] = pack_bf16(lo, hi) & (seen[i] | all);
+                    }
+                } else {
+                    const int gap0 = r.rev ? 32 * b + 16 * half - row : row - 32 * b - 16 * half;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int gap = r.rev ? gap0 + 2 * i : gap0 - 2 * i, gap1 = r.rev ? gap + 1 : gap - 1;
+                        q[i] = pack_bf16(gap >= 0 ? x[2 * i] * ex2(w.lg * gap) : 0.f, gap1 >= 0 ? x[2 * i + 1] * ex2(w.lg * gap1) : 0.f);
+                    }
                 }
-                if (j + 16 < 32 * b1) tmem_ld16(lanes + kTmS + j + 16, x[0]);
-                tmem_st8(lanes + kTmS + j / 2, q);
             }
+            tmem_st8(at, q);
         }
-        // (P's other blocks are zeros; where S lay under them it has been read, and P's own columns 16 b .. lie in S's
-        // first half, of which blocks 32 b .. are read before)
-        uint32_t none[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) none[c] = 0;
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b)
-            if (b < b0 || b >= b1) tmem_st16(lanes + kTmS + 16 * b, none);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(w.bar(B_P));
         if (!w.wait(B_O, m)) return store_wait();
         tc_fence_after();
-        // out through A's tile, which is done with: halves of 128 bytes by 128 rows
-        const uint32_t mine = w.base + (m & 1) * kStage + warp * 4096;
-        const int row0 = w.it.lo + kChunk * w.phys(m) + 32 * warp, rows = min(32, L - 32 * warp);
-        constexpr int kPer = OUT_BF16 ? 64 : 32, kBoxes = DC / kPer;   // features of a half
-        tmem_ld16(lanes + kTmO, x[0]);
+        // out through A's tile, which is done with: 128 rows of 128 bytes in each half of it
+        const int row0 = w.it.lo + kChunk * w.phys(m) + 32 * quarter, rows = min(32, L - 32 * quarter);
+        constexpr int kSize = OUT_BF16 ? 2 : 4, kPer = 128 / kSize;   // features of 128 bytes
+        constexpr int kMine = DC / 2;                                 // this half's columns
+        constexpr int kBoxes = kMine > kPer ? kMine / kPer : 1;       // fp32 with DC = 128: two, one after the other
+        constexpr int kSteps = kMine / kBoxes / 16;
 #pragma unroll 1
         for (int b = 0; b < kBoxes; ++b) {
-            if (!OUT_BF16 && b == 2) {   // (fp32: the first two halves have to leave before the next two)
+            const int first = kMine * half + kMine / kBoxes * b;      // column
+            // (bf16 outputs of 64 columns: both halves' in one row of 128 bytes)
+            constexpr bool kShare = OUT_BF16 && DC == 64;
+            const uint32_t box = w.base + (m & 1) * kStage + (kShare ? 0 : half * kHalf) + quarter * 4096;
+            const int piece0 = kShare ? 4 * half : 0;                 // 16-byte pieces of a row
+            if (b > 0) {   // (the first has to leave before the next)
                 store_wait();
                 __syncwarp();
             }
-            const uint32_t box = mine + (b & 1) * kHalf;
 #pragma unroll 1
-            for (int z = 0; z < kPer / 32; ++z) {
+            for (int z = 0; z < kSteps; ++z) {
+                float f[16];
+                tmem_ld16(lanes + kTmO + first + 16 * z, f);
+                tmem_wait_ld();
+                if (b == kBoxes - 1 && z == kSteps - 1) {
+                    tc_fence_before();
+                    mbar_arrive(w.bar(B_OFREE));
+                }
+                if constexpr (OUT_BF16) {
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    tmem_wait_ld();
-                    const int next = kPer * b + 32 * z + 16 * (y + 1);
-                    if (next < DC) {
-                        tmem_ld16(lanes + kTmO + next, x[1 - y]);
-                    } else {
-                        tc_fence_before();
-                        mbar_arrive(w.bar(B_OFREE));
-                    }
-                    const float (&f)[16] = x[y];
-                    if constexpr (OUT_BF16) {
+                    for (int k = 0; k < 2; ++k)
+                        sts4(box + sw128(lane, piece0 + 2 * z + k), pack_bf16(f[8 * k], f[8 * k + 1]), pack_bf16(f[8 * k + 2], f[8 * k + 3]),
+                             pack_bf16(f[8 * k + 4], f[8 * k + 5]), pack_bf16(f[8 * k + 6], f[8 * k + 7]));
+                } else {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            sts4(box + sw128(lane, 4 * z + 2 * y + k), pack_bf16(f[8 * k], f[8 * k + 1]), pack_bf16(f[8 * k + 2], f[8 * k + 3]),
-                                 pack_bf16(f[8 * k + 4], f[8 * k + 5]), pack_bf16(f[8 * k + 6], f[8 * k + 7]));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            sts4(box + sw128(lane, 4 * y + k), __float_as_uint(f[4 * k]), __float_as_uint(f[4 * k + 1]),
-                                 __float_as_uint(f[4 * k + 2]), __float_as_uint(f[4 * k + 3]));
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        sts4(box + sw128(lane, 4 * z + k), __float_as_uint(f[4 * k]), __float_as_uint(f[4 * k + 1]),
+                             __float_as_uint(f[4 * k + 2]), __float_as_uint(f[4 * k + 3]));
                 }
             }
             fence_proxy_async();
             __syncwarp();
             if (!OUT_BF16 && rows == 32) {
-                if (lane == 0) tma_store_3d(map, box, kPer * b, w.h, row0);
-            } else if (OUT_BF16 ? L < kChunk : rows < 32) {   // the sequence ends in this chunk: row by row, eight lanes each
-                constexpr int kSize = OUT_BF16 ? 2 : 4;
-                for (int i = lane >> 3; i < rows; i += 4) {
-                    const float4 v = lds4(box + sw128(i, lane & 7));
-                    char* to = (char*)r.out + (((long long)(row0 + i) * w.p->H + w.h) * DC + kPer * b) * kSize + 16 * (lane & 7);
+                if (lane == 0) tma_store_3d(map, box, first, w.h, row0);
+            } else if (OUT_BF16 ? L < kChunk : rows < 32) {   // the sequence ends in this chunk: row by row
+                constexpr int kPieces = kMine / kBoxes * kSize / 16;   // of 16 bytes in a row: 4 or 8 lanes each
+                for (int i = lane / kPieces; i < rows; i += 32 / kPieces) {
+                    const int k = lane % kPieces;
+                    const float4 v = lds4(box + sw128(i, piece0 + k));
+                    char* to = (char*)r.out + (((long long)(row0 + i) * w.p->H + w.h) * DC + first) * kSize + 16 * k;
                     *reinterpret_cast<float4*>(to) = v;
                 }
                 __syncwarp();
@@ -458,7 +455,7 @@ __device__ __forceinline__ void store_warp(const Work& w, const CUtensorMap* map
                 tma_store_3d(map, w.base + (m & 1) * kStage + b * kHalf, 64 * b, w.h, w.it.lo + kChunk * w.phys(m));
             store_wait();
         }
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 4;" ::"r"(w.bar(B_AFREE0 + (m & 1))) : "memory");
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 8;" ::"r"(w.bar(B_AFREE0 + (m & 1))) : "memory");
     }
     store_wait();
 }
@@ -478,7 +475,7 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
 #pragma unroll
     for (int i = 0; i < 64; ++i) X[i] = 0.f;
     auto slot = [&](int q) {
-        return r.slots + ((long long)(w.it.slot0 + q - 1) * w.p->H + w.h) * kState + (long long)64 * half * DC + c;
+        return w.p->slots + (w.it.slot + (long long)(q - 1) * w.it.slot_step) * kState + (long long)64 * half * DC + c;
     };
     auto given = [&](auto base) {   // of a state as the caller stores it: this thread's row 0
         const auto at = base + ((long long)w.it.seq * w.p->H + w.h) * kState;
@@ -488,15 +485,22 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
         if (w.it.piece == 0) {
             if (r.start) {
                 const float* from = given(r.start);
-                const int step = r.state_t ? 1 : DC;
+                if (r.state_t) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) X[i] = __ldg(from + i * step);
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 t = __ldg(reinterpret_cast<const float4*>(from + i));
+                        X[i] = t.x, X[i + 1] = t.y, X[i + 2] = t.z, X[i + 3] = t.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) X[i] = __ldg(from + i * DC);
+                }
             }
         } else if (!w.sums) {
             for (int q = 1; q <= w.it.piece; ++q) {
                 // entering piece q: from the state entering piece q - 1 and that piece's sum
                 const float keep = q == 1 ? 0.f
-                    : exp2f(w.lg * tokens_of(w.p->first + (q - 2) * w.p->rest, w.p->first + (q - 1) * w.p->rest, w.it.len, r.rev));
+                    : exp2f(w.lg * tokens_of(w.first + (q - 2) * w.rest, w.first + (q - 1) * w.rest, w.it.len, r.rev));
                 const float* from = slot(q);
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
@@ -526,6 +530,24 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
     const uint32_t ldm = (chan0 >> 6) * kHalf + half * 8192 + (lane >> 4) * 1024 + (lane & 7) * 128 +
                          (((((chan0 & 63) >> 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
     const int tok = 64 * half + 2 * (lane & 3);   // of its pairs in 8-token group 0
+    auto take_u = [&](int m) {   // X' = w^L X + U
+        if (!w.wait(B_U, m)) return false;
+        tc_fence_after();
+        const float keep = exp2f(w.lg * w.length(m));
+        if (64 * half < DA) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float u[32];
+                tmem_ld32(lanes + w.u(m) + 64 * half + 32 * b, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                    unpack(fma2(pack(keep, keep), pack(X[32 * b + i], X[32 * b + i + 1]), pack(u[i], u[i + 1])), X[32 * b + i],
+                           X[32 * b + i + 1]);
+            }
+        }
+        return true;
+    };
     bool zeroed = false;
     for (int m = 0; m < w.chunks; ++m) {
         const int L = w.length(m);
@@ -546,12 +568,13 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
             mbar_arrive(w.bar(B_ZERO));
             if (!w.wait(B_ZERO, 0)) return;
         }
-        // Cw = hi + lo of 64 tokens' values of 32 channels, 16 tokens and 16 channels at a time: hi is the value cut off to bf16
-        // and lo the rest of it, rounded
+        // Cw = hi + lo of 64 tokens' values of 32 channels, 16 tokens and 16 channels at a time: the value rounded to bf16,
+        // and the rest of it, rounded
         const uint32_t weights = key + 4 * (tok + (r.rev ? 0 : kChunk - L));
+        const uint32_t cw_at = w.cw(m);
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-            const uint32_t to = lanes + ((uint32_t)(16 * x) << 16) + 32 * half;
+            const uint32_t to = lanes + cw_at + ((uint32_t)(16 * x) << 16) + 32 * half;
             const uint32_t from = C + (ldm ^ 32 * x);
 #pragma unroll 1
             for (int g = 0; g < 8; g += 2) {
@@ -564,13 +587,12 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
                     const pair_t y = mul2(pack(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u)), weight[i / 2]);
                     float a, b;
                     unpack(y, a, b);
-                    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-                    hi[i] = __byte_perm(ua, ub, 0x7632);
-                    unpack(fma2(pack(__uint_as_float(ua & 0xffff0000u), __uint_as_float(ub & 0xffff0000u)), pack(-1.f, -1.f), y), a, b);
+                    hi[i] = pack_bf16(a, b);
+                    unpack(fma2(pack(__uint_as_float(hi[i] << 16), __uint_as_float(hi[i] & 0xffff0000u)), pack(-1.f, -1.f), y), a, b);
                     lo[i] = pack_bf16(a, b);
                 }
-                tmem_st_16x128b_x2(to + kTmHi + 4 * g, hi);
-                tmem_st_16x128b_x2(to + kTmLo + 4 * g, lo);
+                tmem_st_16x128b_x2(to + 4 * g, hi);
+                tmem_st_16x128b_x2(to + (kTmLo - kTmHi) + 4 * g, lo);
             }
         }
         tmem_wait_st();
@@ -595,26 +617,14 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
             tc_fence_before();
             mbar_arrive(w.bar(B_OSCALED));
         }
-        if (!w.wait(B_U, m)) return;
-        tc_fence_after();
-        const float keep = exp2f(w.lg * L);
-        if (64 * half < DA) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float u[32];
-                tmem_ld32(lanes + kTmU + 64 * half + 32 * b, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; i += 2)
-                    unpack(fma2(pack(keep, keep), pack(X[32 * b + i], X[32 * b + i + 1]), pack(u[i], u[i + 1])), X[32 * b + i],
-                           X[32 * b + i + 1]);
-            }
-        }
+        // (sums alone: U of the chunk before, while this chunk's is formed)
+        if (w.sums ? m > 0 && !take_u(m - 1) : !take_u(m)) return;
         if (!w.sums && m + 1 < w.chunks) {
             tc_fence_before();
             put_x();
         }
     }
+    if (w.sums && !take_u(w.chunks - 1)) return;
     // where the state goes: behind the last piece to the caller, behind the others' first phase to the next piece's slot
     if (!mine) return;
     if (w.it.piece == w.it.pieces - 1) {
@@ -635,13 +645,13 @@ template <int K, int V>
 __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ TcParams q) {
     extern __shared__ uint8_t smem_raw[];
     const Params& p = q.p;
-    const int role = blockIdx.y;
     if (p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
     Work w;
     w.p = &p;
+    if (!item_of(p, blockIdx.x, w.it, w.first, w.rest)) return;
+    const int role = w.it.role;
     w.r = &p.role[role];
-    w.h = blockIdx.x % p.H;
-    if (!item_of(p, blockIdx.x / p.H, w.it)) return;
+    w.h = w.it.h;
     w.sums = p.phase == 1 && w.it.piece > 0;
     w.chunks = w.it.m1 - w.it.m0;
     w.n = (w.it.len + kChunk - 1) / kChunk;
@@ -653,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < B_N; ++i)
-            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? 4 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT || i == B_OFREE ? 128 : i == B_OSCALED || i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
+            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? kOutThreads / 32 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT || i == B_OFREE ? kOutThreads : i == B_OSCALED || i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
         *w.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
@@ -673,10 +683,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     tc_fence_after();
     w.tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const bool turned = K != V && w.r->state_t;   // dA = V, dC = K
-    // The launch's 128 registers a thread, dealt anew: 128 x 144 + 256 x 152 + 128 x 64 = 512 x 128. (At 128 the
-    // state's warps spill, and the stack is in L2.)
-    if (warp < 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+    // The launch's 96 registers a thread, dealt anew: 256 x 64 + 256 x 144 + 128 x 64 = 640 x 96. (At 96 the state's warps
+    // spill, and the stack is in L2.)
+    if (warp < kStateWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
         const bool bf16 = w.r->out_bf16;
         const CUtensorMap* map = &q.out[role];
         if (w.sums) {
@@ -687,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         }
     } else if (warp < kLoadWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
-        turned ? state_warps<V, K>(w, warp - 4, lane) : state_warps<K, V>(w, warp - 4, lane);
+        turned ? state_warps<V, K>(w, warp - kStateWarp0, lane) : state_warps<K, V>(w, warp - kStateWarp0, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
         if (lane == 0 && warp == kLoadWarp)
@@ -726,7 +736,7 @@ cudaError_t launch(const TcParams& q, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(tc_kernel<K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((long long)q.p.entries * q.p.H), (unsigned)q.p.nroles);
+    cfg.gridDim = dim3((unsigned)q.p.blocks);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
