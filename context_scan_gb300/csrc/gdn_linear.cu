@@ -12,15 +12,15 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr unsigned kTagLengths = 0x51;
 // How chains are cut into pieces. `room`: pieces that the GPU runs at once. A chain of n chunks cut into piece 0 of `first` and
-// others of `rest` takes first + rest chunks' time instead of n (a sum over a piece takes about 0.4 of a forward's time,
-// so that first = 0.4 rest ends with the sums), and a second launch, which is worth kSaved chunks.
+// others of `rest` takes first + rest chunks' time instead of n (a sum over a piece takes about half of a forward's time,
+// so that first = rest / 2 ends with the sums), and a second launch, which is worth kSaved chunks.
 constexpr int kSaved = 3;
 struct Cut {
     int whole = INT_MAX;         // chains that are not cut come first
     int first = 0, rest = 0, pieces = 1;
     long long blocks2 = 0;       // of phase 2, which has as many pieces as phase 1 has piece 0s and sums of cut chains
 };
-__host__ __device__ inline int first_of(int rest) { return (2 * rest + 4) / 5; }
+__host__ __device__ inline int first_of(int rest) { return (rest + 1) / 2; }
 
 // Chains of n chunks each: as many as fill the GPU whole rounds run in one piece, the others are cut so that they fill it too.
 Cut cut_even(long long T, long long chains, long long room) {
@@ -29,7 +29,7 @@ Cut cut_even(long long T, long long chains, long long room) {
     if (left == 0) return c;
     const long long more = std::min(room / left, n);       // pieces behind the first one
     if (more < 2) return c;
-    const long long rest = (5 * n + 5 * more + 1) / (5 * more + 2);   // n / (more + 0.4), rounded up
+    const long long rest = (2 * n + 2 * more) / (2 * more + 1);   // n / (more + 1/2), rounded up
     long long first = n - more * rest;
     if (first < 1) first = first_of((int)rest);
     if (first + rest + kSaved > n) return c;
@@ -49,19 +49,29 @@ __device__ __forceinline__ int more_pieces(int n, int first, int rest) { return 
 
 // Checks the lengths of a packed batch and makes the phases' entries: every sequence's piece 0, then the middle pieces;
 // the pieces from 1 on. Bad lengths are recorded and leave no entries, so that nothing is written. The cut: the
-// shortest `rest` with which at most `room` pieces lie behind first ones, where that takes less time than the longest
-// sequence by itself; every warp tries one.
+// shortest `rest` with which at most `room` pieces lie behind first ones (every warp tries one), where that takes less time
+// than no cut. Times in chunks: the longest piece, or, where there are more pieces than room, an even share of all and half of
+// the longest. Longer sequences come first.
+__device__ __forceinline__ long long warp_total(long long x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
 __global__ void __launch_bounds__(kPlanThreads)
     plan_kernel(const int* cu, int nseq, int T, int room, int* words, int4* table1, int4* table2, DeviceError* err) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int warp_sum[32], warp_max[32];
+    __shared__ long long warp_time[32];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     bool bad = t == 0 && (cu[0] != 0 || cu[nseq] > T);
     int longest = 0;
+    long long all = 0;
     for (int s = t; s < nseq; s += kPlanThreads) {
         const int a = cu[s], b = cu[s + 1];
         bad |= b < a;
-        longest = max(longest, (int)(((long long)b - a + kChunk - 1) / kChunk));
+        const int n = (int)(((long long)b - a + kChunk - 1) / kChunk);
+        longest = max(longest, n);
+        all += n;
     }
     if (__syncthreads_or(bad)) {
         if (t == 0) {
@@ -74,28 +84,41 @@ __global__ void __launch_bounds__(kPlanThreads)
     int first = 0, rest = 0;
     if (room > 0) {
         longest = __reduce_max_sync(0xffffffffu, longest);
-        if (lane == 0) warp_max[warp] = longest;
+        all = warp_total(all);
+        if (lane == 0) {
+            warp_max[warp] = longest;
+            warp_time[warp] = all;
+        }
         __syncthreads();
         longest = __reduce_max_sync(0xffffffffu, warp_max[lane]);
+        all = warp_total(warp_time[lane]);
+        const long long uncut = nseq > room ? max((long long)longest, all / room + longest / 2) : longest;
         // lengths worth trying: from what an even cut of all chunks would give on, in steps of a sixteenth of it
         const int even = max(1, (int)(((long long)cu[nseq] / kChunk) / (room + nseq))), step = (even + 15) / 16;
         for (int r0 = even; r0 + first_of(r0) + kSaved <= longest; r0 += 32 * step) {
             const int r = r0 + warp * step, f = first_of(r);
-            long long count = 0;
-            for (int s = lane; s < nseq; s += 32) count += more_pieces(chunks(s), f, r);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) count += __shfl_xor_sync(0xffffffffu, count, off);
+            long long count = 0, work = 0;   // pieces behind first ones; chunks of phase 1 (sums by half)
+            for (int s = lane; s < nseq; s += 32) {
+                const int n = chunks(s), more = more_pieces(n, f, r);
+                count += more;
+                work += more ? f + (more - 1) * r / 2 : n;
+            }
+            count = warp_total(count);
+            work = warp_total(work);
+            const long long phase1 = nseq + count > room + room / 4 ? max((long long)f, work / room + f / 2) : f + 1;
             __syncthreads();
-            if (lane == 0) warp_sum[warp] = count <= room;
+            if (lane == 0) {
+                warp_sum[warp] = count <= room;
+                warp_time[warp] = phase1 + r + kSaved;
+            }
             __syncthreads();
             const unsigned fit = __ballot_sync(0xffffffffu, warp_sum[lane]);
             if (fit) {
-                rest = r0 + (__ffs(fit) - 1) * step;
+                if (warp_time[__ffs(fit) - 1] <= uncut) rest = r0 + (__ffs(fit) - 1) * step;
                 first = first_of(rest);
                 break;
             }
         }
-        if (first + rest + kSaved > longest) rest = 0;
     }
     __syncthreads();
     int before = 0;   // pieces behind the first ones of all sequences before this round's
@@ -122,7 +145,13 @@ __global__ void __launch_bounds__(kPlanThreads)
         __syncthreads();
         const int slot0 = before + sum - (pieces - 1) + (warp ? warp_sum[warp - 1] : 0);
         if (s < nseq) {
-            table1[s] = make_int4(s, 0, pieces, slot0);
+            int place = s;   // in the order of falling length
+            if (nseq <= kPlanThreads) {
+                const int n = chunks(s);
+                place = 0;
+                for (int j = 0; j < nseq; ++j) place += chunks(j) > n || (chunks(j) == n && j < s);
+            }
+            table1[place] = make_int4(s, 0, pieces, slot0);
             for (int q = 1; q < pieces; ++q) {
                 table2[slot0 + q - 1] = make_int4(s, q, pieces, slot0);
                 // (the last piece's place among the sums stays empty: sequence -1)
