@@ -7,11 +7,13 @@
 // by -t:   dw = sum over rows of e x s,   d = e w,   dx = s (d - x s mean(d x s)).
 //
 // Bound by memory: x (and dy) read once, y (dx) written once. A row is a few hundred bytes, so a group of
-// up to 32 lanes takes one token and walks over its heads: the angles' sines and cosines are formed once for them all and stay
-// in registers with the weights. A lane holds both members of its pairs, so that the rotation crosses no lanes.
+// up to 32 lanes takes one token and walks over some of its heads: the angles' sines and cosines are formed once for them all
+// and stay in registers with the weights. A lane holds both members of its pairs, so that the rotation crosses no lanes. A
+// block works on the queries or on the keys (so that it holds one set of weights and, backward, one of their sums), and
+// a group reads its next head's row while it works on one.
 //
 // Angles. n freq is wanted modulo a turn; in fp32 it would be off by n 2^-24. freq / 2 pi is turned into a
-// 64-bit fraction of a turn (one fp64 product per pair of a group); n times that, wrapping as integers do, is the angle
+// 64-bit fraction of a turn (one fp64 product per pair and block); n times that, wrapping as integers do, is the angle
 // modulo a turn to n 2^-53 of it.
 #include <algorithm>
 #include <atomic>
@@ -29,17 +31,22 @@ constexpr int kThreads = 256;
 constexpr int kDevices = 64;
 constexpr int kMaxBlocks = 1024;   // of the backward: rows of partial sums in the workspace
 
+struct Side {                // the queries, or the keys
+    const void* x;
+    const void* dy;
+    void* y;                 // forward: y; backward: dx
+    const float* w;          // null: ones
+    long long x_stride, y_stride, dy_stride;   // values from one token to the next
+    long long groups;        // groups of lanes with work: tokens x parts
+    int H, parts, per;       // a token's heads in `parts` of `per` each
+};
 struct QkParams {
-    const void* x[2];        // q, k
-    const void* dy[2];
-    void* y[2];              // forward: y; backward: dx
-    const float* w[2];       // null: ones
+    Side side[2];
     const float* freq;
     const int* pos;          // null: the token's place in its sequence
-    float* partial;          // backward: [blocks][2][K]
-    long long tokens, x_stride[2], y_stride[2], dy_stride[2];   // values from one token to the next
-    long long groups;        // groups of lanes with work: tokens x parts
-    int T, H[2], K, R, interleaved, G, parts, per;              // a token's heads in `parts` of `per` each
+    float* partial;          // backward: [blocks][K] sums
+    int blocks0;             // the first blocks are the queries'
+    int T, K, R, interleaved, G;
     float eps, inv_k;
 };
 
@@ -148,29 +155,28 @@ __device__ __forceinline__ void put(float (&a)[VEC], float (&b)[VEC], int e, boo
     (i + 1 < VEC ? a[(i + 1) % VEC] : b[(i + 1) % VEC]) = y;
 }
 
-// cosines and sines of a lane's pairs at position n (1 and 0 for channels that are not rotated)
-template <int VEC, int UPL, bool IL>
-__device__ __forceinline__ void turns(const QkParams& p, const Units<VEC, UPL>& un, const unsigned long long (&step)[UPL][VEC],
-                                      int n, float (&c)[UPL][VEC], float (&s)[UPL][VEC]) {
-#pragma unroll
-    for (int i = 0; i < UPL; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const unsigned long long a = (unsigned long long)(long long)n * step[i][e];
-            sincospif((float)(int)(a >> 32) * 0x1p-31f, &s[i][e], &c[i][e]);
+// Every rotated pair's turn from one position to the next, as a 64-bit fraction, in shared memory (zeros for pairs
+// that are not rotated).
+__device__ __forceinline__ void make_steps(const QkParams& p, unsigned long long* step) {
+    for (int i = threadIdx.x; i < kMaxK / 2; i += kThreads) {
+        step[i] = 0;
+        if (i < p.R / 2) {
+            const double f = (double)__ldg(p.freq + i) * 0.15915494309189533577;   // 1 / 2 pi
+            step[i] = __double2ull_rd((f - floor(f)) * 0x1p64);
         }
+    }
+    __syncthreads();
 }
+// cosines and sines of a lane's pairs at position n (1 and 0 for channels that are not rotated)
 template <int VEC, int UPL>
-__device__ __forceinline__ void steps(const QkParams& p, const Units<VEC, UPL>& un, unsigned long long (&step)[UPL][VEC]) {
+__device__ __forceinline__ void turns(const Units<VEC, UPL>& un, const unsigned long long* step, int n, float (&c)[UPL][VEC],
+                                      float (&s)[UPL][VEC]) {
 #pragma unroll
     for (int i = 0; i < UPL; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            step[i][e] = 0;
-            if (un.has(i) && un.turned(i)) {
-                const double f = (double)__ldg(p.freq + un.pair0(i) + e) * 0.15915494309189533577;   // 1 / 2 pi
-                step[i][e] = __double2ull_rd((f - floor(f)) * 0x1p64);
-            }
+            const unsigned long long a = un.has(i) ? (unsigned long long)(long long)n * step[un.pair0(i) + e] : 0;
+            sincospif((float)(int)(a >> 32) * 0x1p-31f, &s[i][e], &c[i][e]);
         }
 }
 
@@ -179,195 +185,213 @@ __device__ __forceinline__ float group_sum(float x, int G) {
     return x;
 }
 
-template <int VEC, int UPL, bool XB, bool YB, bool IL>
-__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkParams p) {
-    const int G = p.G, lane = threadIdx.x % G;
-    const Units<VEC, UPL> un(p, lane);
-    const long long group = ((long long)blockIdx.x * kThreads + threadIdx.x) / G;
-    // (a whole warp leaves together or stays: groups without work take part in the exchanges)
-    const bool live = group < p.groups;
-    const long long token = live ? group / p.parts : 0;
-    const int part = live ? (int)(group - token * p.parts) : 0;
-    const int h_end = live ? min(p.H[0] + p.H[1], (part + 1) * p.per) : 0;
-    unsigned long long step[UPL][VEC];
-    float c[UPL][VEC], s[UPL][VEC];
-    steps(p, un, step);
-    turns<VEC, UPL, IL>(p, un, step, p.pos ? (live ? __ldg(p.pos + token) : 0) : (int)(token % p.T), c, s);
-    int h = part * p.per;
-#pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
-        const int h0 = side ? p.H[0] : 0, hn = min(h_end, h0 + p.H[side]);
-        if (!__any_sync(0xffffffffu, h < hn)) continue;
-        const long long xb = token * p.x_stride[side], yb = token * p.y_stride[side];
-        float wa[UPL][VEC], wb[UPL][VEC];
+// The work of a group in one round: a token's heads h0 .. h1 - 1 (none: h0 == h1).
+struct Work {
+    long long token;
+    int h0, h1;
+    __device__ __forceinline__ Work(const Side& s, long long group) {
+        token = 0;
+        h0 = h1 = 0;
+        if (group < s.groups) {
+            token = s.parts == 1 ? group : group / s.parts;
+            h0 = (int)(group - token * s.parts) * s.per;
+            h1 = min(s.H, h0 + s.per);
+        }
+    }
+};
+
+template <int VEC, int UPL, bool BF>
+struct Row {   // a head's values that a lane holds
+    Raw<VEC, BF> a[UPL], b[UPL];
+    __device__ __forceinline__ void load(const Units<VEC, UPL>& un, const void* base, long long at, bool on) {
 #pragma unroll
         for (int i = 0; i < UPL; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                wa[i][e] = wb[i][e] = 1.f;
-                if (un.has(i) && p.w[side]) {
-                    wa[i][e] = __ldg(p.w[side] + un.first(i) + e);
-                    wb[i][e] = __ldg(p.w[side] + un.second(i) + e);
-                }
+            if (on && un.has(i)) {
+                a[i].load(base, at + un.first(i));
+                b[i].load(base, at + un.second(i));
             }
-        // two heads at a time: the second one's loads are under way while the first is worked on
-        Raw<VEC, XB> a[2][UPL], b[2][UPL];
-        auto fetch = [&](int k, int hh) {
+    }
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-            for (int i = 0; i < UPL; ++i) {
-                a[k][i].zero();
-                b[k][i].zero();
-                if (un.has(i) && hh < hn) {
-                    a[k][i].load(p.x[side], xb + (long long)(hh - h0) * p.K + un.first(i));
-                    b[k][i].load(p.x[side], xb + (long long)(hh - h0) * p.K + un.second(i));
-                }
+        for (int i = 0; i < UPL; ++i) {
+            a[i].zero();
+            b[i].zero();
+        }
+    }
+};
+
+template <int VEC, int UPL, bool XB, bool YB, bool IL>
+__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant__ QkParams p) {
+    __shared__ unsigned long long step[kMaxK / 2];
+    make_steps(p, step);
+    const bool keys = (int)blockIdx.x >= p.blocks0;
+    const Side& s = p.side[keys];
+    const int block = keys ? blockIdx.x - p.blocks0 : blockIdx.x, blocks = keys ? gridDim.x - p.blocks0 : p.blocks0;
+    const int G = p.G;
+    const Units<VEC, UPL> un(p, threadIdx.x % G);
+    const int rows = kThreads / G, mine = threadIdx.x / G;
+    float wa[UPL][VEC], wb[UPL][VEC];
+#pragma unroll
+    for (int i = 0; i < UPL; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            wa[i][e] = wb[i][e] = 1.f;
+            if (un.has(i) && s.w) {
+                wa[i][e] = __ldg(s.w + un.first(i) + e);
+                wb[i][e] = __ldg(s.w + un.second(i) + e);
             }
-        };
-        fetch(0, h);
-        while (__any_sync(0xffffffffu, h < hn)) {
+        }
+    // (a warp's groups take part in its exchanges whether or not they have work)
+    for (long long g0 = (long long)block * rows; g0 < s.groups; g0 += (long long)blocks * rows) {
+        const Work wk(s, g0 + mine);
+        Row<VEC, UPL, XB> row[2];
+        row[0].zero();
+        row[1].zero();
+        long long xat = wk.token * s.x_stride + (long long)wk.h0 * p.K, yat = wk.token * s.y_stride + (long long)wk.h0 * p.K;
+        row[0].load(un, s.x, xat, wk.h0 < wk.h1);
+        float c[UPL][VEC], sn[UPL][VEC];
+        turns<VEC, UPL>(un, step, p.pos ? (wk.h0 < wk.h1 ? __ldg(p.pos + wk.token) : 0) : (int)(wk.token % p.T), c, sn);
+        for (int h = wk.h0; __any_sync(0xffffffffu, h < wk.h1); h += 2) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                fetch(k ^ 1, h + 1);
+                row[k ^ 1].load(un, s.x, xat + p.K, h + k + 1 < wk.h1);
                 float sq = 0.f;
 #pragma unroll
                 for (int i = 0; i < UPL; ++i)
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        sq = fmaf(a[k][i].at(e), a[k][i].at(e), sq);
-                        sq = fmaf(b[k][i].at(e), b[k][i].at(e), sq);
+                        sq = fmaf(row[k].a[i].at(e), row[k].a[i].at(e), sq);
+                        sq = fmaf(row[k].b[i].at(e), row[k].b[i].at(e), sq);
                     }
                 const float rstd = rsqrtf(fmaf(group_sum(sq, G), p.inv_k, p.eps));
 #pragma unroll
                 for (int i = 0; i < UPL; ++i) {
-                    float ya[VEC], yb_[VEC], va[VEC], vb[VEC];
+                    float va[VEC], vb[VEC];
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        va[e] = a[k][i].at(e) * rstd * wa[i][e];
-                        vb[e] = b[k][i].at(e) * rstd * wb[i][e];
+                        va[e] = row[k].a[i].at(e) * rstd * wa[i][e];
+                        vb[e] = row[k].b[i].at(e) * rstd * wb[i][e];
                     }
-                    const bool on = un.turned(i);
+                    if (un.turned(i)) {
+                        float ya[VEC], yb[VEC];
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        float x, y;
-                        members(va, vb, e, IL, x, y);
-                        put(ya, yb_, e, IL, x * c[i][e] - y * s[i][e], y * c[i][e] + x * s[i][e]);
+                        for (int e = 0; e < VEC; ++e) {
+                            float x, y;
+                            members(va, vb, e, IL, x, y);
+                            put(ya, yb, e, IL, x * c[i][e] - y * sn[i][e], y * c[i][e] + x * sn[i][e]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) va[e] = ya[e], vb[e] = yb[e];
                     }
-                    if (un.has(i) && h < hn) {
-                        const long long at = yb + (long long)(h - h0) * p.K;
-                        store<VEC, YB>(p.y[side], at + un.first(i), on ? ya : va);
-                        store<VEC, YB>(p.y[side], at + un.second(i), on ? yb_ : vb);
+                    if (un.has(i) && h + k < wk.h1) {
+                        store<VEC, YB>(s.y, yat + un.first(i), va);
+                        store<VEC, YB>(s.y, yat + un.second(i), vb);
                     }
                 }
-                h = h < hn ? h + 1 : h;
+                xat += p.K;
+                yat += p.K;
             }
         }
     }
 }
 
-// The gradients. Groups walk over (token, part) items in a fixed order; dw of their rows stays in registers, is joined in
+// The gradients. Groups walk over their work in a fixed order; dw of their rows stays in registers, is joined in
 // shared memory at the end and goes to the workspace, one row of sums a block; qk_sum_kernel adds those up in order.
+// (Two blocks an SM: at one, with two rows on their way in each group, memory waits for the lanes.)
 template <int VEC, int UPL, bool XB, bool YB, bool IL>
-__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const __grid_constant__ QkParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ float sums[2][kMaxK];
-    const int G = p.G, lane = threadIdx.x % G;
-    const Units<VEC, UPL> un(p, lane);
-    const int mine = threadIdx.x / G, rows = kThreads / G;
-    unsigned long long step[UPL][VEC];
-    steps(p, un, step);
-    float w[2][2][UPL][VEC], dw[2][2][UPL][VEC];
+    __shared__ unsigned long long step[kMaxK / 2];
+    __shared__ float sums[kMaxK];
+    make_steps(p, step);
+    const bool keys = (int)blockIdx.x >= p.blocks0;
+    const Side& s = p.side[keys];
+    const int block = keys ? blockIdx.x - p.blocks0 : blockIdx.x, blocks = keys ? gridDim.x - p.blocks0 : p.blocks0;
+    const int G = p.G;
+    const Units<VEC, UPL> un(p, threadIdx.x % G);
+    const int rows = kThreads / G, mine = threadIdx.x / G;
+    float w[2][UPL][VEC], dw[2][UPL][VEC];
 #pragma unroll
-    for (int side = 0; side < 2; ++side)
+    for (int i = 0; i < UPL; ++i)
 #pragma unroll
-        for (int i = 0; i < UPL; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                w[side][0][i][e] = w[side][1][i][e] = 1.f;
-                dw[side][0][i][e] = dw[side][1][i][e] = 0.f;
-                if (un.has(i) && p.w[side]) {
-                    w[side][0][i][e] = __ldg(p.w[side] + un.first(i) + e);
-                    w[side][1][i][e] = __ldg(p.w[side] + un.second(i) + e);
-                }
+        for (int e = 0; e < VEC; ++e) {
+            w[0][i][e] = w[1][i][e] = 1.f;
+            dw[0][i][e] = dw[1][i][e] = 0.f;
+            if (un.has(i) && s.w) {
+                w[0][i][e] = __ldg(s.w + un.first(i) + e);
+                w[1][i][e] = __ldg(s.w + un.second(i) + e);
             }
-    const long long stride = (long long)gridDim.x * rows;
-    for (long long g0 = (long long)blockIdx.x * rows; g0 < p.groups; g0 += stride) {
-        const long long group = g0 + mine;
-        const bool live = group < p.groups;
-        const long long token = live ? group / p.parts : 0;
-        const int part = live ? (int)(group - token * p.parts) : 0;
-        const int h_end = live ? min(p.H[0] + p.H[1], (part + 1) * p.per) : 0;
-        float c[UPL][VEC], s[UPL][VEC];
-        turns<VEC, UPL, IL>(p, un, step, p.pos ? (live ? __ldg(p.pos + token) : 0) : (int)(token % p.T), c, s);
-        int h = part * p.per;
+        }
+    for (long long g0 = (long long)block * rows; g0 < s.groups; g0 += (long long)blocks * rows) {
+        const Work wk(s, g0 + mine);
+        Row<VEC, UPL, XB> row[2];
+        Row<VEC, UPL, YB> grad[2];
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int h0 = side ? p.H[0] : 0, hn = min(h_end, h0 + p.H[side]);
-            const long long xb = token * p.x_stride[side], db = token * p.dy_stride[side], yb = token * p.y_stride[side];
-#pragma unroll 1
-            while (__any_sync(0xffffffffu, h < hn)) {
-                Raw<VEC, XB> a[UPL], b[UPL];
-                Raw<VEC, YB> da[UPL], db_[UPL];
+        for (int k = 0; k < 2; ++k) {
+            row[k].zero();
+            grad[k].zero();
+        }
+        const long long first = (long long)wk.h0 * p.K;
+        long long xat = wk.token * s.x_stride + first, dat = wk.token * s.dy_stride + first, yat = wk.token * s.y_stride + first;
+        row[0].load(un, s.x, xat, wk.h0 < wk.h1);
+        grad[0].load(un, s.dy, dat, wk.h0 < wk.h1);
+        float c[UPL][VEC], sn[UPL][VEC];
+        turns<VEC, UPL>(un, step, p.pos ? (wk.h0 < wk.h1 ? __ldg(p.pos + wk.token) : 0) : (int)(wk.token % p.T), c, sn);
+        for (int h = wk.h0; __any_sync(0xffffffffu, h < wk.h1); h += 2) {
 #pragma unroll
-                for (int i = 0; i < UPL; ++i) {
-                    a[i].zero();
-                    b[i].zero();
-                    da[i].zero();
-                    db_[i].zero();
-                    if (un.has(i) && h < hn) {
-                        const long long at = xb + (long long)(h - h0) * p.K, dat = db + (long long)(h - h0) * p.K;
-                        a[i].load(p.x[side], at + un.first(i));
-                        b[i].load(p.x[side], at + un.second(i));
-                        da[i].load(p.dy[side], dat + un.first(i));
-                        db_[i].load(p.dy[side], dat + un.second(i));
-                    }
-                }
-                float ea[UPL][VEC], eb[UPL][VEC];
-                float sq = 0.f, dot = 0.f;
+            for (int k = 0; k < 2; ++k) {
+                row[k ^ 1].load(un, s.x, xat + p.K, h + k + 1 < wk.h1);
+                grad[k ^ 1].load(un, s.dy, dat + p.K, h + k + 1 < wk.h1);
+                const bool on = h + k < wk.h1;
+                float sq = 0.f, dot = 0.f, ea[UPL][VEC], eb[UPL][VEC];   // e: dy turned back
 #pragma unroll
                 for (int i = 0; i < UPL; ++i) {
                     float va[VEC], vb[VEC];
-                    const bool on = un.turned(i);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        va[e] = ea[i][e] = da[i].at(e);
-                        vb[e] = eb[i][e] = db_[i].at(e);
+                        va[e] = ea[i][e] = grad[k].a[i].at(e);
+                        vb[e] = eb[i][e] = grad[k].b[i].at(e);
                     }
-                    if (on) {
+                    if (un.turned(i)) {
 #pragma unroll
                         for (int e = 0; e < VEC; ++e) {
                             float x, y;
                             members(va, vb, e, IL, x, y);
-                            put(ea[i], eb[i], e, IL, x * c[i][e] + y * s[i][e], y * c[i][e] - x * s[i][e]);
+                            put(ea[i], eb[i], e, IL, x * c[i][e] + y * sn[i][e], y * c[i][e] - x * sn[i][e]);
                         }
                     }
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        sq = fmaf(a[i].at(e), a[i].at(e), sq);
-                        sq = fmaf(b[i].at(e), b[i].at(e), sq);
-                        dot = fmaf(ea[i][e] * w[side][0][i][e], a[i].at(e), dot);
-                        dot = fmaf(eb[i][e] * w[side][1][i][e], b[i].at(e), dot);
+                        const float xa = row[k].a[i].at(e), xb = row[k].b[i].at(e);
+                        sq = fmaf(xa, xa, sq);
+                        sq = fmaf(xb, xb, sq);
+                        dot = fmaf(ea[i][e] * w[0][i][e], xa, dot);
+                        dot = fmaf(eb[i][e] * w[1][i][e], xb, dot);
                     }
                 }
                 const float rstd = rsqrtf(fmaf(group_sum(sq, G), p.inv_k, p.eps));
-                const float mean = group_sum(dot, G) * p.inv_k * rstd;   // of d u
+                // (a row that there is none of any more was this group's last but one: its sums stay out)
+                const float scale = on ? rstd : 0.f;
+                const float mean = group_sum(dot, G) * p.inv_k * rstd * rstd;   // of d u, times another s for u
 #pragma unroll
                 for (int i = 0; i < UPL; ++i) {
-                    float xa[VEC], xb_[VEC];
+                    float da[VEC], db[VEC];
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        const float ua = a[i].at(e) * rstd, ub = b[i].at(e) * rstd;
-                        dw[side][0][i][e] = fmaf(ea[i][e], ua, dw[side][0][i][e]);
-                        dw[side][1][i][e] = fmaf(eb[i][e], ub, dw[side][1][i][e]);
-                        xa[e] = rstd * fmaf(-ua, mean, ea[i][e] * w[side][0][i][e]);
-                        xb_[e] = rstd * fmaf(-ub, mean, eb[i][e] * w[side][1][i][e]);
+                        const float xa = row[k].a[i].at(e), xb = row[k].b[i].at(e);
+                        dw[0][i][e] = fmaf(ea[i][e], on ? xa * scale : 0.f, dw[0][i][e]);
+                        dw[1][i][e] = fmaf(eb[i][e], on ? xb * scale : 0.f, dw[1][i][e]);
+                        da[e] = rstd * fmaf(-xa, mean, ea[i][e] * w[0][i][e]);
+                        db[e] = rstd * fmaf(-xb, mean, eb[i][e] * w[1][i][e]);
                     }
-                    if (un.has(i) && h < hn) {
-                        const long long at = yb + (long long)(h - h0) * p.K;
-                        store<VEC, XB>(p.y[side], at + un.first(i), xa);
-                        store<VEC, XB>(p.y[side], at + un.second(i), xb_);
+                    if (un.has(i) && on) {
+                        store<VEC, XB>(s.y, yat + un.first(i), da);
+                        store<VEC, XB>(s.y, yat + un.second(i), db);
                     }
                 }
-                h = h < hn ? h + 1 : h;
+                xat += p.K;
+                dat += p.K;
+                yat += p.K;
             }
         }
     }
@@ -376,43 +400,42 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkParams p) {
     for (int w0 = 0; w0 < kThreads / 32; ++w0) {
         if (threadIdx.x / 32 == w0) {
 #pragma unroll
-            for (int side = 0; side < 2; ++side)
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                for (int i = 0; i < UPL; ++i)
 #pragma unroll
-                    for (int i = 0; i < UPL; ++i)
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            float t = dw[side][half][i][e];
-                            for (int off = 16; off >= G; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-                            if ((threadIdx.x & 31) < G && un.has(i)) {
-                                float* to = &sums[side][(half ? un.second(i) : un.first(i)) + e];
-                                *to = w0 ? *to + t : t;
-                            }
+                    for (int e = 0; e < VEC; ++e) {
+                        float t = dw[half][i][e];
+                        for (int off = 16; off >= G; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+                        if ((threadIdx.x & 31) < G && un.has(i)) {
+                            float* to = &sums[(half ? un.second(i) : un.first(i)) + e];
+                            *to = w0 ? *to + t : t;
                         }
+                    }
         }
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < 2 * p.K; i += kThreads)
-        p.partial[(long long)blockIdx.x * 2 * p.K + i] = sums[i / p.K][i % p.K];
+    for (int i = threadIdx.x; i < p.K; i += kThreads) p.partial[(long long)blockIdx.x * p.K + i] = sums[i];
 }
 
-// dw[side][i] = the sum over the blocks' rows: a block of 256 threads for 8 columns, 32 partial sums each
-__global__ void __launch_bounds__(kThreads) qk_sum_kernel(const float* partial, int blocks, int K, float* dwq, float* dwk) {
+// dw[i] = the sum over the blocks' rows, of the queries' (blockIdx.y 0) or the keys' blocks: a block of 256 threads for 8
+// columns, 32 partial sums each
+__global__ void __launch_bounds__(kThreads) qk_sum_kernel(const float* partial, int blocks0, int blocks, int K, float* dwq, float* dwk) {
     __shared__ float part[32][9];
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    float* to = blockIdx.y ? dwk : dwq;
+    if (!to) return;
     const int col = threadIdx.x % 8, row = threadIdx.x / 8, i = blockIdx.x * 8 + col;
     float t = 0.f;
-    if (i < 2 * K)
-        for (int b = row; b < blocks; b += 32) t += __ldcg(partial + (long long)b * 2 * K + i);
+    if (i < K)
+        for (int b = (blockIdx.y ? blocks0 : 0) + row; b < (blockIdx.y ? blocks : blocks0); b += 32) t += __ldcg(partial + (long long)b * K + i);
     part[row][col] = t;
     __syncthreads();
-    if (threadIdx.x < 8 && i < 2 * K) {
+    if (threadIdx.x < 8 && i < K) {
         float total = 0.f;
 #pragma unroll
         for (int r = 0; r < 32; ++r) total += part[r][threadIdx.x];
-        float* to = i < K ? dwq : dwk;
-        if (to) to[i % K] = total;
+        to[i] = total;
     }
 }
 
@@ -451,11 +474,12 @@ bool off_type(const void* ptr, int dtype) {
     return reinterpret_cast<uintptr_t>(ptr) % (dtype == GDN_DTYPE_BF16 ? 2 : 4) != 0;
 }
 
-void fill(QkParams& c, const gdn_qk_problem& p, int vec) {
-    c.tokens = (long long)p.B * p.T;
-    c.T = p.T;
-    c.H[0] = p.Hq;
-    c.H[1] = p.Hk;
+// The sizes, and how tokens' heads are dealt to groups and blocks: `resident` blocks in all, to queries and keys by their heads,
+// that go round their work four times or more (so that the last round weighs little) where there is that much; a token's heads
+// whole where its tokens alone give that, else in parts of four heads at least, down to single ones where lanes would
+// have no work at all (each part forms the angles again).
+int fill(QkParams& c, const gdn_qk_problem& p, int vec, int resident) {
+    c.T = std::max(p.T, 1);
     c.K = p.K;
     c.R = p.R;
     c.interleaved = p.interleaved;
@@ -463,35 +487,64 @@ void fill(QkParams& c, const gdn_qk_problem& p, int vec) {
     c.inv_k = 1.f / p.K;
     c.G = 1;
     while (c.G < 32 && c.G < p.K / (2 * vec)) c.G *= 2;
+    const long long tokens = (long long)p.B * p.T, rows = kThreads / c.G;
+    int blocks[2];
+    for (int i = 0; i < 2; ++i) {
+        Side& s = c.side[i];
+        s.H = i ? p.Hk : p.Hq;
+        const long long share = std::max(1LL, (long long)resident * s.H / (p.Hq + p.Hk));   // blocks
+        const long long round = share * rows, want = tokens > 0 ? (4 * round + tokens - 1) / tokens : 1;
+        long long parts = std::min<long long>(want, (s.H + 3) / 4);
+        if (tokens * parts < round) parts = std::min<long long>(s.H, (round + tokens - 1) / std::max(1LL, tokens));
+        parts = std::max(1LL, parts);
+        s.per = (int)((s.H + parts - 1) / parts);
+        s.parts = (s.H + s.per - 1) / s.per;
+        s.groups = tokens * s.parts;
+        blocks[i] = (int)std::max(1LL, std::min(share, (s.groups + rows - 1) / rows));
+    }
+    c.blocks0 = blocks[0];
+    return blocks[0] + blocks[1];
 }
 
-// A token's heads in parts: whole where the tokens alone give every SM its warps; else so many that they do (each
-// part forms the angles again).
-void split(QkParams& c, long long lanes_wanted) {
-    const int heads = c.H[0] + c.H[1];
-    const long long want = std::max(1LL, lanes_wanted / std::max(1LL, c.tokens * c.G));
-    c.parts = (int)std::min<long long>(heads, want);
-    c.per = (heads + c.parts - 1) / c.parts;
-    c.parts = (heads + c.per - 1) / c.per;
-    c.groups = c.tokens * c.parts;
+template <class F>
+int resident_of(F kernel, std::atomic<int> (&known)[kDevices]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    std::atomic<int>* k = dev < kDevices ? &known[dev] : nullptr;
+    int n = k ? k->load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0) != cudaSuccess || n < 1) n = 1;
+        if (k) k->store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
-template <int VEC, int UPL, bool XB, bool YB>
-cudaError_t fwd(const QkParams& c, cudaStream_t s) {
-    const long long blocks = (c.groups * c.G + kThreads - 1) / kThreads;
-    if (c.interleaved)
-        qk_fwd_kernel<VEC, UPL, XB, YB, true><<<(unsigned)blocks, kThreads, 0, s>>>(c);
-    else
-        qk_fwd_kernel<VEC, UPL, XB, YB, false><<<(unsigned)blocks, kThreads, 0, s>>>(c);
+template <int VEC, int UPL, bool XB, bool YB, bool IL>
+cudaError_t fwd(QkParams& c, const gdn_qk_problem& p, int sms, cudaStream_t s) {
+    static std::atomic<int> known[kDevices];
+    const auto kernel = qk_fwd_kernel<VEC, UPL, XB, YB, IL>;
+    const int blocks = fill(c, p, VEC, resident_of(kernel, known) * sms);
+    kernel<<<blocks, kThreads, 0, s>>>(c);
     return cudaGetLastError();
 }
-template <int VEC, int UPL, bool XB, bool YB>
-cudaError_t bwd(const QkParams& c, int blocks, cudaStream_t s) {
-    if (c.interleaved)
-        qk_bwd_kernel<VEC, UPL, XB, YB, true><<<blocks, kThreads, 0, s>>>(c);
-    else
-        qk_bwd_kernel<VEC, UPL, XB, YB, false><<<blocks, kThreads, 0, s>>>(c);
-    return cudaGetLastError();
+template <int VEC, int UPL, bool XB, bool YB, bool IL>
+cudaError_t bwd(QkParams& c, const gdn_qk_problem& p, int sms, float* dwq, float* dwk, cudaStream_t s) {
+    static std::atomic<int> known[kDevices];
+    const auto kernel = qk_bwd_kernel<VEC, UPL, XB, YB, IL>;
+    const int blocks = fill(c, p, VEC, std::min(resident_of(kernel, known) * sms, kMaxBlocks - 2));
+    kernel<<<blocks, kThreads, 0, s>>>(c);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !c.partial) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((c.K + 7) / 8, 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, qk_sum_kernel, (const float*)c.partial, c.blocks0, blocks, c.K, dwq, dwk);
 }
 // (UPL: units of VEC pairs a lane, 32 lanes holding a row of up to 256 channels)
 template <bool XB, bool YB, class F>
@@ -507,11 +560,6 @@ cudaError_t by_type(const gdn_qk_problem& p, F f) {
     const bool xb = p.x_dtype == GDN_DTYPE_BF16, yb = p.y_dtype == GDN_DTYPE_BF16;
     if (xb) return yb ? f(std::true_type(), std::true_type()) : f(std::true_type(), std::false_type());
     return yb ? f(std::false_type(), std::true_type()) : f(std::false_type(), std::false_type());
-}
-
-int bwd_blocks(const QkParams& c, int sms) {
-    const long long rows = kThreads / c.G;
-    return (int)std::max(1LL, std::min<long long>({(c.groups + rows - 1) / rows, 3LL * sms, (long long)kMaxBlocks}));
 }
 
 }  // namespace
@@ -535,28 +583,28 @@ gdn_status gdn_qk_norm_fwd(const gdn_qk_problem* p, const void* q, const void* k
         if (off_type(f, GDN_DTYPE_F32)) return GDN_ERR_MISALIGNED;
     if ((st = current_device_status()) != GDN_OK) return st;
     if (!any) return GDN_OK;
-    const int vec = widest(*p, {q, k}, {yq, yk});
+    const int vec = widest(*p, {q, k}, {yq, yk}), sms = std::max(1, current_sm_count());
     QkParams c{};
-    fill(c, *p, vec);
-    c.x[0] = q, c.x[1] = k;
-    c.y[0] = yq, c.y[1] = yk;
-    c.w[0] = wq, c.w[1] = wk;
+    c.side[0].x = q, c.side[1].x = k;
+    c.side[0].y = yq, c.side[1].y = yk;
+    c.side[0].w = wq, c.side[1].w = wk;
     c.freq = freq;
     c.pos = positions;
-    c.x_stride[0] = p->q_stride, c.x_stride[1] = p->k_stride;
-    c.y_stride[0] = (long long)p->Hq * p->K, c.y_stride[1] = (long long)p->Hk * p->K;
-    split(c, 1024LL * std::max(1, current_sm_count()));
-    if ((c.groups * c.G + kThreads - 1) / kThreads >= (1LL << 31)) return GDN_ERR_UNSUPPORTED_SHAPE;
+    c.side[0].x_stride = p->q_stride, c.side[1].x_stride = p->k_stride;
+    c.side[0].y_stride = (long long)p->Hq * p->K, c.side[1].y_stride = (long long)p->Hk * p->K;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = by_type(*p, [&](auto xb, auto yb) {
-        return by_vec<xb.value, yb.value>(vec, [&](auto v, auto u) { return fwd<v.value, u.value, xb.value, yb.value>(c, s); });
+        return by_vec<xb.value, yb.value>(vec, [&](auto v, auto u) {
+            return p->interleaved ? fwd<v.value, u.value, xb.value, yb.value, true>(c, *p, sms, s)
+                                  : fwd<v.value, u.value, xb.value, yb.value, false>(c, *p, sms, s);
+        });
     });
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 size_t gdn_qk_norm_bwd_workspace_bytes(int K) {
     if (K < 2 || K > kMaxK || K % 2) return 0;
-    return kWsHeader + ws_round(sizeof(float) * 2 * (size_t)K * kMaxBlocks);
+    return kWsHeader + ws_round(sizeof(float) * (size_t)K * kMaxBlocks);
 }
 
 gdn_status gdn_qk_norm_bwd(const gdn_qk_problem* p, const void* q, const void* k, const float* wq, const float* wk,
@@ -576,37 +624,26 @@ gdn_status gdn_qk_norm_bwd(const gdn_qk_problem* p, const void* q, const void* k
         if (off_type(f, GDN_DTYPE_F32)) return GDN_ERR_MISALIGNED;
     if ((st = current_device_status()) != GDN_OK) return st;
     if (!any && !dwq && !dwk) return GDN_OK;
-    const int vec = widest(*p, {q, k, dq, dk}, {dyq, dyk});
+    const int vec = widest(*p, {q, k, dq, dk}, {dyq, dyk}), sms = std::max(1, current_sm_count());
     QkParams c{};
-    fill(c, *p, vec);
-    c.x[0] = q, c.x[1] = k;
-    c.dy[0] = dyq, c.dy[1] = dyk;
-    c.y[0] = dq, c.y[1] = dk;
-    c.w[0] = wq, c.w[1] = wk;
+    c.side[0].x = q, c.side[1].x = k;
+    c.side[0].dy = dyq, c.side[1].dy = dyk;
+    c.side[0].y = dq, c.side[1].y = dk;
+    c.side[0].w = wq, c.side[1].w = wk;
     c.freq = freq;
     c.pos = positions;
-    c.x_stride[0] = c.y_stride[0] = p->q_stride, c.x_stride[1] = c.y_stride[1] = p->k_stride;
-    c.dy_stride[0] = (long long)p->Hq * p->K, c.dy_stride[1] = (long long)p->Hk * p->K;
+    c.side[0].x_stride = c.side[0].y_stride = p->q_stride, c.side[1].x_stride = c.side[1].y_stride = p->k_stride;
+    c.side[0].dy_stride = (long long)p->Hq * p->K, c.side[1].dy_stride = (long long)p->Hk * p->K;
     if (dwq || dwk) c.partial = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kWsHeader);
-    const int sms = std::max(1, current_sm_count());
-    if (p->T == 0) c.T = 1;   // no tokens: the sums are zeros
-    split(c, 3LL * kThreads * sms);
-    const int blocks = bwd_blocks(c, sms);
+    gdn_qk_problem sizes = *p;
+    if (!any) sizes.R = 0;   // (no tokens: the sums are zeros, and no frequency is read)
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = by_type(*p, [&](auto xb, auto yb) {
-        return by_vec<xb.value, yb.value>(vec, [&](auto v, auto u) { return bwd<v.value, u.value, xb.value, yb.value>(c, blocks, s); });
+    const cudaError_t e = by_type(sizes, [&](auto xb, auto yb) {
+        return by_vec<xb.value, yb.value>(vec, [&](auto v, auto u) {
+            return p->interleaved ? bwd<v.value, u.value, xb.value, yb.value, true>(c, sizes, sms, dwq, dwk, s)
+                                  : bwd<v.value, u.value, xb.value, yb.value, false>(c, sizes, sms, dwq, dwk, s);
+        });
     });
-    if (e != cudaSuccess || !c.partial) return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((2 * p->K + 7) / 8);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, qk_sum_kernel, (const float*)c.partial, blocks, p->K, dwq, dwk);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

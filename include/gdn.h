@@ -603,7 +603,7 @@ GDN_API gdn_status gdn_qk_norm_fwd(const gdn_qk_problem* p, const void* q, const
                                    const float* wk, const float* freq, const int* positions, void* yq,
                                    void* yk, void* stream);
 
-/* Workspace bytes for gdn_qk_norm_bwd (at most 3 MiB). It needs no initial value. Returns 0 for a K outside the set. */
+/* Workspace bytes for gdn_qk_norm_bwd (at most 1.1 MB). It needs no initial value. Returns 0 for a K outside the set. */
 GDN_API size_t gdn_qk_norm_bwd_workspace_bytes(int K);
 
 /* The gradients for dyq, dyk (contiguous, in y_dtype): dq, dk in x_dtype at q's and k's strides (what lies between the
