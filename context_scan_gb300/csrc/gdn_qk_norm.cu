@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 
 #include "gdn_internal.h"
+#include "gdn_pair.cuh"
 
 namespace gdn {
 namespace {
@@ -29,6 +30,9 @@ namespace {
 constexpr int kMaxK = 256;
 constexpr int kThreads = 256;
 constexpr int kDevices = 64;
+// pairs a lane holds at most, backward: with 4, three blocks of 80 registers a thread an SM and 92 us for 524288 rows of
+// 128 in bf16; with 8 two blocks and 110 us. (Forward 8: three blocks and 125 us for 1310720 rows; with 4 131.)
+constexpr int kBwdVec = 4;
 constexpr int kMaxBlocks = 1024;   // of the backward: rows of partial sums in the workspace
 
 struct Side {                // the queries, or the keys
@@ -132,27 +136,106 @@ struct Units {
     __device__ __forceinline__ int pair0(int i) const { return VEC * unit(i); }
 };
 
-// In an interleaved unit the 2 VEC values lie in order: pair e is (2 e, 2 e + 1). f: the values in the order of the
-// two loads; e-th pair's members:
-template <int VEC>
-__device__ __forceinline__ void members(const float (&a)[VEC], const float (&b)[VEC], int e, bool il, float& x, float& y) {
-    x = a[e];
-    y = b[e];
-    if (VEC == 1 || !il) return;
-    const int i = 2 * e;
-    x = i < VEC ? a[i % VEC] : b[i % VEC];
-    y = i + 1 < VEC ? a[(i + 1) % VEC] : b[(i + 1) % VEC];
+__device__ __forceinline__ float total(pair_t x) {
+    float lo, hi;
+    unpack(x, lo, hi);
+    return lo + hi;
 }
+__device__ __forceinline__ pair_t both(float x) { return pack(x, x); }
+
+// A unit's values in fp32, by pairs of channels that turn together: x the first members, y the second ones, two
+// channels to a register pair for the two-wide instructions (of a single channel the second place is 0). In an
+// interleaved unit the 2 VEC values of the two loads lie in order, pair e being (2 e, 2 e + 1).
 template <int VEC>
-__device__ __forceinline__ void put(float (&a)[VEC], float (&b)[VEC], int e, bool il, float x, float y) {
-    if (VEC == 1 || !il) {
-        a[e] = x;
-        b[e] = y;
-        return;
+struct Members {
+    static constexpr int N = (VEC + 1) / 2;
+    pair_t x[N], y[N];
+    template <bool IL, class A, class B>   // a(i), b(i): the i-th values of the two loads
+    __device__ __forceinline__ void take(A a, B b) {
+        float mx[2 * N], my[2 * N];
+        mx[2 * N - 1] = my[2 * N - 1] = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int i = 2 * e, j = 2 * e + 1;
+            mx[e] = !IL || VEC == 1 ? a(e) : i < VEC ? a(i % VEC) : b(i % VEC);
+            my[e] = !IL || VEC == 1 ? b(e) : j < VEC ? a(j % VEC) : b(j % VEC);
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            x[n] = pack(mx[2 * n], mx[2 * n + 1]);
+            y[n] = pack(my[2 * n], my[2 * n + 1]);
+        }
     }
-    const int i = 2 * e;
-    (i < VEC ? a[i % VEC] : b[i % VEC]) = x;
-    (i + 1 < VEC ? a[(i + 1) % VEC] : b[(i + 1) % VEC]) = y;
+    template <bool IL>
+    __device__ __forceinline__ void give(float (&a)[VEC], float (&b)[VEC]) const {
+        float mx[2 * N], my[2 * N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            unpack(x[n], mx[2 * n], mx[2 * n + 1]);
+            unpack(y[n], my[2 * n], my[2 * n + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int i = 2 * e, j = 2 * e + 1;
+            (!IL || VEC == 1 ? a[e] : i < VEC ? a[i % VEC] : b[i % VEC]) = mx[e];
+            (!IL || VEC == 1 ? b[e] : j < VEC ? a[j % VEC] : b[j % VEC]) = my[e];
+        }
+    }
+    // turned by the angles of cosines c and sines s (BACK: the other way round)
+    template <bool BACK>
+    __device__ __forceinline__ void turn(const pair_t (&c)[N], const pair_t (&s)[N]) {
+        const pair_t less = both(-1.f);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const pair_t u = x[n], v = y[n];
+            if constexpr (BACK) {
+                x[n] = fma2(v, s[n], mul2(u, c[n]));
+                y[n] = fma2(mul2(u, s[n]), less, mul2(v, c[n]));
+            } else {
+                x[n] = fma2(mul2(v, s[n]), less, mul2(u, c[n]));
+                y[n] = fma2(u, s[n], mul2(v, c[n]));
+            }
+        }
+    }
+    // in shared memory, 2 N pairs a unit
+    __device__ __forceinline__ void put(pair_t* to) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n) to[n] = x[n], to[N + n] = y[n];
+    }
+    __device__ __forceinline__ void get(const pair_t* from) {   // (volatile: not kept in registers over the rows)
+        const unsigned at = (unsigned)__cvta_generic_to_shared(from);
+        if constexpr (N % 2 == 0) {
+#pragma unroll
+            for (int n = 0; n < N; n += 2) {
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x[n]), "=l"(x[n + 1]) : "r"(at + 8 * n));
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(y[n]), "=l"(y[n + 1]) : "r"(at + 8 * (N + n)));
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                asm volatile("ld.shared.b64 %0, [%1];" : "=l"(x[n]) : "r"(at + 8 * n));
+                asm volatile("ld.shared.b64 %0, [%1];" : "=l"(y[n]) : "r"(at + 8 * (N + n)));
+            }
+        }
+    }
+};
+// A side's weights in shared memory, by units (in registers they would cost a block an SM).
+template <int VEC>
+struct Weights {
+    static constexpr int N = Members<VEC>::N;
+    pair_t w[kMaxK / (2 * VEC) * 2 * N];
+};
+template <int VEC, int UPL, bool IL>
+__device__ __forceinline__ void make_weights(const Units<VEC, UPL>& un, const float* w, Weights<VEC>& to) {
+#pragma unroll
+    for (int i = 0; i < UPL; ++i)
+        if ((int)threadIdx.x < un.G && un.has(i)) {
+            Members<VEC> m;
+            m.template take<IL>([&](int e) { return w ? __ldg(w + un.first(i) + e) : 1.f; },
+                                [&](int e) { return w ? __ldg(w + un.second(i) + e) : 1.f; });
+            m.put(to.w + 2 * Members<VEC>::N * un.unit(i));
+        }
+    __syncthreads();
 }
 
 // Every rotated pair's turn from one position to the next, as a 64-bit fraction, in shared memory (zeros for pairs
@@ -167,18 +250,29 @@ __device__ __forceinline__ void make_steps(const QkParams& p, unsigned long long
     }
     __syncthreads();
 }
-// cosines and sines of a lane's pairs at position n (1 and 0 for channels that are not rotated)
+// cosines and sines of a lane's pairs at position n
 template <int VEC, int UPL>
-__device__ __forceinline__ void turns(const Units<VEC, UPL>& un, const unsigned long long* step, int n, float (&c)[UPL][VEC],
-                                      float (&s)[UPL][VEC]) {
+struct Turns {
+    static constexpr int N = (VEC + 1) / 2;
+    pair_t c[UPL][N], s[UPL][N];
+    __device__ __forceinline__ Turns(const Units<VEC, UPL>& un, const unsigned long long* step, int n) {
 #pragma unroll
-    for (int i = 0; i < UPL; ++i)
+        for (int i = 0; i < UPL; ++i) {
+            float co[2 * N], si[2 * N];
+            co[2 * N - 1] = si[2 * N - 1] = 0.f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const unsigned long long a = un.has(i) ? (unsigned long long)(long long)n * step[un.pair0(i) + e] : 0;
-            sincospif((float)(int)(a >> 32) * 0x1p-31f, &s[i][e], &c[i][e]);
+            for (int e = 0; e < VEC; ++e) {
+                const unsigned long long a = un.has(i) && un.turned(i) ? (unsigned long long)(long long)n * step[un.pair0(i) + e] : 0;
+                sincospif((float)(int)(a >> 32) * 0x1p-31f, &si[e], &co[e]);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                c[i][k] = pack(co[2 * k], co[2 * k + 1]);
+                s[i][k] = pack(si[2 * k], si[2 * k + 1]);
+            }
         }
-}
+    }
+};
 
 __device__ __forceinline__ float group_sum(float x, int G) {
     for (int off = G / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -221,8 +315,9 @@ struct Row {   // a head's values that a lane holds
 };
 
 template <int VEC, int UPL, bool XB, bool YB, bool IL>
-__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kThreads, VEC == 8 ? 3 : VEC == 1 ? 2 : 4) qk_fwd_kernel(const __grid_constant__ QkParams p) {
     __shared__ unsigned long long step[kMaxK / 2];
+    __shared__ __align__(16) Weights<VEC> weights;
     make_steps(p, step);
     const bool keys = (int)blockIdx.x >= p.blocks0;
     const Side& s = p.side[keys];
@@ -230,17 +325,8 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant_
     const int G = p.G;
     const Units<VEC, UPL> un(p, threadIdx.x % G);
     const int rows = kThreads / G, mine = threadIdx.x / G;
-    float wa[UPL][VEC], wb[UPL][VEC];
-#pragma unroll
-    for (int i = 0; i < UPL; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            wa[i][e] = wb[i][e] = 1.f;
-            if (un.has(i) && s.w) {
-                wa[i][e] = __ldg(s.w + un.first(i) + e);
-                wb[i][e] = __ldg(s.w + un.second(i) + e);
-            }
-        }
+    constexpr int N = Members<VEC>::N;
+    make_weights<VEC, UPL, IL>(un, s.w, weights);
     // (a warp's groups take part in its exchanges whether or not they have work)
     for (long long g0 = (long long)block * rows; g0 < s.groups; g0 += (long long)blocks * rows) {
         const Work wk(s, g0 + mine);
@@ -249,43 +335,35 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant_
         row[1].zero();
         long long xat = wk.token * s.x_stride + (long long)wk.h0 * p.K, yat = wk.token * s.y_stride + (long long)wk.h0 * p.K;
         row[0].load(un, s.x, xat, wk.h0 < wk.h1);
-        float c[UPL][VEC], sn[UPL][VEC];
-        turns<VEC, UPL>(un, step, p.pos ? (wk.h0 < wk.h1 ? __ldg(p.pos + wk.token) : 0) : (int)(wk.token % p.T), c, sn);
+        const Turns<VEC, UPL> t(un, step, p.pos ? (wk.h0 < wk.h1 ? __ldg(p.pos + wk.token) : 0) : (int)(wk.token % p.T));
         for (int h = wk.h0; __any_sync(0xffffffffu, h < wk.h1); h += 2) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 row[k ^ 1].load(un, s.x, xat + p.K, h + k + 1 < wk.h1);
-                float sq = 0.f;
-#pragma unroll
-                for (int i = 0; i < UPL; ++i)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        sq = fmaf(row[k].a[i].at(e), row[k].a[i].at(e), sq);
-                        sq = fmaf(row[k].b[i].at(e), row[k].b[i].at(e), sq);
-                    }
-                const float rstd = rsqrtf(fmaf(group_sum(sq, G), p.inv_k, p.eps));
+                Members<VEC> m[UPL];
+                pair_t sq = 0;
 #pragma unroll
                 for (int i = 0; i < UPL; ++i) {
-                    float va[VEC], vb[VEC];
+                    m[i].template take<IL>([&](int e) { return row[k].a[i].at(e); }, [&](int e) { return row[k].b[i].at(e); });
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        va[e] = row[k].a[i].at(e) * rstd * wa[i][e];
-                        vb[e] = row[k].b[i].at(e) * rstd * wb[i][e];
+                    for (int n = 0; n < N; ++n) sq = fma2(m[i].y[n], m[i].y[n], fma2(m[i].x[n], m[i].x[n], sq));
+                }
+                const pair_t rstd = both(rsqrtf(fmaf(group_sum(total(sq), G), p.inv_k, p.eps)));
+#pragma unroll
+                for (int i = 0; i < UPL; ++i) {
+                    Members<VEC> w;
+                    w.get(weights.w + 2 * N * min(un.unit(i), un.n - 1));
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        m[i].x[n] = mul2(mul2(m[i].x[n], rstd), w.x[n]);
+                        m[i].y[n] = mul2(mul2(m[i].y[n], rstd), w.y[n]);
                     }
-                    if (un.turned(i)) {
-                        float ya[VEC], yb[VEC];
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            float x, y;
-                            members(va, vb, e, IL, x, y);
-                            put(ya, yb, e, IL, x * c[i][e] - y * sn[i][e], y * c[i][e] + x * sn[i][e]);
-                        }
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) va[e] = ya[e], vb[e] = yb[e];
-                    }
+                    if (un.turned(i)) m[i].template turn<false>(t.c[i], t.s[i]);
+                    float a[VEC], b[VEC];
+                    m[i].template give<IL>(a, b);
                     if (un.has(i) && h + k < wk.h1) {
-                        store<VEC, YB>(s.y, yat + un.first(i), va);
-                        store<VEC, YB>(s.y, yat + un.second(i), vb);
+                        store<VEC, YB>(s.y, yat + un.first(i), a);
+                        store<VEC, YB>(s.y, yat + un.second(i), b);
                     }
                 }
                 xat += p.K;
@@ -297,12 +375,12 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const __grid_constant_
 
 // The gradients. Groups walk over their work in a fixed order; dw of their rows stays in registers, is joined in
 // shared memory at the end and goes to the workspace, one row of sums a block; qk_sum_kernel adds those up in order.
-// (Two blocks an SM: at one, with two rows on their way in each group, memory waits for the lanes.)
 template <int VEC, int UPL, bool XB, bool YB, bool IL>
-__global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kThreads, VEC == 1 ? 2 : 3) qk_bwd_kernel(const __grid_constant__ QkParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ unsigned long long step[kMaxK / 2];
-    __shared__ float sums[kMaxK];
+    __shared__ __align__(16) Weights<VEC> weights;
+    __shared__ float sums[kThreads / 32][kMaxK];
     make_steps(p, step);
     const bool keys = (int)blockIdx.x >= p.blocks0;
     const Side& s = p.side[keys];
@@ -310,112 +388,97 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const __grid_consta
     const int G = p.G;
     const Units<VEC, UPL> un(p, threadIdx.x % G);
     const int rows = kThreads / G, mine = threadIdx.x / G;
-    float w[2][UPL][VEC], dw[2][UPL][VEC];
+    constexpr int N = Members<VEC>::N;
+    Members<VEC> dw[UPL];
+    make_weights<VEC, UPL, IL>(un, s.w, weights);
 #pragma unroll
     for (int i = 0; i < UPL; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            w[0][i][e] = w[1][i][e] = 1.f;
-            dw[0][i][e] = dw[1][i][e] = 0.f;
-            if (un.has(i) && s.w) {
-                w[0][i][e] = __ldg(s.w + un.first(i) + e);
-                w[1][i][e] = __ldg(s.w + un.second(i) + e);
-            }
-        }
+        for (int n = 0; n < N; ++n) dw[i].x[n] = dw[i].y[n] = 0;
     for (long long g0 = (long long)block * rows; g0 < s.groups; g0 += (long long)blocks * rows) {
         const Work wk(s, g0 + mine);
-        Row<VEC, UPL, XB> row[2];
-        Row<VEC, UPL, YB> grad[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            row[k].zero();
-            grad[k].zero();
-        }
+        Row<VEC, UPL, XB> next_row;
+        Row<VEC, UPL, YB> next_grad;
+        next_row.zero();
+        next_grad.zero();
         const long long first = (long long)wk.h0 * p.K;
         long long xat = wk.token * s.x_stride + first, dat = wk.token * s.dy_stride + first, yat = wk.token * s.y_stride + first;
-        row[0].load(un, s.x, xat, wk.h0 < wk.h1);
-        grad[0].load(un, s.dy, dat, wk.h0 < wk.h1);
-        float c[UPL][VEC], sn[UPL][VEC];
-        turns<VEC, UPL>(un, step, p.pos ? (wk.h0 < wk.h1 ? __ldg(p.pos + wk.token) : 0) : (int)(wk.token % p.T), c, sn);
-        for (int h = wk.h0; __any_sync(0xffffffffu, h < wk.h1); h += 2) {
+        next_row.load(un, s.x, xat, wk.h0 < wk.h1);
+        next_grad.load(un, s.dy, dat, wk.h0 < wk.h1);
+        const Turns<VEC, UPL> t(un, step, p.pos ? (wk.h0 < wk.h1 ? __ldg(p.pos + wk.token) : 0) : (int)(wk.token % p.T));
+#pragma unroll 1
+        for (int h = wk.h0; __any_sync(0xffffffffu, h < wk.h1); ++h) {
+            const Row<VEC, UPL, XB> row = next_row;
+            const Row<VEC, UPL, YB> grad = next_grad;
+            next_row.load(un, s.x, xat + p.K, h + 1 < wk.h1);
+            next_grad.load(un, s.dy, dat + p.K, h + 1 < wk.h1);
+            const bool on = h < wk.h1;
+            Members<VEC> x[UPL], g[UPL];   // g: dy turned back
+            pair_t sq = 0, dot = 0;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                row[k ^ 1].load(un, s.x, xat + p.K, h + k + 1 < wk.h1);
-                grad[k ^ 1].load(un, s.dy, dat + p.K, h + k + 1 < wk.h1);
-                const bool on = h + k < wk.h1;
-                float sq = 0.f, dot = 0.f, ea[UPL][VEC], eb[UPL][VEC];   // e: dy turned back
+            for (int i = 0; i < UPL; ++i) {
+                x[i].template take<IL>([&](int e) { return row.a[i].at(e); }, [&](int e) { return row.b[i].at(e); });
+                g[i].template take<IL>([&](int e) { return grad.a[i].at(e); }, [&](int e) { return grad.b[i].at(e); });
+                if (un.turned(i)) g[i].template turn<true>(t.c[i], t.s[i]);
+                Members<VEC> w;
+                w.get(weights.w + 2 * N * min(un.unit(i), un.n - 1));
 #pragma unroll
-                for (int i = 0; i < UPL; ++i) {
-                    float va[VEC], vb[VEC];
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        va[e] = ea[i][e] = grad[k].a[i].at(e);
-                        vb[e] = eb[i][e] = grad[k].b[i].at(e);
-                    }
-                    if (un.turned(i)) {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            float x, y;
-                            members(va, vb, e, IL, x, y);
-                            put(ea[i], eb[i], e, IL, x * c[i][e] + y * sn[i][e], y * c[i][e] - x * sn[i][e]);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float xa = row[k].a[i].at(e), xb = row[k].b[i].at(e);
-                        sq = fmaf(xa, xa, sq);
-                        sq = fmaf(xb, xb, sq);
-                        dot = fmaf(ea[i][e] * w[0][i][e], xa, dot);
-                        dot = fmaf(eb[i][e] * w[1][i][e], xb, dot);
-                    }
+                for (int n = 0; n < N; ++n) {
+                    sq = fma2(x[i].y[n], x[i].y[n], fma2(x[i].x[n], x[i].x[n], sq));
+                    dot = fma2(mul2(g[i].x[n], w.x[n]), x[i].x[n], dot);
+                    dot = fma2(mul2(g[i].y[n], w.y[n]), x[i].y[n], dot);
                 }
-                const float rstd = rsqrtf(fmaf(group_sum(sq, G), p.inv_k, p.eps));
-                // (a row that there is none of any more was this group's last but one: its sums stay out)
-                const float scale = on ? rstd : 0.f;
-                const float mean = group_sum(dot, G) * p.inv_k * rstd * rstd;   // of d u, times another s for u
-#pragma unroll
-                for (int i = 0; i < UPL; ++i) {
-                    float da[VEC], db[VEC];
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float xa = row[k].a[i].at(e), xb = row[k].b[i].at(e);
-                        dw[0][i][e] = fmaf(ea[i][e], on ? xa * scale : 0.f, dw[0][i][e]);
-                        dw[1][i][e] = fmaf(eb[i][e], on ? xb * scale : 0.f, dw[1][i][e]);
-                        da[e] = rstd * fmaf(-xa, mean, ea[i][e] * w[0][i][e]);
-                        db[e] = rstd * fmaf(-xb, mean, eb[i][e] * w[1][i][e]);
-                    }
-                    if (un.has(i) && on) {
-                        store<VEC, XB>(s.y, yat + un.first(i), da);
-                        store<VEC, XB>(s.y, yat + un.second(i), db);
-                    }
-                }
-                xat += p.K;
-                dat += p.K;
-                yat += p.K;
             }
+            const float s1 = rsqrtf(fmaf(group_sum(total(sq), G), p.inv_k, p.eps));
+            const float m1 = group_sum(total(dot), G) * p.inv_k * s1 * s1 * s1;   // mean(d u), times s^2 for -u s
+            // (behind the group's last row its values are still there: out of the sums by a factor of 0)
+            const pair_t rstd = both(s1), kept = both(on ? s1 : 0.f), minus = both(-m1);
+#pragma unroll
+            for (int i = 0; i < UPL; ++i) {
+                Members<VEC> w;
+                w.get(weights.w + 2 * N * min(un.unit(i), un.n - 1));
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    dw[i].x[n] = fma2(g[i].x[n], mul2(x[i].x[n], kept), dw[i].x[n]);
+                    dw[i].y[n] = fma2(g[i].y[n], mul2(x[i].y[n], kept), dw[i].y[n]);
+                    x[i].x[n] = fma2(x[i].x[n], minus, mul2(rstd, mul2(g[i].x[n], w.x[n])));
+                    x[i].y[n] = fma2(x[i].y[n], minus, mul2(rstd, mul2(g[i].y[n], w.y[n])));
+                }
+                float a[VEC], b[VEC];
+                x[i].template give<IL>(a, b);
+                if (un.has(i) && on) {
+                    store<VEC, XB>(s.y, yat + un.first(i), a);
+                    store<VEC, XB>(s.y, yat + un.second(i), b);
+                }
+            }
+            xat += p.K;
+            dat += p.K;
+            yat += p.K;
         }
     }
     if (!p.partial) return;
-    // the groups of a warp first (their lanes hold the same channels), then the warps in turn
-    for (int w0 = 0; w0 < kThreads / 32; ++w0) {
-        if (threadIdx.x / 32 == w0) {
+    // the groups of a warp first (their lanes hold the same channels), then the warps, side by side in shared memory
+    float* mine_ = sums[threadIdx.x / 32];
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+    for (int i = 0; i < UPL; ++i) {
+        float v[2][VEC];
+        dw[i].template give<IL>(v[0], v[1]);
 #pragma unroll
-                for (int i = 0; i < UPL; ++i)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        float t = dw[half][i][e];
-                        for (int off = 16; off >= G; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-                        if ((threadIdx.x & 31) < G && un.has(i)) {
-                            float* to = &sums[(half ? un.second(i) : un.first(i)) + e];
-                            *to = w0 ? *to + t : t;
-                        }
-                    }
-        }
-        __syncthreads();
+            for (int e = 0; e < VEC; ++e) {
+                float t = v[half][e];
+                for (int off = 16; off >= G; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+                if ((threadIdx.x & 31) < G && un.has(i)) mine_[(half ? un.second(i) : un.first(i)) + e] = t;
+            }
     }
-    for (int i = threadIdx.x; i < p.K; i += kThreads) p.partial[(long long)blockIdx.x * p.K + i] = sums[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.K; i += kThreads) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < kThreads / 32; ++k) t += sums[k][i];
+        p.partial[(long long)blockIdx.x * p.K + i] = t;
+    }
 }
 
 // dw[i] = the sum over the blocks' rows, of the queries' (blockIdx.y 0) or the keys' blocks: a block of 256 threads for 8
@@ -547,9 +610,9 @@ cudaError_t bwd(QkParams& c, const gdn_qk_problem& p, int sms, float* dwq, float
     return cudaLaunchKernelEx(&cfg, qk_sum_kernel, (const float*)c.partial, c.blocks0, blocks, c.K, dwq, dwk);
 }
 // (UPL: units of VEC pairs a lane, 32 lanes holding a row of up to 256 channels)
-template <bool XB, bool YB, class F>
+template <int MOST, bool XB, bool YB, class F>
 cudaError_t by_vec(int vec, F f) {
-    if constexpr (XB && YB)
+    if constexpr (XB && YB && MOST == 8)
         if (vec == 8) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
     if (vec == 4) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
     if (vec == 2) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
@@ -594,7 +657,7 @@ gdn_status gdn_qk_norm_fwd(const gdn_qk_problem* p, const void* q, const void* k
     c.side[0].y_stride = (long long)p->Hq * p->K, c.side[1].y_stride = (long long)p->Hk * p->K;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = by_type(*p, [&](auto xb, auto yb) {
-        return by_vec<xb.value, yb.value>(vec, [&](auto v, auto u) {
+        return by_vec<8, xb.value, yb.value>(vec, [&](auto v, auto u) {
             return p->interleaved ? fwd<v.value, u.value, xb.value, yb.value, true>(c, *p, sms, s)
                                   : fwd<v.value, u.value, xb.value, yb.value, false>(c, *p, sms, s);
         });
@@ -624,7 +687,7 @@ gdn_status gdn_qk_norm_bwd(const gdn_qk_problem* p, const void* q, const void* k
         if (off_type(f, GDN_DTYPE_F32)) return GDN_ERR_MISALIGNED;
     if ((st = current_device_status()) != GDN_OK) return st;
     if (!any && !dwq && !dwk) return GDN_OK;
-    const int vec = widest(*p, {q, k, dq, dk}, {dyq, dyk}), sms = std::max(1, current_sm_count());
+    const int vec = std::min(kBwdVec, widest(*p, {q, k, dq, dk}, {dyq, dyk})), sms = std::max(1, current_sm_count());
     QkParams c{};
     c.side[0].x = q, c.side[1].x = k;
     c.side[0].dy = dyq, c.side[1].dy = dyk;
@@ -639,7 +702,7 @@ gdn_status gdn_qk_norm_bwd(const gdn_qk_problem* p, const void* q, const void* k
     if (!any) sizes.R = 0;   // (no tokens: the sums are zeros, and no frequency is read)
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = by_type(sizes, [&](auto xb, auto yb) {
-        return by_vec<xb.value, yb.value>(vec, [&](auto v, auto u) {
+        return by_vec<kBwdVec, xb.value, yb.value>(vec, [&](auto v, auto u) {
             return p->interleaved ? bwd<v.value, u.value, xb.value, yb.value, true>(c, sizes, sms, dwq, dwk, s)
                                   : bwd<v.value, u.value, xb.value, yb.value, false>(c, sizes, sms, dwq, dwk, s);
         });
