@@ -170,28 +170,36 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
 }
 
-// out[t][g][k] = the sum over the heads h of group g, in order, of part[t][h][k], four values a thread
-__global__ void __launch_bounds__(256) group_kernel(const float* part, void* out, int out_bf16, long long fours, int H, int groups,
-                                                    int D, const int* tokens) {
-    const int rep = H / groups, d4 = D / 4;
-    if (tokens) fours = min(fours, (long long)__ldcg(tokens) * groups * d4);
+// out[t][g][k] = the sum over the heads h of group g, in order, of part[t][h][k], four values a thread; dq (blockIdx.y 0), dk
+struct Groups {
+    const float* part[2];
+    void* out[2];
+    const int* tokens;   // of packed sequences, on the device; or null
+    long long fours;
+    int out_bf16, H, groups, D;
+};
+__global__ void __launch_bounds__(256) group_kernel(const Groups g) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int rep = g.H / g.groups, d4 = g.D / 4;
+    long long fours = g.fours;
+    if (g.tokens) fours = min(fours, (long long)__ldcg(g.tokens) * g.groups * d4);
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < fours; i += (long long)gridDim.x * 256) {
         const int k = (int)(i % d4);
         const long long tg = i / d4;   // token * groups + group: its first head is tg * rep
-        const float4* from = reinterpret_cast<const float4*>(part) + (tg * rep) * d4 + k;
+        const float4* from = reinterpret_cast<const float4*>(g.part[blockIdx.y]) + (tg * rep) * d4 + k;
         float4 s = __ldcs(from);
         for (int r = 1; r < rep; ++r) {
             const float4 x = __ldcs(from + (long long)r * d4);
             s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
         }
-        if (out_bf16) {
+        if (g.out_bf16) {
             const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
             uint2 u;
             u.x = *reinterpret_cast<const unsigned*>(&lo);
             u.y = *reinterpret_cast<const unsigned*>(&hi);
-            reinterpret_cast<uint2*>(out)[i] = u;
+            reinterpret_cast<uint2*>(g.out[blockIdx.y])[i] = u;
         } else {
-            reinterpret_cast<float4*>(out)[i] = s;
+            reinterpret_cast<float4*>(g.out[blockIdx.y])[i] = s;
         }
     }
 }
@@ -283,14 +291,17 @@ gdn_status run(Params& c, const gdn_problem& p, int Hqk, bool backward, void* wo
         blocks1 += blocks2 / (k.pieces - 1) * (k.pieces - 2);
     }
     c.words = words;
-    for (int phase = 1; phase <= (blocks2 > 0 ? 2 : 1); ++phase) {
-        c.phase = phase;
-        c.blocks = (int)(phase == 1 ? blocks1 : blocks2);
-        c.table = reinterpret_cast<const int*>(phase == 1 ? table1 : table2);
-        c.dependent = packed || phase == 2;
-        if ((tc ? launch_tc(c, s) : launch_simt(c, s)) != cudaSuccess) return GDN_ERR_CUDA;
-    }
-    return GDN_OK;
+    c.phase = 1;
+    c.blocks = (int)blocks1;
+    c.table = reinterpret_cast<const int*>(table1);
+    c.dependent = packed;
+    Params phases[2] = {c, c};
+    phases[1].phase = 2;
+    phases[1].blocks = (int)blocks2;
+    phases[1].table = reinterpret_cast<const int*>(table2);
+    phases[1].dependent = 1;
+    const int n = blocks2 > 0 ? 2 : 1;
+    return (tc ? launch_tc(phases, n, s) : launch_simt(phases, n, s)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace
@@ -399,14 +410,26 @@ gdn_status gdn_linear_bwd(const gdn_problem* p, int Hqk, int nseq, const int* cu
         }
     st = run(c, *p, Hqk, true, workspace, s);
     if (st != GDN_OK || !grouped || p->T == 0) return st;
-    for (int i = 0; i < 2; ++i) {
-        const long long fours = (long long)p->B * p->T * Hqk * p->K / 4;
-        const unsigned blocks = (unsigned)std::min<long long>((fours + 255) / 256, 16LL * std::max(1, current_sm_count()));
-        group_kernel<<<blocks, 256, 0, s>>>(reinterpret_cast<const float*>(ws + l.part[i]), i ? dk : dq, in, fours, p->H, Hqk,
-                                            p->K, cu_seqlens ? reinterpret_cast<const int*>(ws + kWsVerdict) + kTokens : nullptr);
-        if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
-    }
-    return GDN_OK;
+    Groups g{};
+    for (int i = 0; i < 2; ++i) g.part[i] = reinterpret_cast<const float*>(ws + l.part[i]);
+    g.out[0] = dq;
+    g.out[1] = dk;
+    g.tokens = cu_seqlens ? reinterpret_cast<const int*>(ws + kWsVerdict) + kTokens : nullptr;
+    g.fours = (long long)p->B * p->T * Hqk * p->K / 4;
+    g.out_bf16 = in;
+    g.H = p->H;
+    g.groups = Hqk;
+    g.D = p->K;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)std::min<long long>((g.fours + 255) / 256, 8LL * std::max(1, current_sm_count())), 2);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, group_kernel, g) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -131,10 +131,10 @@ __device__ __forceinline__ float log2_weight(const float* decay, int h) {
     return (g < -200.f ? -200.f : g) * kLog2e;
 }
 
-// One launch of a phase.
-cudaError_t launch_simt(const Params& p, cudaStream_t s);
+// One launch for each of n phases.
+cudaError_t launch_simt(const Params* phases, int n, cudaStream_t s);
 bool tc_supported(const Params& p);
-cudaError_t launch_tc(const Params& p, cudaStream_t s);
+cudaError_t launch_tc(const Params* phases, int n, cudaStream_t s);
 
 }  // namespace linear
 }  // namespace gdn

@@ -268,25 +268,26 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
 
 }  // namespace
 
-cudaError_t launch_simt(const Params& q, cudaStream_t s) {
-    Params p = q;
-    int dA = 0, dC = 0;
-    for (int i = 0; i < p.nroles; ++i) dA = max(dA, p.role[i].dA), dC = max(dC, p.role[i].dC);
-    const int smem = dA == 64 ? (int)sizeof(Smem<64>) : (int)sizeof(Smem<128>);
-    p.tiles = dC / kTile;
+cudaError_t launch_simt(const Params* phases, int n, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<128>));
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((long long)p.blocks * p.tiles));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.dependent ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, simt_kernel, p);
+    for (int i = 0; i < n && e == cudaSuccess; ++i) {
+        Params p = phases[i];
+        int dA = 0, dC = 0;
+        for (int k = 0; k < p.nroles; ++k) dA = max(dA, p.role[k].dA), dC = max(dC, p.role[k].dC);
+        p.tiles = dC / kTile;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)((long long)p.blocks * p.tiles));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = dA == 64 ? sizeof(Smem<64>) : sizeof(Smem<128>);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = p.dependent ? 1 : 0;
+        e = cudaLaunchKernelEx(&cfg, simt_kernel, p);
+    }
+    return e;
 }
 
 }  // namespace linear

@@ -21,8 +21,8 @@
 //
 // A sequence's last chunk may hold fewer than 128 tokens: the rows of B and C behind it (the next sequence's) are
 // overwritten by zeros in shared memory, so that nothing of another sequence enters a sum, not as 0 times NaN either.
+#include <atomic>
 #include <cstring>
-#include <type_traits>
 
 #include "gdn_linear.cuh"
 #include "gdn_pair.cuh"
@@ -35,7 +35,7 @@ namespace {
 constexpr int kThreads = 640;   // five warpgroups
 constexpr int kOutThreads = 256, kStateThreads = 256;
 constexpr int kStateWarp0 = 8;
-constexpr int kRegsOut = 64, kRegsState = 144, kRegsRest = 64, kRegsLaunch = 96;
+constexpr int kRegsOut = 72, kRegsState = 144, kRegsRest = 48, kRegsLaunch = 96;
 static_assert(256 * kRegsOut + 256 * kRegsState + 128 * kRegsRest == kRegsLaunch * kThreads, "the registers of the launch");
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kStoreWarp = 18, kStateMmaWarp = 19;
 constexpr long long kWaitLimit = 4000000000LL;   // SM cycles, some two seconds (for the waits while shutting down)
@@ -206,14 +206,17 @@ struct Work {
     }
 };
 
-template <int DA, int DC>
+// The loads of a piece's chunks (one lane): the first two of them, for which there is nothing to wait for, before the CTA is
+// set up; the others as the stages become free.
+template <int DA, int DC, bool FIRST>
 __device__ __forceinline__ void load_warp(const Work& w, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* mc) {
-    const int rep = w.p->H;
-    const int ah = w.h / (rep / w.r->a_heads), bh = w.h / (rep / w.r->b_heads), ch = w.h / (rep / w.r->c_heads);
-    int issued = 0, issued_a = 0;
-    for (int m = 0; m < w.chunks; ++m) {
+    const int heads = w.p->H;
+    const int ah = w.h / (heads / w.r->a_heads), bh = w.h / (heads / w.r->b_heads), ch = w.h / (heads / w.r->c_heads);
+    int issued = min(2, w.chunks), issued_a = w.sums ? 0 : issued;
+#pragma unroll 1
+    for (int m = FIRST ? 0 : 2; m < (FIRST ? min(2, w.chunks) : w.chunks); ++m) {
         const int s = m & 1;
-        if (m >= 2 && !w.wait1(B_EMPTY0 + s, (m >> 1) - 1)) break;
+        if (!FIRST && !w.wait1(B_EMPTY0 + s, (m >> 1) - 1)) break;
         const uint32_t to = w.base + s * kStage;
         const int row = w.it.lo + kChunk * w.phys(m);
         mbar_arrive_expect_tx(w.bar(B_FULL0 + s), (DA / 64 + DC / 64) * kHalf);
@@ -221,16 +224,16 @@ __device__ __forceinline__ void load_warp(const Work& w, const CUtensorMap* ma, 
         for (int f = 0; f < DC / 64; ++f) tma_load_3d(to + 2 * kTileBytes + f * kHalf, mc, w.bar(B_FULL0 + s), 64 * f, ch, row);
 #pragma unroll
         for (int f = 0; f < DA / 64; ++f) tma_load_3d(to + kTileBytes + f * kHalf, mb, w.bar(B_FULL0 + s), 64 * f, bh, row);
-        issued = m + 1;
+        issued = max(issued, m + 1);
         if (w.sums) continue;
         // (A's tile holds the outputs of chunk m - 2 until they have left)
-        if (m >= 2 && !w.wait1(B_AFREE0 + s, (m >> 1) - 1)) break;
+        if (!FIRST && !w.wait1(B_AFREE0 + s, (m >> 1) - 1)) break;
         mbar_arrive_expect_tx(w.bar(B_AFULL0 + s), (DA / 64) * kHalf);
 #pragma unroll
         for (int f = 0; f < DA / 64; ++f) tma_load_3d(to + f * kHalf, ma, w.bar(B_AFULL0 + s), 64 * f, ah, row);
-        issued_a = m + 1;
+        issued_a = max(issued_a, m + 1);
     }
-    if (*w.abort_flag) {   // (what is in flight lands before shared memory is given back)
+    if (!FIRST && *w.abort_flag) {   // (what is in flight lands before shared memory is given back)
         for (int m = max(0, issued - 2); m < issued; ++m) drain(w.bar(B_FULL0 + (m & 1)), (m >> 1) & 1, kWaitLimit);
         for (int m = max(0, issued_a - 2); m < issued_a; ++m) drain(w.bar(B_AFULL0 + (m & 1)), (m >> 1) & 1, kWaitLimit);
     }
@@ -661,12 +664,15 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     w.abort_flag = reinterpret_cast<volatile int*>(sm + kBar + 8 * B_N);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBar + 8 * B_N + 8);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    if (tid == 0) {
+    const bool turned = K != V && w.r->state_t;   // dA = V, dC = K
+    if (warp == kLoadWarp && lane == 0) {
         for (int i = 0; i < B_N; ++i)
             mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? kOutThreads / 32 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT || i == B_OFREE ? kOutThreads : i == B_OSCALED || i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
         *w.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
+        turned ? load_warp<V, K, true>(w, &q.a[role], &q.b[role], &q.c[role])
+               : load_warp<K, V, true>(w, &q.a[role], &q.b[role], &q.c[role]);
     }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
@@ -682,8 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     __syncthreads();
     tc_fence_after();
     w.tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    const bool turned = K != V && w.r->state_t;   // dA = V, dC = K
-    // The launch's 96 registers a thread, dealt anew: 256 x 64 + 256 x 144 + 128 x 64 = 640 x 96. (At 96 the state's warps
+    // The launch's 96 registers a thread, dealt anew: 256 x 72 + 256 x 144 + 128 x 48 = 640 x 96. (At 96 the state's warps
     // spill, and the stack is in L2.)
     if (warp < kStateWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
@@ -701,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
         if (lane == 0 && warp == kLoadWarp)
-            turned ? load_warp<V, K>(w, &q.a[role], &q.b[role], &q.c[role]) : load_warp<K, V>(w, &q.a[role], &q.b[role], &q.c[role]);
+            turned ? load_warp<V, K, false>(w, &q.a[role], &q.b[role], &q.c[role])
+                   : load_warp<K, V, false>(w, &q.a[role], &q.b[role], &q.c[role]);
         if (lane == 0 && warp == kStoreWarp && !w.sums && w.r->out_bf16) {
             const CUtensorMap* map = &q.out[role];
             turned ? store_warp<K>(w, map) : store_warp<V>(w, map);
@@ -733,8 +739,15 @@ bool tile_map(CUtensorMap* m, const void* ptr, bool bf16, int D, int heads, long
 
 template <int K, int V>
 cudaError_t launch(const TcParams& q, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(tc_kernel<K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    static std::atomic<unsigned long long> set{0};   // devices on which the shared memory has been asked for
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(tc_kernel<K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)q.p.blocks);
     cfg.blockDim = dim3(kThreads);
@@ -757,23 +770,47 @@ bool tc_supported(const Params& p) {
     return p.nroles == kMaxRoles || p.role[0].out_bf16;   // (gradients of shared heads leave as fp32, to be summed)
 }
 
-cudaError_t launch_tc(const Params& p, cudaStream_t s) {
+cudaError_t launch_tc(const Params* phases, int n, cudaStream_t s) {
     TcParams q;
     memset(&q, 0, sizeof q);
-    q.p = p;
+    const Params& p = phases[0];
     const long long tokens = p.cu ? p.T : (long long)p.nseq * p.T;
+    // a tensor in several roles has one map
+    struct Known {
+        const void* ptr;
+        int D, heads;
+        const CUtensorMap* map;
+    } known[4];
+    int count = 0;
+    auto load_map = [&](CUtensorMap* m, const void* ptr, int D, int heads) {
+        for (int i = 0; i < count; ++i)
+            if (known[i].ptr == ptr && known[i].D == D && known[i].heads == heads) {
+                *m = *known[i].map;
+                return true;
+            }
+        if (!tile_map(m, ptr, true, D, heads, tokens, kChunk)) return false;
+        if (count < 4) known[count++] = Known{ptr, D, heads, m};
+        return true;
+    };
     for (int i = 0; i < p.nroles; ++i) {
         const Role& r = p.role[i];
-        if (!tile_map(&q.a[i], r.a, true, r.dA, r.a_heads, tokens, kChunk) || !tile_map(&q.b[i], r.b, true, r.dA, r.b_heads, tokens, kChunk) ||
-            !tile_map(&q.c[i], r.c, true, r.dC, r.c_heads, tokens, kChunk) ||
+        if (!load_map(&q.a[i], r.a, r.dA, r.a_heads) || !load_map(&q.b[i], r.b, r.dA, r.b_heads) ||
+            !load_map(&q.c[i], r.c, r.dC, r.c_heads) ||
             !tile_map(&q.out[i], r.out, r.out_bf16, r.dC, p.H, tokens, r.out_bf16 ? kChunk : 32))
             return cudaErrorInvalidValue;
     }
     // (K, V: of the roles whose state is stored as it is)
     const bool t = p.role[0].state_t;
     const int K = t ? p.role[0].dC : p.role[0].dA, V = t ? p.role[0].dA : p.role[0].dC;
-    if (K == 64) return V == 64 ? launch<64, 64>(q, s) : launch<64, 128>(q, s);
-    return V == 64 ? launch<128, 64>(q, s) : launch<128, 128>(q, s);
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < n && e == cudaSuccess; ++i) {
+        q.p = phases[i];
+        if (K == 64)
+            e = V == 64 ? launch<64, 64>(q, s) : launch<64, 128>(q, s);
+        else
+            e = V == 64 ? launch<128, 64>(q, s) : launch<128, 128>(q, s);
+    }
+    return e;
 }
 
 }  // namespace linear

@@ -9,6 +9,7 @@ has not been built, loading raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -135,6 +136,16 @@ def lib():
             getattr(L, fn).restype = ctypes.c_int
         _lib = L
     return _lib
+
+
+class _Codes(dict):
+    def __missing__(self, dtype):
+        import torch
+        self.update({torch.float32: GDN_DTYPE_F32, torch.bfloat16: GDN_DTYPE_BF16})
+        return dict.get(self, dtype, 99)   # the library rejects it with GDN_ERR_UNSUPPORTED_DTYPE
+
+
+_CODES = _Codes()
 
 
 def _dtype_code(t) -> int:
@@ -387,6 +398,23 @@ def _on_device(*tensors):
             raise ValueError(f"tensor argument {i} is not contiguous")
 
 
+def _all_on(*tensors):
+    """_on_device, in few steps; the current CUDA device."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            _on_device(*tensors)   # names what is wrong
+    return dev
+
+
+def _stream_on(stream, dev):
+    """_stream on a device that is known to be the current one."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if stream is None and raw else _stream(stream)
+
+
 def _is(name, t, dtype, shape):
     """Raises ValueError unless t (or None) has this dtype and shape."""
     if t is not None and (t.dtype is not dtype or t.shape != shape):
@@ -595,26 +623,58 @@ def alloc_linear_workspace(k, v, cu_seqlens=None, backward=False):
     return torch.zeros(n, dtype=torch.uint8, device=k.device)
 
 
+@functools.lru_cache(maxsize=256)
+def _linear_problem(vshape, kshape, nseq, in_dtype, out_dtype):
+    """The problem of these shapes and types, or None where they do not fit together (their tensors are then looked at one
+    by one). Kept, so that a call of known sizes costs the host little: it is read only."""
+    if len(vshape) != 4 or len(kshape) != 4 or kshape[:2] != vshape[:2] or max(*vshape, *kshape, nseq) >= 2**31:
+        return None
+    return Problem(*vshape[:3], kshape[3], vshape[3], 64, _CODES[in_dtype], _CODES[out_dtype], 0, 0)
+
+
+def _linear_call(q, k, v, decay, o, cu_seqlens, kv, states, dev):
+    """(problem, nseq) of a call whose tensors fit: kv are those of k's and v's shapes, states those of the states'; else
+    ValueError. As _linear, in few steps."""
+    import torch
+    vshape, kshape, dt, f32 = v.shape, k.shape, k.dtype, torch.float32
+    nseq = vshape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+    prob = _linear_problem(vshape, kshape, nseq, dt, o.dtype)
+    ok = (prob is not None and q.dtype is dt and v.dtype is dt and q.shape == kshape and o.shape == vshape and
+          decay is not None and decay.dtype is f32 and decay.shape == vshape[2:3] and
+          (cu_seqlens is None or (cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1)))
+    if ok:
+        for t, shape in kv:
+            ok = ok and t.dtype is dt and t.shape == shape
+        want = (nseq, vshape[2], kshape[3], vshape[3])
+        for t in states:
+            ok = ok and (t is None or (t.dtype is f32 and t.shape == want))
+    return (prob if ok else None), nseq
+
+
 def gdn_linear_fwd(q, k, v, decay, h0, o, h_final, workspace, cu_seqlens=None, stream=None):
     """Linear attention with a decay for each head, H_t = exp(decay[h]) H_{t-1} + k_t v_t^T, o_t = q_t^T H_t, in chunks: q, k
     [B, T, Hqk, K], v, o [B, T, H, V], decay [H] fp32, h0, h_final [nseq, H, K, V] fp32 (or None). Without cu_seqlens B
     sequences of T tokens; with it (int32, on the GPU) B == 1 and len(cu_seqlens) - 1 packed sequences."""
-    _on_device(q, k, v, decay, h0, o, h_final, workspace, cu_seqlens)
-    prob, Hqk, nseq = _linear(q, k, v, decay, o, cu_seqlens, dict(h0=h0, h_final=h_final))
-    _check(lib().gdn_linear_fwd(ctypes.byref(prob), Hqk, nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    dev = _all_on(q, k, v, decay, h0, o, h_final, workspace, cu_seqlens)
+    prob, nseq = _linear_call(q, k, v, decay, o, cu_seqlens, (), (h0, h_final), dev)
+    if prob is None:
+        prob, _, nseq = _linear(q, k, v, decay, o, cu_seqlens, dict(h0=h0, h_final=h_final))
+    _check(lib().gdn_linear_fwd(prob, k.shape[2], nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                 _ptr(decay), _ptr(h0), o.data_ptr(), _ptr(h_final), *_room(workspace),
-                                _stream(stream)), "gdn_linear_fwd")
+                                _stream_on(stream, dev)), "gdn_linear_fwd")
 
 
 def gdn_linear_bwd(q, k, v, decay, h0, dO, dht, dq, dk, dv, dh0, workspace, cu_seqlens=None, stream=None):
     """Gradients of gdn_linear_fwd for dO (o's type) and dht (or None): dq, dk, dv (q's, k's and v's shape and type) and
     dh0 (or None). workspace: alloc_linear_workspace(..., backward=True)."""
-    _on_device(q, k, v, decay, h0, dO, dht, dq, dk, dv, dh0, workspace, cu_seqlens)
-    prob, Hqk, nseq = _linear(q, k, v, decay, dO, cu_seqlens, dict(h0=h0, dht=dht, dh0=dh0), dq=(dq, q), dk=(dk, k),
-                              dv=(dv, v))
-    _check(lib().gdn_linear_bwd(ctypes.byref(prob), Hqk, nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    dev = _all_on(q, k, v, decay, h0, dO, dht, dq, dk, dv, dh0, workspace, cu_seqlens)
+    prob, nseq = _linear_call(q, k, v, decay, dO, cu_seqlens, ((dq, k.shape), (dk, k.shape), (dv, v.shape)), (h0, dht, dh0), dev)
+    if prob is None:
+        prob, _, nseq = _linear(q, k, v, decay, dO, cu_seqlens, dict(h0=h0, dht=dht, dh0=dh0), dq=(dq, q), dk=(dk, k),
+                                dv=(dv, v))
+    _check(lib().gdn_linear_bwd(prob, k.shape[2], nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                 _ptr(decay), _ptr(h0), dO.data_ptr(), _ptr(dht), dq.data_ptr(), dk.data_ptr(),
-                                dv.data_ptr(), _ptr(dh0), *_room(workspace), _stream(stream)), "gdn_linear_bwd")
+                                dv.data_ptr(), _ptr(dh0), *_room(workspace), _stream_on(stream, dev)), "gdn_linear_bwd")
 
 
 def gdn_linear_recurrent_fwd(q, k, v, decay, state, slots_in, slots_out, o, workspace, cu_seqlens=None,
@@ -622,16 +682,21 @@ def gdn_linear_recurrent_fwd(q, k, v, decay, state, slots_in, slots_out, o, work
     """The same rule token by token over a state cache [num_slots, H, K, V] fp32, as gdn_recurrent_fwd takes it;
     workspace: alloc_recurrent_workspace(num_slots)."""
     import torch
-    _on_device(q, k, v, decay, state, slots_in, slots_out, o, workspace, cu_seqlens)
-    prob, Hqk, nseq = _linear(q, k, v, decay, o, cu_seqlens, {})
-    B, T, H, V = v.shape
-    slots = 0 if state is None else _int("the number of slots", state.shape[0])
-    _is("state", state, torch.float32, (slots, H, k.shape[-1], V))
-    _is("slots_in", slots_in, torch.int32, (nseq,))
-    _is("slots_out", slots_out, torch.int32, (B * T if per_token else nseq,))
-    _check(lib().gdn_linear_recurrent_fwd(ctypes.byref(prob), Hqk, nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(),
-                                          v.data_ptr(), _ptr(decay), _ptr(state), slots, _ptr(slots_in), _ptr(slots_out),
-                                          int(per_token), o.data_ptr(), *_room(workspace), _stream(stream)),
+    dev = _all_on(q, k, v, decay, state, slots_in, slots_out, o, workspace, cu_seqlens)
+    prob, nseq = _linear_call(q, k, v, decay, o, cu_seqlens, (), (), dev)
+    if prob is None:
+        prob, _, nseq = _linear(q, k, v, decay, o, cu_seqlens, {})
+    vshape, slots = v.shape, 0
+    if state is not None:
+        slots = state.shape[0]
+        if slots >= 2**31 or state.dtype is not torch.float32 or state.shape[1:] != (vshape[2], k.shape[3], vshape[3]):
+            _is("state", state, torch.float32, (_int("the number of slots", slots), vshape[2], k.shape[3], vshape[3]))
+    for name, t, n in (("slots_in", slots_in, nseq), ("slots_out", slots_out, vshape[0] * vshape[1] if per_token else nseq)):
+        if t is not None and (t.dtype is not torch.int32 or t.shape != (n,)):
+            _is(name, t, torch.int32, (n,))
+    _check(lib().gdn_linear_recurrent_fwd(prob, k.shape[2], nseq, _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                          _ptr(decay), _ptr(state), slots, _ptr(slots_in), _ptr(slots_out),
+                                          per_token, o.data_ptr(), *_room(workspace), _stream_on(stream, dev)),
            "gdn_linear_recurrent_fwd")
 
 
@@ -649,37 +714,43 @@ def _head_stride(name, t, like=None):
     return n
 
 
-def _qk(q, k, wq, wk, freq, y_dtype, positions, eps, interleaved):
+@functools.lru_cache(maxsize=256)
+def _qk_problem(qshape, Hk, R, interleaved, x_dtype, y_dtype, eps, q_stride, k_stride):
+    return QkProblem(*qshape[:3], Hk, qshape[3], R, interleaved, _CODES[x_dtype], _CODES[y_dtype], eps, q_stride, k_stride)
+
+
+def _qk(q, k, wq, wk, freq, yq, yk, positions, eps, interleaved, dev):
+    """The problem of these heads; yq, yk are contiguous and of one type."""
     import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
-    for name, t in (("q", q), ("k", k)):
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
-    _on_device(wq, wk, freq, positions)
-    qs, ks = _head_stride("q", q), _head_stride("k", k)
-    B, T, Hq, K = q.shape
-    for name, n in (("B", B), ("T", T), ("Hq", Hq), ("Hk", k.shape[2]), ("K", K)):
-        _int(name, n)
-    _is("k", k, q.dtype, (B, T, k.shape[2], K))
+    f32, qshape, kshape = torch.float32, q.shape, k.shape
+    if q.get_device() != dev or k.get_device() != dev:
+        name, t = ("q", q) if q.get_device() != dev else ("k", k)
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    qs = qshape[2] * qshape[3] if len(qshape) == 4 and q.is_contiguous() else _head_stride("q", q)
+    ks = kshape[2] * kshape[3] if len(kshape) == 4 and k.is_contiguous() else _head_stride("k", k)
+    B, T, Hq, K = qshape
+    if max(qshape) >= 2**31 or kshape[2] >= 2**31:
+        for name, n in (("B", B), ("T", T), ("Hq", Hq), ("Hk", kshape[2]), ("K", K)):
+            _int(name, n)
     R = 0 if freq is None else 2 * freq.numel()
-    _is("wq", wq, torch.float32, (K,))
-    _is("wk", wk, torch.float32, (K,))
-    _is("freq", freq, torch.float32, (R // 2,))
-    if positions is not None and (positions.dtype != torch.int32 or positions.numel() != B * T):
+    for name, t, dtype, shape in (("k", k, q.dtype, (B, T, kshape[2], K)), ("wq", wq, f32, (K,)), ("wk", wk, f32, (K,)),
+                                  ("freq", freq, f32, (R // 2,)), ("the queries' results", yq, yq.dtype, qshape),
+                                  ("the keys' results", yk, yq.dtype, kshape)):
+        if t is not None and (t.dtype is not dtype or t.shape != shape):
+            _is(name, t, dtype, shape)
+    if positions is not None and (positions.dtype is not torch.int32 or positions.numel() != B * T):
         raise ValueError("positions holds one int32 a token")
-    return QkProblem(B, T, Hq, k.shape[2], K, R, int(interleaved), _dtype_code(q), y_dtype, eps, qs, ks)
+    return _qk_problem(qshape, kshape[2], R, int(interleaved), q.dtype, yq.dtype, eps, qs, ks)
 
 
 def gdn_qk_norm_fwd(q, k, wq, wk, freq, yq, yk, positions=None, eps=1e-6, interleaved=False, stream=None):
     """Every head of q [B, T, Hq, K] and k [B, T, Hk, K] (tokens evenly apart: parts of one projection's rows, say)
     normalised by its root mean square, scaled by wq, wk [K] fp32 (or None) and rotated by its position: freq [R / 2]
     fp32 (or None: not rotated), positions int32 (or None: 0 .. T - 1). yq, yk: contiguous, of one type."""
-    prob = _qk(q, k, wq, wk, freq, _dtype_code(yq), positions, eps, interleaved)
-    _on_device(yq, yk)
-    _is("yq", yq, yq.dtype, q.shape)
-    _is("yk", yk, yq.dtype, k.shape)
-    _check(lib().gdn_qk_norm_fwd(ctypes.byref(prob), q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freq),
-                                 _ptr(positions), yq.data_ptr(), yk.data_ptr(), _stream(stream)), "gdn_qk_norm_fwd")
+    dev = _all_on(wq, wk, freq, positions, yq, yk)
+    prob = _qk(q, k, wq, wk, freq, yq, yk, positions, eps, interleaved, dev)
+    _check(lib().gdn_qk_norm_fwd(prob, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freq), _ptr(positions),
+                                 yq.data_ptr(), yk.data_ptr(), _stream_on(stream, dev)), "gdn_qk_norm_fwd")
 
 
 def alloc_qk_norm_bwd_workspace(q, k=None):
@@ -696,10 +767,8 @@ def gdn_qk_norm_bwd(q, k, wq, wk, freq, dyq, dyk, dq, dk, dwq, dwk, workspace, p
     """Gradients of gdn_qk_norm_fwd for dyq, dyk (contiguous): dq, dk (q's and k's type, shape and token stride), dwq, dwk [K]
     fp32 (None skips either)."""
     import torch
-    prob = _qk(q, k, wq, wk, freq, _dtype_code(dyq), positions, eps, interleaved)
-    _on_device(dyq, dyk, dwq, dwk, workspace)
-    _is("dyq", dyq, dyq.dtype, q.shape)
-    _is("dyk", dyk, dyq.dtype, k.shape)
+    dev = _all_on(wq, wk, freq, positions, dyq, dyk, dwq, dwk, workspace)
+    prob = _qk(q, k, wq, wk, freq, dyq, dyk, positions, eps, interleaved, dev)
     for name, t, like, stride in (("dq", dq, q, prob.q_stride), ("dk", dk, k, prob.k_stride)):
         if t.device != like.device:
             raise ValueError(f"{name} is on {t.device}, not on {like.device}")
@@ -708,9 +777,9 @@ def gdn_qk_norm_bwd(q, k, wq, wk, freq, dyq, dyk, dq, dk, dwq, dwk, workspace, p
     K = q.shape[-1]
     _is("dwq", dwq, torch.float32, (K,))
     _is("dwk", dwk, torch.float32, (K,))
-    _check(lib().gdn_qk_norm_bwd(ctypes.byref(prob), q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freq),
-                                 _ptr(positions), dyq.data_ptr(), dyk.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                 _ptr(dwq), _ptr(dwk), *_room(workspace), _stream(stream)), "gdn_qk_norm_bwd")
+    _check(lib().gdn_qk_norm_bwd(prob, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freq), _ptr(positions),
+                                 dyq.data_ptr(), dyk.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk),
+                                 *_room(workspace), _stream_on(stream, dev)), "gdn_qk_norm_bwd")
 
 
 def gdn_selftest_wait_timeout(workspace, limit_cycles, stream=None):
