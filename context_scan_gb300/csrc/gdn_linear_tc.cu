@@ -55,8 +55,10 @@ static_assert(kTab % 16 == 0 && kKey % 16 == 0 && kBar % 16 == 0, "alignment");
 // tensor memory, columns
 constexpr uint32_t kTmS = 0, kTmU = 128, kTmHi = 256, kTmLo = 320, kTmO = 384;
 
-// mbarriers, 8 bytes each from kBar on
-enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_AFULL0, B_AFULL1, B_AFREE0, B_AFREE1, B_OUT, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_DRAIN0, B_DRAIN1, B_N };
+// mbarriers, 8 bytes each from kBar on. A wait names a phase by its parity, so no barrier may get two phases ahead of any warp that
+// waits on it, however long that warp is held up: between two phases of each lies something that every one of its
+// waiters does only once it has seen the first.
+enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_AFULL0, B_AFULL1, B_AFREE0, B_AFREE1, B_OUT0, B_OUT1, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_DRAIN0, B_DRAIN1, B_N };
 constexpr unsigned kTag = 0x60;   // + the barrier's number
 
 struct TcParams {
@@ -176,9 +178,8 @@ struct Work {
     __device__ __forceinline__ int phys(int m) const { return r->rev ? n - 1 - (it.m0 + m) : it.m0 + m; }
     __device__ __forceinline__ int length(int m) const { return min(kChunk, it.len - kChunk * phys(m)); }
     __device__ __forceinline__ uint32_t bar(int i) const { return base + kBar + 8 * i; }
-    // tensor memory of Cw and U; sums alone have two of each, in the places of S and O, and form a chunk's Cw during the last one's U
+    // tensor memory of Cw; sums alone have two, the other in the place of S, and form a chunk's Cw during the last one's U
     __device__ __forceinline__ uint32_t cw(int m) const { return sums && (m & 1) ? kTmS : kTmHi; }
-    __device__ __forceinline__ uint32_t u(int m) const { return sums && (m & 1) ? kTmO : kTmU; }
     // the whole warp waits; every lane gets the same verdict
     __device__ __forceinline__ bool wait(int i, int parity) const {
         for (int left = kWaitTries; !__all_sync(0xffffffffu, mbar_try_wait_suspend(bar(i), parity & 1, 20000u)); --left) {
@@ -306,7 +307,7 @@ __device__ __forceinline__ void state_mma_warp(const Work& w, int lane) {
         }
         if (!w.wait(B_VD, m)) break;
         tc_fence_after();
-        mma_tokens<ID_U, 2, 8>(w.tmem + w.u(m), w.tmem + w.cw(m), B, 0, first);
+        mma_tokens<ID_U, 2, 8>(w.tmem + kTmU, w.tmem + w.cw(m), B, 0, first);
         commit_one(w.bar(B_U), first);
         commit_one(w.bar(B_EMPTY0 + st), first);
     }
@@ -437,7 +438,7 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
             }
         }
         if constexpr (OUT_BF16) {
-            mbar_arrive(w.bar(B_OUT));   // (to store_warp)
+            mbar_arrive(w.bar(B_OUT0 + (m & 1)));   // (to store_warp)
         } else {
             store_wait();
             __syncwarp();
@@ -451,7 +452,7 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
 template <int DC>
 __device__ __forceinline__ void store_warp(const Work& w, const CUtensorMap* map) {
     for (int m = 0; m < w.chunks; ++m) {
-        if (!w.wait1(B_OUT, m)) break;
+        if (!w.wait1(B_OUT0 + (m & 1), m >> 1)) break;
         if (w.length(m) == kChunk) {   // (a sequence's last rows have gone by other ways)
 #pragma unroll
             for (int b = 0; b < DC / 64; ++b)
@@ -541,7 +542,7 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 float u[32];
-                tmem_ld32(lanes + w.u(m) + 64 * half + 32 * b, u);
+                tmem_ld32(lanes + kTmU + 64 * half + 32 * b, u);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 32; i += 2)
@@ -599,6 +600,9 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
             }
         }
         tmem_wait_st();
+        // (sums alone: U of the chunk before, while this chunk's Cw waits. Not behind the arrival: a warp held up there for as long
+        // as the next U takes would find B_U a phase too far, and wait for ever)
+        if (w.sums && m > 0 && !take_u(m - 1)) return;
         tc_fence_before();
         mbar_arrive(w.bar(B_VD));
         if (!w.sums) {   // the rows' weights on O = A X, while U is formed: half of the columns each; here lane = row
@@ -620,8 +624,7 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
             tc_fence_before();
             mbar_arrive(w.bar(B_OSCALED));
         }
-        // (sums alone: U of the chunk before, while this chunk's is formed)
-        if (w.sums ? m > 0 && !take_u(m - 1) : !take_u(m)) return;
+        if (!w.sums && !take_u(m)) return;
         if (!w.sums && m + 1 < w.chunks) {
             tc_fence_before();
             put_x();
@@ -667,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     const bool turned = K != V && w.r->state_t;   // dA = V, dC = K
     if (warp == kLoadWarp && lane == 0) {
         for (int i = 0; i < B_N; ++i)
-            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? kOutThreads / 32 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT || i == B_OFREE ? kOutThreads : i == B_OSCALED || i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
+            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? kOutThreads / 32 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT0 || i == B_OUT1 || i == B_OFREE ? kOutThreads : i == B_OSCALED || i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
         *w.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();

@@ -293,6 +293,25 @@ def test_graph_and_other_stream():
     assert gdn.gdn_check_device_error(ws)[0] == 0
 
 
+@pytest.mark.parametrize("name", ["packed_pieces", "in_pieces", "ragged"])
+def test_many_calls_in_a_row(name):
+    # one behind the other, without a wait on the host: no wait in a kernel runs out, every call gives the same
+    lens, H, Hqk, K, V, kw = CASES[name]
+    lens = [5 * n for n in lens]
+    d = make(lens, 16, 8, K, V, **kw)
+    o, ht, _ = run_fwd(d)
+    g = run_bwd(d)
+    wf = gdn.alloc_linear_workspace(d["k"], d["v"], d["cu"])
+    wb = gdn.alloc_linear_workspace(d["k"], d["v"], d["cu"], backward=True)
+    o2, ht2, g2 = torch.empty_like(o), torch.empty_like(ht), [torch.empty_like(x) for x in g[:4]]
+    for _ in range(400):
+        gdn.gdn_linear_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], o2, ht2, wf, cu_seqlens=d["cu"])
+    for _ in range(100):
+        gdn.gdn_linear_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["do"], d["dht"], *g2, wb, cu_seqlens=d["cu"])
+    assert gdn.gdn_check_device_error(wf)[0] == 0 and gdn.gdn_check_device_error(wb)[0] == 0
+    assert torch.equal(o, o2) and torch.equal(ht, ht2) and all(torch.equal(x, y) for x, y in zip(g, g2))
+
+
 def test_split_and_joined_prompts_agree():
     # a prompt in one call, and in three that hand the state on
     d = make([1000], 3, 3, 128, 128, packed=False)
