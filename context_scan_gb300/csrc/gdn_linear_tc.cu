@@ -485,6 +485,7 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
         const auto at = base + ((long long)w.it.seq * w.p->H + w.h) * kState;
         return r.state_t ? at + (long long)c * DA + 64 * half : at + (long long)64 * half * DC + c;
     };
+    if (w.p->phase == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (mine) {
         if (w.it.piece == 0) {
             if (r.start) {
@@ -651,7 +652,12 @@ template <int K, int V>
 __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ TcParams q) {
     extern __shared__ uint8_t smem_raw[];
     const Params& p = q.p;
-    if (p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Phase 1 waits for the plan that names its pieces, and then lets phase 2's blocks start on the SMs that it leaves: these
+    // set up and load, and wait only before they read phase 1's states.
+    if (p.phase == 1) {
+        if (p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
     Work w;
     w.p = &p;
     if (!item_of(p, blockIdx.x, w.it, w.first, w.rest)) return;
