@@ -7,6 +7,7 @@
 // X' = w^n X + B^T C. A thread keeps 8 x 4 (dA = 128) values of the state in registers and the next step's tokens
 // on their way. Bound by the fp32 pipe and shared memory's reads beside it.
 #include "gdn_linear.cuh"
+#include "gdn_pair.cuh"
 
 namespace gdn {
 namespace linear {
@@ -29,13 +30,21 @@ __device__ __forceinline__ void load4(const void* base, bool bf16, long long at,
     }
 }
 
+__device__ __forceinline__ float total(pair_t x) {
+    float lo, hi;
+    unpack(x, lo, hi);
+    return lo + hi;
+}
+
 template <int DA>
 struct Smem {
     float A[kS][DA + 4];
     float B[kS][DA + 4];
     float C[kS][kTile];
     float P[kS][kS + 4];
-    float X[DA][kTile];
+    // rows in pairs, for the two-wide fp32 instructions; of every four columns the first two lie in the first half (16 bytes
+    // a lane, a warp's side by side)
+    pair_t X[DA / 2][kTile];
     float weight[kS + 2];   // w^0 .. w^32 and beyond
 };
 
@@ -50,11 +59,11 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
     // the state: rows 8 tr .. (DA / 16 of them), columns 4 tc .. of this tile
     constexpr int RT = DA / 16;
     const int tc = tid % 16, tr = tid / 16;
-    float X[RT][4];
+    pair_t X[RT / 2][4];   // rows in pairs
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT / 2; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) X[i][c] = 0.f;
+        for (int c = 0; c < 4; ++c) X[i][c] = 0;
     const long long state = (long long)DA * r.dC;
     auto place = [&](int i, int c) {   // in a state as the caller stores it
         const long long row = RT * tr + i, col = col0 + 4 * tc + c;
@@ -66,9 +75,9 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
         if (r.start) {
             const float* from = r.start + ((long long)it.seq * p.H + h) * state;
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
+            for (int i = 0; i < RT; i += 2)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) X[i][c] = __ldg(from + place(i, c));
+                for (int c = 0; c < 4; ++c) X[i / 2][c] = pack(__ldg(from + place(i, c)), __ldg(from + place(i + 1, c)));
         }
     } else if (!sums) {
         for (int q = 1; q <= it.piece; ++q) {
@@ -76,12 +85,14 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
             const float keep = q == 1 ? 0.f
                 : exp2f(lg * tokens_of(first + (q - 2) * rest, first + (q - 1) * rest, it.len, r.rev));
             const float* from = slot(q);
+            const pair_t keep2 = pack(keep, keep);
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
+            for (int i = 0; i < RT; i += 2) {
                 const float4 u = __ldcg(reinterpret_cast<const float4*>(from + slot_at(i)));
-                const float v[4] = {u.x, u.y, u.z, u.w};
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + slot_at(i + 1)));
+                const pair_t t[4] = {pack(u.x, v.x), pack(u.y, v.y), pack(u.z, v.z), pack(u.w, v.w)};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) X[i][c] = q == 1 ? v[c] : fmaf(keep, X[i][c], v[c]);
+                for (int c = 0; c < 4; ++c) X[i / 2][c] = q == 1 ? t[c] : fma2(keep2, X[i / 2][c], t[c]);
             }
         }
     }
@@ -132,28 +143,34 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
             *reinterpret_cast<float4*>(&sm.C[row][c]) = make_float4(fc[j][0], fc[j][1], fc[j][2], fc[j][3]);
         }
 #pragma unroll
-        for (int j = 0; j < RT; ++j)
-            *reinterpret_cast<float4*>(&sm.X[RT * tr + j][4 * tc]) = make_float4(X[j][0], X[j][1], X[j][2], X[j][3]);
+        for (int j = 0; j < RT / 2; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; c += 2)
+                *reinterpret_cast<ulonglong2*>(&sm.X[RT / 2 * tr + j][kTile / 4 * c + 2 * tc]) = make_ulonglong2(X[j][c], X[j][c + 1]);
         __syncthreads();
         if (i + 1 < steps) fetch(r.rev ? steps - 2 - i : i + 1);
         if (!sums) {
             // P: rows pr, pr + 16, columns pc, pc + 16
             const int pr = tid / 16, pc = tid % 16;
-            float d[2][2] = {};
+            pair_t d2[2][2] = {};
 #pragma unroll 4
             for (int k = 0; k < DA; k += 4) {
-                float4 x[2], y[2];
+                ulonglong2 x[2], y[2];
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
-                    x[z] = *reinterpret_cast<const float4*>(&sm.A[pr + 16 * z][k]);
-                    y[z] = *reinterpret_cast<const float4*>(&sm.B[pc + 16 * z][k]);
+                    x[z] = *reinterpret_cast<const ulonglong2*>(&sm.A[pr + 16 * z][k]);
+                    y[z] = *reinterpret_cast<const ulonglong2*>(&sm.B[pc + 16 * z][k]);
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int v = 0; v < 2; ++v)
-                        d[u][v] = fmaf(x[u].w, y[v].w, fmaf(x[u].z, y[v].z, fmaf(x[u].y, y[v].y, fmaf(x[u].x, y[v].x, d[u][v]))));
+                    for (int v = 0; v < 2; ++v) d2[u][v] = fma2(x[u].y, y[v].y, fma2(x[u].x, y[v].x, d2[u][v]));
             }
+            float d[2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) d[u][v] = total(d2[u][v]);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -164,23 +181,27 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
             __syncthreads();
             // out: rows orow, orow + 16, columns 4 tc ..
             const int orow = tid / 16;
-            float intra[2][4] = {}, inter[2][4] = {};
-#pragma unroll 4
+            float intra[2][4] = {}, inter[2][4];
+            pair_t sums2[2][4] = {};
+#pragma unroll 2
             for (int k = 0; k < DA; k += 4) {
-                const float4 x0 = *reinterpret_cast<const float4*>(&sm.A[orow][k]);
-                const float4 x1 = *reinterpret_cast<const float4*>(&sm.A[orow + 16][k]);
-                const float u0[4] = {x0.x, x0.y, x0.z, x0.w}, u1[4] = {x1.x, x1.y, x1.z, x1.w};
+                const ulonglong2 x0 = *reinterpret_cast<const ulonglong2*>(&sm.A[orow][k]);
+                const ulonglong2 x1 = *reinterpret_cast<const ulonglong2*>(&sm.A[orow + 16][k]);
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const float4 y = *reinterpret_cast<const float4*>(&sm.X[k + z][4 * tc]);
-                    const float v[4] = {y.x, y.y, y.z, y.w};
+                for (int z = 0; z < 2; ++z)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        inter[0][c] = fmaf(u0[z], v[c], inter[0][c]);
-                        inter[1][c] = fmaf(u1[z], v[c], inter[1][c]);
+                    for (int c = 0; c < 4; c += 2) {
+                        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(&sm.X[k / 2 + z][kTile / 4 * c + 2 * tc]);
+                        sums2[0][c] = fma2(z ? x0.y : x0.x, y.x, sums2[0][c]);
+                        sums2[1][c] = fma2(z ? x1.y : x1.x, y.x, sums2[1][c]);
+                        sums2[0][c + 1] = fma2(z ? x0.y : x0.x, y.y, sums2[0][c + 1]);
+                        sums2[1][c + 1] = fma2(z ? x1.y : x1.x, y.y, sums2[1][c + 1]);
                     }
-                }
             }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) inter[u][c] = total(sums2[u][c]);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int row = orow + 16 * u;
@@ -213,24 +234,24 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
             }
         }
         // X' = w^L X + sum_j w^(L - 1 - j + s) b_j c_j^T (j in the role's direction)
-        const float keep = sm.weight[L];
+        const pair_t keep = pack(sm.weight[L], sm.weight[L]);
 #pragma unroll
-        for (int j = 0; j < RT; ++j)
+        for (int j = 0; j < RT / 2; ++j)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) X[j][c] *= keep;
-#pragma unroll 2
+            for (int c = 0; c < 4; ++c) X[j][c] = mul2(X[j][c], keep);
+#pragma unroll 4
         for (int j = 0; j < L; ++j) {
             const float wj = sm.weight[r.rev ? j + 1 : L - 1 - j];
             const float4 y = *reinterpret_cast<const float4*>(&sm.C[j][4 * tc]);
-            const float v[4] = {y.x * wj, y.y * wj, y.z * wj, y.w * wj};
+            const pair_t v[4] = {pack(y.x * wj, y.x * wj), pack(y.y * wj, y.y * wj), pack(y.z * wj, y.z * wj), pack(y.w * wj, y.w * wj)};
 #pragma unroll
             for (int x = 0; x < RT; x += 4) {
-                const float4 b = *reinterpret_cast<const float4*>(&sm.B[j][RT * tr + x]);
-                const float u[4] = {b.x, b.y, b.z, b.w};
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&sm.B[j][RT * tr + x]);
 #pragma unroll
-                for (int z = 0; z < 4; ++z)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) X[x + z][c] = fmaf(u[z], v[c], X[x + z][c]);
+                for (int c = 0; c < 4; ++c) {
+                    X[x / 2][c] = fma2(b.x, v[c], X[x / 2][c]);
+                    X[x / 2 + 1][c] = fma2(b.y, v[c], X[x / 2 + 1][c]);
+                }
             }
         }
     }
@@ -239,15 +260,22 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
         if (r.last) {
             float* to = r.last + ((long long)it.seq * p.H + h) * state;
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
+            for (int i = 0; i < RT; i += 2)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) to[place(i, c)] = X[i][c];
+                for (int c = 0; c < 4; ++c) unpack(X[i / 2][c], to[place(i, c)], to[place(i + 1, c)]);
         }
     } else if (p.phase == 1) {
         float* to = slot(it.piece + 1);
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-            *reinterpret_cast<float4*>(to + slot_at(i)) = make_float4(X[i][0], X[i][1], X[i][2], X[i][3]);
+        for (int i = 0; i < RT; i += 2) {
+            float4 a, b;
+            unpack(X[i / 2][0], a.x, b.x);
+            unpack(X[i / 2][1], a.y, b.y);
+            unpack(X[i / 2][2], a.z, b.z);
+            unpack(X[i / 2][3], a.w, b.w);
+            *reinterpret_cast<float4*>(to + slot_at(i)) = a;
+            *reinterpret_cast<float4*>(to + slot_at(i + 1)) = b;
+        }
     }
 }
 
