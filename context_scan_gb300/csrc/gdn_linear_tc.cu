@@ -581,7 +581,7 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
         for (int x = 0; x < 2; ++x) {
             const uint32_t to = lanes + cw_at + ((uint32_t)(16 * x) << 16) + 32 * half;
             const uint32_t from = C + (ldm ^ 32 * x);
-#pragma unroll 1
+#pragma unroll
             for (int g = 0; g < 8; g += 2) {
                 uint32_t v[4], hi[4], lo[4];   // two 8-token groups x 16 channels
                 ldmatrix_trans(from + g * 1024, v);
