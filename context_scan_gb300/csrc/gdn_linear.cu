@@ -93,10 +93,11 @@ __global__ void __launch_bounds__(kPlanThreads)
         longest = __reduce_max_sync(0xffffffffu, warp_max[lane]);
         all = warp_total(warp_time[lane]);
         const long long uncut = nseq > room ? max((long long)longest, all / room + longest / 2) : longest;
-        // lengths worth trying: from what an even cut of all chunks would give on, in steps of a sixteenth of it
-        const int even = max(1, (int)(((long long)cu[nseq] / kChunk) / (room + nseq))), step = (even + 15) / 16;
-        for (int r0 = even; r0 + first_of(r0) + kSaved <= longest; r0 += 32 * step) {
-            const int r = r0 + warp * step, f = first_of(r);
+        // lengths worth trying: from what an even cut of all chunks would give on, in steps of a sixteenth, three times as far
+        // a round
+        const int even = max(1, (int)(((long long)cu[nseq] / kChunk) / (room + nseq)));
+        for (int r0 = even; r0 + first_of(r0) + kSaved <= longest; r0 *= 3) {
+            const int step = (r0 + 15) / 16, r = r0 + warp * step, f = first_of(r);
             long long count = 0, work = 0;   // pieces behind first ones; chunks of phase 1 (sums by half)
             for (int s = lane; s < nseq; s += 32) {
                 const int n = chunks(s), more = more_pieces(n, f, r);

@@ -547,7 +547,8 @@ GDN_API size_t gdn_linear_workspace_bytes(const gdn_problem* p, int Hqk, int nse
 /* The chunked form, for prompts and training.
  *   h0       [nseq,H,K,V] fp32, or NULL for zero states
  *   o        [B,T,H,V] out_dtype, written
- *   h_final  [nseq,H,K,V] fp32, the state after each sequence's last token (after none: h0); NULL skips it */
+ *   h_final  [nseq,H,K,V] fp32, the state after each sequence's last token (after none: h0); NULL skips it
+ * Outputs overlap nothing. */
 GDN_API gdn_status gdn_linear_fwd(const gdn_problem* p, int Hqk, int nseq, const int* cu_seqlens, const void* q,
                                   const void* k, const void* v, const float* decay, const float* h0,
                                   void* o, float* h_final, void* workspace, size_t workspace_bytes,

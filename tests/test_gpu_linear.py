@@ -133,6 +133,7 @@ CASES = {
     "in_pieces": ([2900], 2, 2, 128, 128, {}),
     "in_pieces_no_start": ([3001], 1, 1, 128, 128, dict(start=False)),
     "packed_pieces": ([1800, 17, 900, 0, 1500], 2, 1, 128, 128, {}),
+    "long_among_many_short": ([1 + i % 3 for i in range(300)] + [20000], 2, 1, 64, 128, {}),
     "k64": ([200, 7, 129], 3, 3, 64, 64, {}),
     "k64_v128": ([130, 0, 257], 4, 2, 64, 128, {}),
     "k128_v64": ([130, 1, 257], 4, 2, 128, 64, {}),
