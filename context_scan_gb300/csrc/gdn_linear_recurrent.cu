@@ -7,13 +7,14 @@
 //
 // As in gdn_recurrent.cu a warp holds some columns of one head's state, all K rows of them, in registers, and
 // every column is independent of the others; here the update needs nothing that the lanes have to exchange, so
-// a token is one pass over the state: decayed, updated, and read for the output.
+// a token is one pass over the state: decayed, updated, and read for the output. Bound by memory: each state is read and
+// written once.
 #include "gdn_recurrent.cuh"
 
 namespace gdn {
 namespace {
 
-// (one block: the decay of this head; -inf and what is as good as that give w = 0)
+// the factor of a head's state; -inf, and what is as good as that, gives 0
 __device__ __forceinline__ float head_weight(const RecurrentParams& p, int h) {
     return expf(__ldg(reinterpret_cast<const float*>(p.g) + h));
 }
@@ -205,11 +206,19 @@ cudaError_t launch_fn(const void* fn, const RecurrentParams& p, int cols, cudaSt
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// 16 columns a warp read every token's k and q least often; 8 columns make twice as many warps. us (16 / 8 columns; K = V = 128,
+// bf16, by the number of 16-column warps and the tokens a sequence, cold caches):
+//   warps     128          512          1024         2048         8192
+//   8 tokens  10.2 / 8.2   10.2 / 10.2  12.3 / 14.5  16.4 / 20.5  41.0 / 55.3
+//   64        26.6 / 23.6  26.6 / 28.5  36.9 / 47.1  57.3 / 71.7  164 / 236
+// (K = V = 64, 256 warps: 10.2 / 8.2 and 20.5 / 22.5.) So 8 only while 16 leave half of the schedulers without a warp. One
+// token of each of 256 sequences of 32 heads takes linear_decode_kernel 171 us, 6.3 TB/s; 1 to 8 draft tokens of 48 with the
+// state kept after each linear_tokens_kernel 93 us, 6.0 TB/s.
 template <int K, bool BF>
 cudaError_t launch_k(const RecurrentParams& p, int sms, cudaStream_t s) {
     if (p.T == 1 && !p.cu) return launch_fn((const void*)linear_decode_kernel<K, 16, 4, BF>, p, 16 * kWarps, s);
     const long long warps = (long long)p.nseq * p.H * (p.V / 16);
-    if (warps >= 12LL * sms) return launch_fn((const void*)linear_tokens_kernel<K, 16, 4, BF>, p, 16 * kWarps, s);
+    if (warps >= 2LL * sms) return launch_fn((const void*)linear_tokens_kernel<K, 16, 4, BF>, p, 16 * kWarps, s);
     return launch_fn((const void*)linear_tokens_kernel<K, 8, 1, BF>, p, 8 * kWarps, s);
 }
 
