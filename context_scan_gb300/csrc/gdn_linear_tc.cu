@@ -158,6 +158,7 @@ __device__ __forceinline__ void sts4(uint32_t at, uint32_t x, uint32_t y, uint32
 // while shutting down after a wait that ran out: lets what the CTA issued retire
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, long long limit) {
     const long long t0 = clock64();
+#pragma unroll 1
     while (!mbar_try_wait(bar, parity))
         if (clock64() - t0 > limit) return;
 }
@@ -182,24 +183,22 @@ struct Work {
     __device__ __forceinline__ uint32_t cw(int m) const { return sums && (m & 1) ? kTmS : kTmHi; }
     // the whole warp waits; every lane gets the same verdict
     __device__ __forceinline__ bool wait(int i, int parity) const {
+#pragma unroll 1
         for (int left = kWaitTries; !__all_sync(0xffffffffu, mbar_try_wait_suspend(bar(i), parity & 1, 20000u)); --left) {
             if (__any_sync(0xffffffffu, *abort_flag)) return false;
             if (left == 0) {
-                give_up(i);
+                *abort_flag = kTag + i;   // (the CTA's end records it)
                 return false;
             }
         }
         return true;
     }
-    __device__ __forceinline__ void give_up(int i) const {
-        record_error(p->err, GDN_ERR_TIMEOUT, kTag + i);
-        *abort_flag = 1;
-    }
     __device__ __forceinline__ bool wait1(int i, int parity) const {   // one lane
+#pragma unroll 1
         for (int left = kWaitTries; !mbar_try_wait_suspend(bar(i), parity & 1, 20000u); --left) {
             if (*abort_flag) return false;
             if (left == 0) {
-                give_up(i);
+                *abort_flag = kTag + i;   // (the CTA's end records it)
                 return false;
             }
         }
@@ -428,6 +427,7 @@ __device__ __forceinline__ void out_warps(const Work& w, const CUtensorMap* map,
                 if (lane == 0) tma_store_3d(map, box, first, w.h, row0);
             } else if (OUT_BF16 ? L < kChunk : rows < 32) {   // the sequence ends in this chunk: row by row
                 constexpr int kPieces = kMine / kBoxes * kSize / 16;   // of 16 bytes in a row: 4 or 8 lanes each
+#pragma unroll 1
                 for (int i = lane / kPieces; i < rows; i += 32 / kPieces) {
                     const int k = lane % kPieces;
                     const float4 v = lds4(box + sw128(i, piece0 + k));
@@ -502,6 +502,7 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
                 }
             }
         } else if (!w.sums) {
+#pragma unroll 1
             for (int q = 1; q <= w.it.piece; ++q) {
                 // entering piece q: from the state entering piece q - 1 and that piece's sum
                 const float keep = q == 1 ? 0.f
@@ -565,6 +566,7 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
             if (row >= L) {
                 const uint32_t tile = t & 1 ? C : B;
                 const int halves = t & 1 ? DC / 64 : DA / 64;
+#pragma unroll 1
                 for (int f = 0; f < halves; ++f)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) sts4(tile + f * kHalf + row * 128 + 16 * k, 0, 0, 0, 0);
@@ -728,6 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && *w.abort_flag) record_error(p.err, GDN_ERR_TIMEOUT, *w.abort_flag);
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(w.tmem), "r"(512u) : "memory");
 }
