@@ -62,6 +62,7 @@ struct Params {
     int phase;             // 1: piece 0 of every chain, sums of the middle pieces; 2: the other pieces
     int blocks;            // of the phase, by tiles
     int tiles;             // of the columns, of the role with the most of them
+    int by_role;           // a sequence's chains in the order of their roles, not of their heads
     int dependent;         // launched while the grid before it still runs
     DeviceError* err;
 };
@@ -71,7 +72,7 @@ enum { kCount1 = 0, kCount2, kTokens, kFirst, kRest };
 
 // What block number e of the phase does; false: nothing. It wants sums alone where 1 <= piece in phase 1.
 __device__ __forceinline__ bool item_of(const Params& p, int e, Item& it, int& first, int& rest) {
-    const int width = p.H * p.nroles;   // chains of a sequence; roles side by side, which read the same tensors
+    const int width = p.H * p.nroles;   // chains of a sequence
     int chain;
     if (p.cu) {
         const int entry = e / width;
@@ -110,8 +111,13 @@ __device__ __forceinline__ bool item_of(const Params& p, int e, Item& it, int& f
         first = p.first;
         rest = p.rest;
     }
-    it.h = chain / p.nroles;
-    it.role = chain - it.h * p.nroles;
+    if (p.by_role) {
+        it.role = chain / p.H;
+        it.h = chain - it.role * p.H;
+    } else {
+        it.h = chain / p.nroles;
+        it.role = chain - it.h * p.nroles;
+    }
     const int n = (it.len + kChunk - 1) / kChunk;
     it.m0 = it.piece == 0 ? 0 : first + (it.piece - 1) * rest;
     it.m1 = it.piece == it.pieces - 1 ? n : first + it.piece * rest;

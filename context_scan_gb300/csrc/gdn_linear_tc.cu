@@ -504,15 +504,12 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
         } else if (!w.sums) {
 #pragma unroll 1
             for (int q = 1; q <= w.it.piece; ++q) {
-                // entering piece q: from the state entering piece q - 1 and that piece's sum
+                // entering piece q: from the state entering piece q - 1 and that piece's sum (q = 1: what piece 0 left)
                 const float keep = q == 1 ? 0.f
                     : exp2f(w.lg * tokens_of(w.first + (q - 2) * w.rest, w.first + (q - 1) * w.rest, w.it.len, r.rev));
                 const float* from = slot(q);
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    const float u = __ldcg(from + i * DC);
-                    X[i] = q == 1 ? u : fmaf(keep, X[i], u);
-                }
+                for (int i = 0; i < 64; ++i) X[i] = fmaf(keep, X[i], __ldcg(from + i * DC));
             }
         }
     }
