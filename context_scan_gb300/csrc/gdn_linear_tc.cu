@@ -16,8 +16,18 @@
 // memory (two stages of A, B, C: 192 KB, and 32 KB of X), which would not hold scaled copies as well.
 //
 // Warps: 0-7 P and the outputs; 8-15 the state: Cw (each half of them 64 tokens), X (each half 64 rows) and the scaling of O;
-// 16 loads (TMA, 128-byte swizzle), 17 and 19 issue the MMAs, 18 stores bf16 outputs (TMA). Every wait on an mbarrier is bounded: on expiry the kernel records
-// GDN_ERR_TIMEOUT, lets what it issued retire, frees tensor memory and returns.
+// 16 loads (TMA, 128-byte swizzle), 17 issues S and O += P C, 19 O = A X and U, 18 stores bf16 outputs (TMA). P takes S's place in
+// tensor memory, outputs leave through A's tile. Every wait on an mbarrier is bounded: on expiry it sets a flag that ends the
+// other waits too; the CTA then lets what it issued retire, records GDN_ERR_TIMEOUT, frees tensor memory and returns.
+//
+// Measured (dA = dC = 128): 2.9 us a chunk, some 4900 cycles. Some 3500 of them are shared memory's traffic (450 KB a chunk: tiles
+// written once and read by two or three products, X, Cw and the outputs), 3600 the MMAs (two operands of 128 rows from
+// shared memory take 90 cycles instead of 64), 1800 the dependent way S -> P, 1100 O += P C. Sums alone take 1.4 to 1.6
+// us a chunk, setting a CTA up, its first loads and its end 5 us. 2 x 32768 tokens of 32 heads: 462 us, 4.67 TB/s of
+// 6.78; their gradients at 2 x 8192: 284 us.
+//
+// Code. The two SMs of a pair share what holds their instructions, and 20 warps are at as many places of the code: what the
+// compiler unrolls counts. With every wait's loop unrolled (118 KB instead of 79) the first case took 472 us.
 //
 // A sequence's last chunk may hold fewer than 128 tokens: the rows of B and C behind it (the next sequence's) are
 // overwritten by zeros in shared memory, so that nothing of another sequence enters a sum, not as 0 times NaN either.

@@ -6,11 +6,13 @@
 // for the R / 2 pairs (a, b) of rotated channels, y = u for the others. Backward, with e the gradient on y turned back
 // by -t:   dw = sum over rows of e x s,   d = e w,   dx = s (d - x s mean(d x s)).
 //
-// Bound by memory: x (and dy) read once, y (dx) written once. A row is a few hundred bytes, so a group of
+// Memory's work: x (and dy) read once, y (dx) written once. A row is a few hundred bytes, so a group of
 // up to 32 lanes takes one token and walks over some of its heads: the angles' sines and cosines are formed once for them all
-// and stay in registers with the weights. A lane holds both members of its pairs, so that the rotation crosses no lanes. A
-// block works on the queries or on the keys (so that it holds one set of weights and, backward, one of their sums), and
-// a group reads its next head's row while it works on one.
+// and stay in registers. A lane holds both members of its pairs, so that the rotation crosses no lanes. A
+// block works on the queries or on the keys (so that it holds one set of weights, in shared memory, and, backward, one of their
+// sums), and a group reads its next head's row while it works on one (two rows ahead: 129 us instead of 126 and 98
+// instead of 93). Measured: 32768 tokens of 32 + 8 heads of 128 in bf16 125 us, 5.4 TB/s of 6.8; gradients of 8192 tokens of 32 + 32
+// heads, 64 channels rotated, 92 us, 4.4 TB/s. Beside memory it is the instructions around a row that take the time.
 //
 // Angles. n freq is wanted modulo a turn; in fp32 it would be off by n 2^-24. freq / 2 pi is turned into a
 // 64-bit fraction of a turn (one fp64 product per pair and block); n times that, wrapping as integers do, is the angle
