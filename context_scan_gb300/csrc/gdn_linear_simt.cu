@@ -5,9 +5,10 @@
 // A block of 256 threads owns one piece of one sequence, one head and 64 columns of the state, and walks over steps of 32
 // tokens: A, B, C tiles and the state X in shared memory as fp32; P = (A B^T) with the weights; out = P C + w^.. A X;
 // X' = w^n X + B^T C. A thread keeps 8 x 4 (dA = 128) values of the state in registers and the next step's tokens
-// on their way. Full of blocks it is bound by the fp32 pipe and shared memory's reads beside it (1.4 of 4.5 cycles an instruction
-// waits for them): bf16 in and fp32 out, 2 x 32768 tokens of 32 heads take 11 ms, 24 times what the tensor cores do. With few
-// blocks the steps are a chain: 5 sequences of 130 fp32 tokens, 2 heads, K = V = 64: 28.7 us, five steps of 5 us.
+// on their way. C lies there once more with the weights of the update (8.2 -> 7.8 ms for the case below). Full of blocks it is bound
+// by the fp32 pipe and shared memory's reads beside it (1.4 of 4.5 cycles an instruction waits for them): 2 x 32768 fp32 tokens of 32
+// heads, K = V = 128, take 7.8 ms, bf16 ones with fp32 outputs 9.3, 20 times what the tensor cores do. With few
+// blocks the steps are a chain: 5 sequences of 130 fp32 tokens, 2 heads, K = V = 64: 28.1 us, five steps of 5 us.
 #include "gdn_linear.cuh"
 #include "gdn_pair.cuh"
 
@@ -42,7 +43,7 @@ template <int DA>
 struct Smem {
     float A[kS][DA + 4];
     float B[kS][DA + 4];
-    float C[kS][kTile];
+    float C[kS][kTile], W[kS][kTile];   // W: C with the weights of the update
     float P[kS][kS + 4];
     // rows in pairs, for the two-wide fp32 instructions; of every four columns the first two lie in the first half (16 bytes
     // a lane, a warp's side by side)
@@ -143,6 +144,8 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
         for (int j = 0; j < CF; ++j) {
             const int at = tid + j * kThreads, row = at / (kTile / 4), c = 4 * (at % (kTile / 4));
             *reinterpret_cast<float4*>(&sm.C[row][c]) = make_float4(fc[j][0], fc[j][1], fc[j][2], fc[j][3]);
+            const float wj = row < L ? sm.weight[r.rev ? row + 1 : L - 1 - row] : 0.f;
+            *reinterpret_cast<float4*>(&sm.W[row][c]) = make_float4(fc[j][0] * wj, fc[j][1] * wj, fc[j][2] * wj, fc[j][3] * wj);
         }
 #pragma unroll
         for (int j = 0; j < RT / 2; ++j)
@@ -209,6 +212,7 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
                 const int row = orow + 16 * u;
                 // (the tokens that this row sees: a later one's infinity must not reach it as 0 times infinity)
                 const int j0 = r.rev ? row : 0, j1 = r.rev ? L : min(row + 1, L);
+#pragma unroll 4
                 for (int j = j0; j < j1; ++j) {
                     const float x = sm.P[row][j];
                     const float4 y = *reinterpret_cast<const float4*>(&sm.C[j][4 * tc]);
@@ -243,9 +247,8 @@ __device__ __forceinline__ void walk(const Params& p, const Role& r, const Item&
             for (int c = 0; c < 4; ++c) X[j][c] = mul2(X[j][c], keep);
 #pragma unroll 4
         for (int j = 0; j < L; ++j) {
-            const float wj = sm.weight[r.rev ? j + 1 : L - 1 - j];
-            const float4 y = *reinterpret_cast<const float4*>(&sm.C[j][4 * tc]);
-            const pair_t v[4] = {pack(y.x * wj, y.x * wj), pack(y.y * wj, y.y * wj), pack(y.z * wj, y.z * wj), pack(y.w * wj, y.w * wj)};
+            const float4 y = *reinterpret_cast<const float4*>(&sm.W[j][4 * tc]);
+            const pair_t v[4] = {pack(y.x, y.x), pack(y.y, y.y), pack(y.z, y.z), pack(y.w, y.w)};
 #pragma unroll
             for (int x = 0; x < RT; x += 4) {
                 const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&sm.B[j][RT * tr + x]);
