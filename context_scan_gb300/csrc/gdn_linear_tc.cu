@@ -669,7 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     }
     Work w;
     w.p = &p;
-    if (!item_of(p, blockIdx.x, w.it, w.first, w.rest)) return;
+    if (!item_of(p, blockIdx.x, w.it, w.first, w.rest)) {
+        // Every block of phase 2 waits for phase 1, those without work too (of a packed batch that is not cut, all): what comes behind
+        // this grid in the stream waits for this grid alone, and reads what phase 1 wrote.
+        if (p.phase == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     const int role = w.it.role;
     w.r = &p.role[role];
     w.h = w.it.h;
