@@ -30,7 +30,8 @@
 // compiler unrolls counts. With every wait's loop unrolled (118 KB instead of 79) the first case took 472 us.
 //
 // A sequence's last chunk may hold fewer than 128 tokens: the rows of B and C behind it (the next sequence's) are
-// overwritten by zeros in shared memory, so that nothing of another sequence enters a sum, not as 0 times NaN either.
+// overwritten by zeros in shared memory, so that nothing of another sequence enters a sum, not as 0 times NaN either. Nor
+// does an infinity or a NaN of a token reach tokens that do not see it: see run_again.
 #include <atomic>
 #include <cstring>
 
@@ -58,7 +59,11 @@ constexpr uint32_t kX = 2 * kStage;              // [dA / 64][dC rows of 128 byt
 constexpr uint32_t kTab = kX + kTileBytes;       // w^0 .. w^128
 constexpr uint32_t kKey = kTab + 132 * 4;        // weights of the update (see below): 256
 constexpr uint32_t kBar = kKey + 256 * 4;
-constexpr uint32_t kSmem = kBar + 256 + 1024;    // (with the slack of a 1024-byte alignment)
+// a second pass is wanted (see run_again); in it, for each half of the tokens and column of C, the first token, in the role's
+// direction, whose value is infinite or NaN, or kNone
+constexpr uint32_t kOdd = kBar + 200, kOddToken = kBar + 208;
+constexpr int kNone = 255;
+constexpr uint32_t kSmem = kOddToken + 256 + 1024;   // (with the slack of a 1024-byte alignment)
 static_assert(kSmem <= 232448, "shared memory");
 static_assert(kTab % 16 == 0 && kKey % 16 == 0 && kBar % 16 == 0, "alignment");
 
@@ -68,8 +73,9 @@ constexpr uint32_t kTmS = 0, kTmU = 128, kTmHi = 256, kTmLo = 320, kTmO = 384;
 // mbarriers, 8 bytes each from kBar on. A wait names a phase by its parity, so no barrier may get two phases ahead of any warp that
 // waits on it, however long that warp is held up: between two phases of each lies something that every one of its
 // waiters does only once it has seen the first.
-enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_AFULL0, B_AFULL1, B_AFREE0, B_AFREE1, B_OUT0, B_OUT1, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_DRAIN0, B_DRAIN1, B_N };
+enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_AFULL0, B_AFULL1, B_AFREE0, B_AFREE1, B_OUT0, B_OUT1, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_TAKEN, B_DRAIN0, B_DRAIN1, B_N };
 constexpr unsigned kTag = 0x60;   // + the barrier's number
+static_assert(kBar + 8 * B_N + 12 <= kOdd, "the barriers, the flag and tensor memory's address");
 
 struct TcParams {
     Params p;
@@ -156,6 +162,26 @@ __device__ __forceinline__ float lds(uint32_t at) {
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
     return x;
 }
+__device__ __forceinline__ int lds_int(uint32_t at) {   // (volatile, these: what other threads write)
+    int x;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ int lds_u8(uint32_t at) {
+    int x;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ int lds_u16(uint32_t at) {
+    int x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ void sts_int(uint32_t at, int x) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(x) : "memory"); }
+__device__ __forceinline__ void sts_u8(uint32_t at, int x) { asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(x) : "memory"); }
+__device__ __forceinline__ void sts_zero16(uint32_t at) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)0) : "memory");
+}
 __device__ __forceinline__ float4 lds4(uint32_t at) {
     float4 x;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at));
@@ -217,16 +243,16 @@ struct Work {
 };
 
 // The loads of a piece's chunks (one lane): the first two of them, for which there is nothing to wait for, before the CTA is
-// set up; the others as the stages become free.
+// set up; the others (in a second pass, where `from` is 0, all) as the stages become free.
 template <int DA, int DC, bool FIRST>
-__device__ __forceinline__ void load_warp(const Work& w, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* mc) {
+__device__ __forceinline__ void load_warp(const Work& w, const CUtensorMap* ma, const CUtensorMap* mb, const CUtensorMap* mc, int from = 0) {
     const int heads = w.p->H;
     const int ah = w.h / (heads / w.r->a_heads), bh = w.h / (heads / w.r->b_heads), ch = w.h / (heads / w.r->c_heads);
-    int issued = min(2, w.chunks), issued_a = w.sums ? 0 : issued;
+    int issued = min(from, w.chunks), issued_a = w.sums ? 0 : issued;
 #pragma unroll 1
-    for (int m = FIRST ? 0 : 2; m < (FIRST ? min(2, w.chunks) : w.chunks); ++m) {
+    for (int m = from; m < (FIRST ? min(2, w.chunks) : w.chunks); ++m) {
         const int s = m & 1;
-        if (!FIRST && !w.wait1(B_EMPTY0 + s, (m >> 1) - 1)) break;
+        if (!FIRST && m >= 2 && !w.wait1(B_EMPTY0 + s, (m >> 1) - 1)) break;
         const uint32_t to = w.base + s * kStage;
         const int row = w.it.lo + kChunk * w.phys(m);
         mbar_arrive_expect_tx(w.bar(B_FULL0 + s), (DA / 64 + DC / 64) * kHalf);
@@ -237,7 +263,7 @@ __device__ __forceinline__ void load_warp(const Work& w, const CUtensorMap* ma, 
         issued = max(issued, m + 1);
         if (w.sums) continue;
         // (A's tile holds the outputs of chunk m - 2 until they have left)
-        if (!FIRST && !w.wait1(B_AFREE0 + s, (m >> 1) - 1)) break;
+        if (!FIRST && m >= 2 && !w.wait1(B_AFREE0 + s, (m >> 1) - 1)) break;
         mbar_arrive_expect_tx(w.bar(B_AFULL0 + s), (DA / 64) * kHalf);
 #pragma unroll
         for (int f = 0; f < DA / 64; ++f) tma_load_3d(to + f * kHalf, ma, w.bar(B_AFULL0 + s), 64 * f, ah, row);
@@ -476,7 +502,7 @@ __device__ __forceinline__ void store_warp(const Work& w, const CUtensorMap* map
 
 // Cw and the state: thread = channel of C = lane of tensor memory; the two halves of the warps take 64 tokens of Cw and 64
 // rows of the state each
-template <int DA, int DC>
+template <int DA, int DC, bool CAREFUL>
 __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
     const Role& r = *w.r;
     const int half = warp >> 2, quarter = warp & 3;
@@ -561,6 +587,38 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
         }
         return true;
     };
+    // Second pass: this thread's 64 values of C that are infinite or NaN leave the tile (Cw has them); where the first one was
+    auto take_out = [&](int m) {
+        if (chan < DC) {   // (what its warp made Cw from)
+            const uint32_t column = w.base + (m & 1) * kStage + 2 * kTileBytes + (c >> 6) * kHalf + half * 8192 + 2 * (c & 7);
+            int token = kNone;
+#pragma unroll 1
+            for (int i = 0; i < 64; ++i) {   // (the last one to be met stays)
+                const int t = r.rev ? i : 63 - i;
+                const uint32_t at = column + t * 128 + ((((c & 63) >> 3) ^ (t & 7)) << 4);
+                if ((lds_u16(at) & 0x7f80) != 0x7f80) continue;
+                sts_zero16(at);
+                token = 64 * half + t;
+            }
+            sts_u8(w.base + kOddToken + 128 * half + c, token);
+            fence_proxy_async();
+        }
+        mbar_arrive(w.bar(B_TAKEN));
+    };
+    // ... and O's rows that see one get NaN in its column, for P C to be added to: this thread's row, half of the columns
+    auto put_nan = [&]() {
+#pragma unroll 1
+        for (int k = DC / 2 * half; k < DC / 2 * (half + 1); ++k) {
+            const int a = lds_u8(w.base + kOddToken + k), b = lds_u8(w.base + kOddToken + 128 + k);
+            if (a == kNone && b == kNone) continue;
+            uint32_t x;
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(lanes + kTmO + k) : "memory");
+            tmem_wait_ld();
+            if (r.rev ? (a != kNone && chan <= a) || (b != kNone && chan <= b) : chan >= a || chan >= b) x = 0x7fffffffu;
+            asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(lanes + kTmO + k), "r"(x) : "memory");
+        }
+        tmem_wait_st();
+    };
     bool zeroed = false;
     for (int m = 0; m < w.chunks; ++m) {
         const int L = w.length(m);
@@ -618,6 +676,10 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
         if (!w.sums) {   // the rows' weights on O = A X, while U is formed: half of the columns each; here lane = row
             if (!w.wait(B_OI, m)) return;
             tc_fence_after();
+            if constexpr (CAREFUL) {   // (behind B_X the tokens of the chunk before have been read)
+                if (!w.wait(B_X, m)) return;
+                take_out(m);
+            }
             const int row = chan;
             const float keep = exp2f(w.lg * (r.rev ? max(L - 1 - row, 0) : row + 1));
             const pair_t keep2 = pack(keep, keep);
@@ -631,6 +693,10 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
                 tmem_st32(lanes + kTmO + DC / 2 * half + 32 * b, x);
             }
             tmem_wait_st();
+            if constexpr (CAREFUL) {
+                if (!w.wait(B_TAKEN, m)) return;
+                put_nan();
+            }
             tc_fence_before();
             mbar_arrive(w.bar(B_OSCALED));
         }
@@ -641,6 +707,8 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
         }
     }
     if (w.sums && !take_u(w.chunks - 1)) return;
+    // (row 0 tells: a value of C that is not finite makes U's whole column NaN)
+    if (mine && !w.sums && !(fabsf(X[0]) <= 3.4028235e38f)) sts_int(w.base + kOdd, 1);
     // where the state goes: behind the last piece to the caller, behind the others' first phase to the next piece's slot
     if (!mine) return;
     if (w.it.piece == w.it.pieces - 1) {
@@ -655,6 +723,41 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) to[i * DC] = X[i];
     }
+}
+
+__device__ __forceinline__ void init_barriers(const Work& w) {
+    for (int i = 0; i < B_N; ++i)
+        mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? kOutThreads / 32 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT0 || i == B_OUT1 || i == B_OFREE ? kOutThreads : i == B_OSCALED || i == B_VD || i == B_X || i == B_ZERO || i == B_TAKEN ? kStateThreads : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async();
+}
+
+// Where all warps end a pass over the piece; whether another one follows.
+//
+// O += P C spreads an infinity or a NaN of C over all rows of its chunk, 0 times NaN being NaN. Whether there was one is
+// seen by the state at the piece's end, which is then NaN in that column; the piece is then walked through a second time, in
+// which the state's warps take what is not finite out of C's tile and give NaN to the rows that see it. So the pieces that
+// have none pay for one look at the end. (Looking through C as it comes cost the training gradients 3 to 4 %, by the state's warps or
+// an idle one; the second pass costs them 1 %, as long as the warps with much code have it behind the first one instead of in a
+// loop around it: 285 us instead of 293, 283 without it.)
+__device__ __forceinline__ bool run_again(const Work& w, int pass) {
+    __syncwarp();
+    tc_fence_before();
+    asm volatile("barrier.sync 0;" ::: "memory");
+    tc_fence_after();
+    if (pass > 0 || *w.abort_flag || !lds_int(w.base + kOdd)) return false;
+    // the outputs have to be there before they are written again; nothing may arrive at a barrier that is made anew
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (threadIdx.x == 32 * kLoadWarp) {
+        bool ended = true;
+        for (int m = max(0, w.chunks - 2); m < w.chunks; ++m) ended = ended && w.wait1(B_EMPTY0 + (m & 1), m >> 1);
+        if (ended) {
+            for (int i = 0; i < B_N; ++i) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(w.bar(i)) : "memory");
+            init_barriers(w);
+        }
+    }
+    asm volatile("barrier.sync 0;" ::: "memory");
+    return !*w.abort_flag;
 }
 
 template <int K, int V>
@@ -689,11 +792,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const bool turned = K != V && w.r->state_t;   // dA = V, dC = K
     if (warp == kLoadWarp && lane == 0) {
-        for (int i = 0; i < B_N; ++i)
-            mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? kOutThreads / 32 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT0 || i == B_OUT1 || i == B_OFREE ? kOutThreads : i == B_OSCALED || i == B_VD || i == B_X || i == B_ZERO ? kStateThreads : 1);
+        init_barriers(w);
         *w.abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        fence_proxy_async();
+        sts_int(w.base + kOdd, 0);
         turned ? load_warp<V, K, true>(w, &q.a[role], &q.b[role], &q.c[role])
                : load_warp<K, V, true>(w, &q.a[role], &q.b[role], &q.c[role]);
     }
@@ -723,25 +824,37 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         } else {
             bf16 ? out_warps<K, V, true>(w, map, warp, lane) : out_warps<K, V, false>(w, map, warp, lane);
         }
+        if (run_again(w, 0)) {
+            if (w.sums) {
+            } else if (turned) {
+                bf16 ? out_warps<V, K, true>(w, map, warp, lane) : out_warps<V, K, false>(w, map, warp, lane);
+            } else {
+                bf16 ? out_warps<K, V, true>(w, map, warp, lane) : out_warps<K, V, false>(w, map, warp, lane);
+            }
+            run_again(w, 1);
+        }
     } else if (warp < kLoadWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
-        turned ? state_warps<V, K>(w, warp - kStateWarp0, lane) : state_warps<K, V>(w, warp - kStateWarp0, lane);
+        turned ? state_warps<V, K, false>(w, warp - kStateWarp0, lane) : state_warps<K, V, false>(w, warp - kStateWarp0, lane);
+        if (run_again(w, 0)) {
+            turned ? state_warps<V, K, true>(w, warp - kStateWarp0, lane) : state_warps<K, V, true>(w, warp - kStateWarp0, lane);
+            run_again(w, 1);
+        }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-        if (lane == 0 && warp == kLoadWarp)
-            turned ? load_warp<V, K, false>(w, &q.a[role], &q.b[role], &q.c[role])
-                   : load_warp<K, V, false>(w, &q.a[role], &q.b[role], &q.c[role]);
-        if (lane == 0 && warp == kStoreWarp && !w.sums && w.r->out_bf16) {
-            const CUtensorMap* map = &q.out[role];
-            turned ? store_warp<K>(w, map) : store_warp<V>(w, map);
-        }
-        if (warp == kMmaWarp && !w.sums) turned ? intra_warp<V, K>(w, lane) : intra_warp<K, V>(w, lane);
-        if (warp == kStateMmaWarp) turned ? state_mma_warp<V, K>(w, lane) : state_mma_warp<K, V>(w, lane);
+        int pass = 0;
+        do {
+            if (lane == 0 && warp == kLoadWarp)
+                turned ? load_warp<V, K, false>(w, &q.a[role], &q.b[role], &q.c[role], pass > 0 ? 0 : 2)
+                       : load_warp<K, V, false>(w, &q.a[role], &q.b[role], &q.c[role], pass > 0 ? 0 : 2);
+            if (lane == 0 && warp == kStoreWarp && !w.sums && w.r->out_bf16) {
+                const CUtensorMap* map = &q.out[role];
+                turned ? store_warp<K>(w, map) : store_warp<V>(w, map);
+            }
+            if (warp == kMmaWarp && !w.sums) turned ? intra_warp<V, K>(w, lane) : intra_warp<K, V>(w, lane);
+            if (warp == kStateMmaWarp) turned ? state_mma_warp<V, K>(w, lane) : state_mma_warp<K, V>(w, lane);
+        } while (run_again(w, pass++));
     }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     if (tid == 0 && *w.abort_flag) record_error(p.err, GDN_ERR_TIMEOUT, *w.abort_flag);
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(w.tmem), "r"(512u) : "memory");

@@ -536,9 +536,9 @@ GDN_API gdn_status gdn_norm_bwd(long long rows, int N, int x_dtype, int y_dtype,
  * a workspace must not overlap; its first 256 bytes must be zero before the first call.
  * bf16 inputs and outputs run on the tensor cores: products of bf16 values summed in fp32, where the weighted
  * attention inside a chunk of 128 tokens and the state that a chunk's outputs read are rounded to bf16 once, and the state
- * itself is fp32, its updates good to 2^-17 of each term. A NaN or infinity in one token may then reach the
- * outputs of the tokens of its chunk that lie before it (never those of another sequence). Other types run in fp32
- * throughout. */
+ * itself is fp32, its updates good to 2^-17 of each term. Other types run in fp32 throughout.
+ * A NaN or an infinity in one token reaches the results that see it by the formulas (where it may turn from an infinity
+ * into a NaN) and no others, whatever the types: a padded batch may hold anything behind its sequences' last tokens. */
 
 /* Workspace bytes for gdn_linear_fwd (backward == 0) or gdn_linear_bwd (1), with or without cu_seqlens. Depends
  * on the sizes and the current device's SM count, not on the lengths. Returns 0 for an invalid problem. */
