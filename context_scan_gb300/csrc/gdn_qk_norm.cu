@@ -15,8 +15,9 @@
 // heads, 64 channels rotated, 92 us, 4.4 TB/s. Beside memory it is the instructions around a row that take the time.
 //
 // Angles. n freq is wanted modulo a turn; in fp32 it would be off by n 2^-24. freq / 2 pi is turned into a
-// 64-bit fraction of a turn (one fp64 product per pair and block); n times that, wrapping as integers do, is the angle
-// modulo a turn to n 2^-53 of it.
+// 64-bit fraction of a turn, rounded once (integer products with the digits of 1 / 2 pi that count for freq's exponent, as in
+// Payne and Hanek's argument reduction, once per pair and block); n times that, wrapping as integers do, is the angle modulo a
+// turn to n 2^-65 of it, 2^-34 for the farthest position, whatever freq.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -240,16 +241,27 @@ __device__ __forceinline__ void make_weights(const Units<VEC, UPL>& un, const fl
     __syncthreads();
 }
 
+// 64 binary digits of 1 / 2 pi from place p behind the point on (zeros before it), p from -149 to 169
+__device__ __forceinline__ unsigned long long turn_digits(int p) {
+    constexpr unsigned long long d[4] = {0x28be60db9391054a, 0x7f09d5f47d4d3770, 0x36d8a5664f10e410, 0x7f9458eaf7aef158};
+    if (p < 0) return p <= -64 ? 0 : d[0] >> -p;
+    const unsigned long long hi = p < 64 ? d[0] : p < 128 ? d[1] : d[2], lo = p < 64 ? d[1] : p < 128 ? d[2] : d[3];
+    return p % 64 ? hi << p % 64 | lo >> (64 - p % 64) : hi;
+}
+// f / 2 pi modulo 1, times 2^64, rounded: f = +-m 2^e, m of 24 bits, times 128 digits of 1 / 2 pi from place e on (those before
+// give whole turns)
+__device__ __forceinline__ unsigned long long turn_of(float f) {
+    const unsigned bits = __float_as_uint(f), field = bits >> 23 & 255u;
+    const unsigned long long m = (bits & 0x7fffffu) | (field ? 0x800000u : 0u);
+    const int e = (int)max(field, 1u) - 150;
+    const unsigned long long hi = turn_digits(e), lo = turn_digits(e + 64);
+    const unsigned long long turn = m * hi + __umul64hi(m, lo) + (m * lo >> 63);
+    return bits >> 31 ? 0 - turn : turn;
+}
 // Every rotated pair's turn from one position to the next, as a 64-bit fraction, in shared memory (zeros for pairs
 // that are not rotated).
 __device__ __forceinline__ void make_steps(const QkParams& p, unsigned long long* step) {
-    for (int i = threadIdx.x; i < kMaxK / 2; i += kThreads) {
-        step[i] = 0;
-        if (i < p.R / 2) {
-            const double f = (double)__ldg(p.freq + i) * 0.15915494309189533577;   // 1 / 2 pi
-            step[i] = __double2ull_rd((f - floor(f)) * 0x1p64);
-        }
-    }
+    for (int i = threadIdx.x; i < kMaxK / 2; i += kThreads) step[i] = i < p.R / 2 ? turn_of(__ldg(p.freq + i)) : 0;
     __syncthreads();
 }
 // cosines and sines of a lane's pairs at position n

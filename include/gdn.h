@@ -583,8 +583,9 @@ GDN_API gdn_status gdn_linear_recurrent_fwd(const gdn_problem* p, int Hqk, int n
  *   (y_a, y_b) = (u_a cos t - u_b sin t, u_b cos t + u_a sin t),  t = n freq_i,  for the R / 2 pairs (a, b),
  *   y = u for the K - R channels behind the first R.
  * Pair i is (i, i + R / 2), or with interleaved == 1 (2 i, 2 i + 1). With w = 1/sqrt(K) and eps / K for eps this is
- * the L2 normalisation that the delta rule takes its q and k in. t is formed modulo a turn in 64 bits: any position is
- * as exact as the first. */
+ * the L2 normalisation that the delta rule takes its q and k in. t is formed modulo a turn in 64 bits, exact to
+ * 2^-34 of a turn at any position and frequency. Squares are summed in fp32 (a row whose squares leave its range
+ * overflows as they do). */
 typedef struct {
     int B, T;                      /* sequences and tokens; packed ones: B = 1 and positions given */
     int Hq, Hk, K;                 /* heads of q and of k, channels of a head: even, 2 .. 256 */
