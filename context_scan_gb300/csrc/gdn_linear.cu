@@ -51,17 +51,52 @@ __device__ __forceinline__ int more_pieces(int n, int first, int rest) { return 
 // the pieces from 1 on. Bad lengths are recorded and leave no entries, so that nothing is written. The cut: the
 // shortest `rest` with which at most `room` pieces lie behind first ones (every warp tries one), where that takes less time
 // than no cut. Times in chunks: the longest piece, or, where there are more pieces than room, an even share of all and half of
-// the longest. Longer sequences come first.
+// the longest. Longer sequences come first, any number of them, sorted by counting chunks (in steps of a power of two where a
+// length exceeds 1023 chunks). Whole calls on sequences of up to three tokens, one head, K = V = 64: 300 sequences 18.5 us, 1000 45 us
+// (25.6 and 107 when every thread counted the longer ones).
 __device__ __forceinline__ long long warp_total(long long x) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
     return x;
+}
+// exclusive sum of x over the block's threads; `scratch` has a place for each warp
+__device__ __forceinline__ int block_scan(int x, int* scratch, int& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int sum = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += y;
+    }
+    __syncthreads();   // (the scratch of the call before)
+    if (lane == 31) scratch[warp] = sum;
+    __syncthreads();
+    int before = scratch[lane];   // every warp sums all of them up
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off) before += y;
+    }
+    all = __shfl_sync(0xffffffffu, before, 31);
+    const int mine = __shfl_sync(0xffffffffu, before, warp > 0 ? warp - 1 : 0);
+    return sum - x + (warp > 0 ? mine : 0);
+}
+// counter[b] += 1 for every lane that is `on` (all lanes take part), one addition for those of a warp with the same b; the lane's
+// place among all that have counted there
+__device__ __forceinline__ int count_up(int* counter, int b, bool on) {
+    const int lane = threadIdx.x & 31;
+    const unsigned same = __match_any_sync(0xffffffffu, on ? b : -1);
+    const int first = __ffs(same) - 1;
+    int from = 0;
+    if (on && lane == first) from = atomicAdd(counter + b, __popc(same));
+    return __shfl_sync(0xffffffffu, from, first) + __popc(same & ((1u << lane) - 1u));
 }
 __global__ void __launch_bounds__(kPlanThreads)
     plan_kernel(const int* cu, int nseq, int T, int room, int* words, int4* table1, int4* table2, DeviceError* err) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int warp_sum[32], warp_max[32];
     __shared__ long long warp_time[32];
+    __shared__ int place[kPlanThreads];   // of the next sequence of a length, the longest first
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     bool bad = t == 0 && (cu[0] != 0 || cu[nseq] > T);
     int longest = 0;
@@ -82,16 +117,17 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     auto chunks = [&](int s) { return (cu[s + 1] - cu[s] + kChunk - 1) / kChunk; };
     int first = 0, rest = 0;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    all = warp_total(all);
+    if (lane == 0) {
+        warp_max[warp] = longest;
+        warp_time[warp] = all;
+    }
+    place[t] = 0;
+    __syncthreads();
+    longest = __reduce_max_sync(0xffffffffu, warp_max[lane]);
+    all = warp_total(warp_time[lane]);
     if (room > 0) {
-        longest = __reduce_max_sync(0xffffffffu, longest);
-        all = warp_total(all);
-        if (lane == 0) {
-            warp_max[warp] = longest;
-            warp_time[warp] = all;
-        }
-        __syncthreads();
-        longest = __reduce_max_sync(0xffffffffu, warp_max[lane]);
-        all = warp_total(warp_time[lane]);
         const long long uncut = nseq > room ? max((long long)longest, all / room + longest / 2) : longest;
         // lengths worth trying: from what an even cut of all chunks would give on, in steps of a sixteenth, three times as far
         // a round
@@ -121,46 +157,29 @@ __global__ void __launch_bounds__(kPlanThreads)
             }
         }
     }
+    int step = 0, sum;
+    while (longest >> step >= kPlanThreads) ++step;
+    auto bucket = [&](int s) { return kPlanThreads - 1 - (chunks(s) >> step); };
+    for (int s0 = 0; s0 < nseq; s0 += kPlanThreads) count_up(place, s0 + t < nseq ? bucket(s0 + t) : 0, s0 + t < nseq);
+    __syncthreads();
+    const int ahead = block_scan(place[t], warp_sum, sum);
+    place[t] = ahead;
     __syncthreads();
     int before = 0;   // pieces behind the first ones of all sequences before this round's
     for (int s0 = 0; s0 < nseq; s0 += kPlanThreads) {
         const int s = s0 + t;
-        const int pieces = s < nseq && rest > 0 ? 1 + more_pieces(chunks(s), first, rest) : 1;
-        int sum = pieces - 1;   // inclusive sums over the warp, then over the warps
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, sum, off);
-            if (lane >= off) sum += y;
+        const bool on = s < nseq;
+        const int pieces = on && rest > 0 ? 1 + more_pieces(chunks(s), first, rest) : 1;
+        const int slot0 = before + block_scan(pieces - 1, warp_sum, sum);
+        before += sum;
+        const int at = count_up(place, on ? bucket(s) : 0, on);
+        if (!on) continue;
+        table1[at] = make_int4(s, 0, pieces, slot0);
+        for (int q = 1; q < pieces; ++q) {
+            table2[slot0 + q - 1] = make_int4(s, q, pieces, slot0);
+            // (the last piece's place among the sums stays empty: sequence -1)
+            table1[nseq + slot0 + q - 1] = make_int4(q < pieces - 1 ? s : -1, q, pieces, slot0);
         }
-        if (lane == 31) warp_sum[warp] = sum;
-        __syncthreads();
-        if (t < 32) {
-            int x = warp_sum[t];
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, off);
-                if (t >= off) x += y;
-            }
-            warp_sum[t] = x;
-        }
-        __syncthreads();
-        const int slot0 = before + sum - (pieces - 1) + (warp ? warp_sum[warp - 1] : 0);
-        if (s < nseq) {
-            int place = s;   // in the order of falling length
-            if (nseq <= kPlanThreads) {
-                const int n = chunks(s);
-                place = 0;
-                for (int j = 0; j < nseq; ++j) place += chunks(j) > n || (chunks(j) == n && j < s);
-            }
-            table1[place] = make_int4(s, 0, pieces, slot0);
-            for (int q = 1; q < pieces; ++q) {
-                table2[slot0 + q - 1] = make_int4(s, q, pieces, slot0);
-                // (the last piece's place among the sums stays empty: sequence -1)
-                table1[nseq + slot0 + q - 1] = make_int4(q < pieces - 1 ? s : -1, q, pieces, slot0);
-            }
-        }
-        before += warp_sum[31];
-        __syncthreads();
     }
     if (t == 0) {
         words[kCount1] = nseq + before;
