@@ -73,7 +73,22 @@ constexpr uint32_t kTmS = 0, kTmU = 128, kTmHi = 256, kTmLo = 320, kTmO = 384;
 // mbarriers, 8 bytes each from kBar on. A wait names a phase by its parity, so no barrier may get two phases ahead of any warp that
 // waits on it, however long that warp is held up: between two phases of each lies something that every one of its
 // waiters does only once it has seen the first.
-enum { B_FULL0 = 0, B_FULL1, B_EMPTY0, B_EMPTY1, B_AFULL0, B_AFULL1, B_AFREE0, B_AFREE1, B_OUT0, B_OUT1, B_S, B_P, B_OI, B_OSCALED, B_O, B_OFREE, B_VD, B_U, B_X, B_ZERO, B_TAKEN, B_DRAIN0, B_DRAIN1, B_N };
+enum {
+    B_FULL0 = 0, B_FULL1,    // a stage: B and C have come
+    B_EMPTY0, B_EMPTY1,      //          B and C are done with
+    B_AFULL0, B_AFULL1,      //          A has come
+    B_AFREE0, B_AFREE1,      //          the outputs have left A's tile
+    B_OUT0, B_OUT1,          //          bf16 outputs lie in A's tile
+    B_S, B_P,                // S, P are in tensor memory
+    B_OI, B_OSCALED, B_O,    // O = A X; with the rows' weights; with P C
+    B_OFREE,                 // O has been read
+    B_VD, B_U,               // Cw, U are in tensor memory
+    B_X,                     // X is in shared memory
+    B_ZERO,                  // the rows behind the sequence's end are zeros
+    B_TAKEN,                 // second pass: C is finite
+    B_DRAIN0, B_DRAIN1,      // shutting down: what the two MMA warps issued has retired
+    B_N
+};
 constexpr unsigned kTag = 0x60;   // + the barrier's number
 static_assert(kBar + 8 * B_N + 12 <= kOdd, "the barriers, the flag and tensor memory's address");
 
@@ -725,9 +740,23 @@ __device__ __forceinline__ void state_warps(const Work& w, int warp, int lane) {
     }
 }
 
+// how many arrivals end a phase of barrier i
+__device__ __forceinline__ int arrivals(int i, bool sums) {
+    switch (i) {
+        case B_EMPTY0: case B_EMPTY1:                                  // commits: of O += P C and U, of sums alone U
+            return sums ? 1 : 2;
+        case B_AFREE0: case B_AFREE1:                                  // fp32: a lane of each output warp; bf16: store_warp, at once
+            return kOutThreads / 32;
+        case B_P: case B_OUT0: case B_OUT1: case B_OFREE:              // every output thread
+            return kOutThreads;
+        case B_OSCALED: case B_VD: case B_X: case B_ZERO: case B_TAKEN:   // every state thread
+            return kStateThreads;
+        default:                                                       // B_FULL, B_AFULL: the loading lane, beside its bytes;
+            return 1;                                                  // B_S, B_OI, B_O, B_U, B_DRAIN: a commit
+    }
+}
 __device__ __forceinline__ void init_barriers(const Work& w) {
-    for (int i = 0; i < B_N; ++i)
-        mbar_init(w.bar(i), i == B_AFREE0 || i == B_AFREE1 ? kOutThreads / 32 : i == B_EMPTY0 || i == B_EMPTY1 ? (w.sums ? 1 : 2) : i == B_P || i == B_OUT0 || i == B_OUT1 || i == B_OFREE ? kOutThreads : i == B_OSCALED || i == B_VD || i == B_X || i == B_ZERO || i == B_TAKEN ? kStateThreads : 1);
+    for (int i = 0; i < B_N; ++i) mbar_init(w.bar(i), arrivals(i, w.sums));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async();
 }
