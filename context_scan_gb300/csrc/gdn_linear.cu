@@ -313,8 +313,8 @@ gdn_status run(Params& c, const gdn_problem& p, int Hqk, bool backward, void* wo
     c.words = words;
     // Roles of different sizes or outputs run different code, and the two SMs of a pair share what holds it: with a head's roles
     // side by side their CTAs keep displacing each other's. So blocks of one role lie side by side there (gradients of 1 x
-    // 32768 tokens of 64 heads, K = 64, V = 128: 918 us instead of 1324; with a quarter of the heads for q and k, K = V = 128: 1504
-    // instead of 1526). Else a head's roles do, which read the same tensors (K = V = 128: 1039 us, by role 1058).
+    // 32768 tokens of 64 heads, K = 64, V = 128: 930 us instead of 1360; with a quarter of the heads for q and k, K = V = 128: 1507
+    // instead of 1526). Else a head's roles do, which read the same tensors (K = V = 128: 1036 us, by role 1059).
     c.by_role = tc && c.nroles > 1 && (p.K != p.V || Hqk != p.H);
     c.phase = 1;
     c.blocks = (int)blocks1;

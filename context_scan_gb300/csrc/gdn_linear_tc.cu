@@ -20,14 +20,15 @@
 // tensor memory, outputs leave through A's tile. Every wait on an mbarrier is bounded: on expiry it sets a flag that ends the
 // other waits too; the CTA then lets what it issued retire, records GDN_ERR_TIMEOUT, frees tensor memory and returns.
 //
-// Measured (dA = dC = 128): 2.9 us a chunk, some 4900 cycles. Some 3500 of them are shared memory's traffic (450 KB a chunk: tiles
-// written once and read by two or three products, X, Cw and the outputs), 3600 the MMAs (two operands of 128 rows from
-// shared memory take 90 cycles instead of 64), 1800 the dependent way S -> P, 1100 O += P C. Sums alone take 1.4 to 1.6
-// us a chunk, setting a CTA up, its first loads and its end 5 us. 2 x 32768 tokens of 32 heads: 462 us, 4.67 TB/s of
-// 6.78; their gradients at 2 x 8192: 284 us.
+// Measured (dA = dC = 128), from pieces of 64 and of 128 chunks, calls back to back: with half of the SMs at work a chunk takes 1.91 us
+// (3800 cycles at 1.99 GHz), with all of them 2.94 us in the gradients (5350 cycles at the 1.82 GHz that the power limit leaves) and 3.1 us
+// in the forward, which then moves 6.4 TB/s. By arithmetic: shared memory's traffic 450 KB, 3500 cycles (tiles written
+// once and read by two or three products, X, Cw and the outputs), the MMAs 40 of 64 cycles, one chain of S, P, O += P C from one
+// chunk to the next. Sums alone take 1.7 us a chunk at most (103 of them in 172 us). 2 x 32768 tokens of 32 heads: 462 us, 4.67
+// TB/s of 6.80; their gradients at 2 x 8192: 283 us.
 //
 // Code. The two SMs of a pair share what holds their instructions, and 20 warps are at as many places of the code: what the
-// compiler unrolls counts. With every wait's loop unrolled (118 KB instead of 79) the first case took 472 us.
+// compiler unrolls counts. With every wait's loop unrolled (118 KB instead of 79, without the copies for a second pass) the first case took 472 us.
 //
 // A sequence's last chunk may hold fewer than 128 tokens: the rows of B and C behind it (the next sequence's) are
 // overwritten by zeros in shared memory, so that nothing of another sequence enters a sum, not as 0 times NaN either. Nor
