@@ -16,8 +16,8 @@
 // memory (two stages of A, B, C: 192 KB, and 32 KB of X), which would not hold scaled copies as well.
 // P and X are rounded to bf16 because the products' other operand is bf16 (fp32 ones would take two or three parts each): outputs
 // off by 2.3e-3 of their RMS instead of a bf16 result's 1.7e-3. Cw has two parts because a third one takes 24 instead of 16
-// MMAs a chunk and room that only slices of 32 tokens leave: 25 % of the forward's time, 19 % of the gradients', for states good to
-// fp32's 2e-7 of their RMS instead of 2e-6.
+// MMAs a chunk and room that only slices of 32 tokens leave: 25 % of the forward's time, 19 % of the gradients', for states off by
+// 4 to 6e-7 of their RMS instead of 2.4e-6.
 //
 // Warps: 0-7 P and the outputs; 8-15 the state: Cw (each half of them 64 tokens), X (each half 64 rows) and the scaling of O;
 // 16 loads (TMA, 128-byte swizzle), 17 issues S and O += P C, 19 O = A X and U, 18 stores bf16 outputs (TMA). P takes S's place in

@@ -537,7 +537,7 @@ GDN_API gdn_status gdn_norm_bwd(long long rows, int N, int x_dtype, int y_dtype,
  * bf16 inputs and outputs run on the tensor cores: products of bf16 values summed in fp32, where the weighted
  * attention inside a chunk of 128 tokens and the state that a chunk's outputs read are rounded to bf16 once (outputs and
  * gradients are off by 2.3e-3 of their RMS, a bf16 result's own rounding being 1.7e-3), and the state itself is fp32, its
- * updates good to 2^-17 of each term (h_final and dh0 are off by some 2e-6, by 2e-7 from fp32 tensors). Other types run in
+ * updates good to 2^-17 of each term (h_final and dh0 are off by 2.4e-6, from fp32 tensors by 2e-7). Other types run in
  * fp32 throughout.
  * A NaN or an infinity in one token reaches the results that see it by the formulas (where it may turn from an infinity
  * into a NaN) and no others, whatever the types: a padded batch may hold anything behind its sequences' last tokens. */
