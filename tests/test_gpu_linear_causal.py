@@ -99,3 +99,31 @@ def test_garbage_behind_each_sequence_of_a_batch(dtype):
     for s, length in enumerate((200, 70, 130)):
         assert torch.equal(o[s, :length], clean[s, :length])
         assert not torch.isfinite(o[s, length:]).any()
+
+
+def same_bits(a, b):
+    return torch.equal(torch.nan_to_num(a, nan=7.0), torch.nan_to_num(b, nan=7.0)) and torch.equal(torch.isnan(a), torch.isnan(b))
+
+
+def test_clean_and_bad_calls_in_turn():
+    # many blocks at work, pieces and whole sequences, one call behind the other without a wait on the host
+    lens = [3000, 0, 85, 640, 2500, 1, 1500]
+    clean = make(lens, 16, 8, 128, 128, seed=14)
+    bad = {**clean, "v": clean["v"].clone(), "do": clean["do"].clone()}
+    for row in (5, 2999, 3080, 4000, 6222):
+        bad["v"][0, row, :, row % 128] = NAN
+        bad["do"][0, row + 1, row % 16, 3] = INF
+    wants = [(run_fwd(d), run_bwd(d)) for d in (clean, bad)]
+    wf = gdn.alloc_linear_workspace(clean["k"], clean["v"], clean["cu"])
+    wb = gdn.alloc_linear_workspace(clean["k"], clean["v"], clean["cu"], backward=True)
+    o, ht = torch.empty_like(wants[0][0][0]), torch.empty_like(wants[0][0][1])
+    g = [torch.empty_like(x) for x in wants[0][1][:4]]
+    for i in range(60):
+        d, (f, b) = (clean, bad)[i % 2], wants[i % 2]
+        gdn.gdn_linear_fwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], o, ht, wf, cu_seqlens=d["cu"])
+        gdn.gdn_linear_bwd(d["q"], d["k"], d["v"], d["decay"], d["h0"], d["do"], d["dht"], *g, wb, cu_seqlens=d["cu"])
+        assert same_bits(o, f[0]) and same_bits(ht, f[1]) and all(same_bits(x, y) for x, y in zip(g, b)), i
+    for _ in range(100):
+        gdn.gdn_linear_bwd(bad["q"], bad["k"], bad["v"], bad["decay"], bad["h0"], bad["do"], bad["dht"], *g, wb, cu_seqlens=bad["cu"])
+    assert all(same_bits(x, y) for x, y in zip(g, wants[1][1]))
+    assert gdn.gdn_check_device_error(wf)[0] == 0 and gdn.gdn_check_device_error(wb)[0] == 0
